@@ -379,6 +379,198 @@ tcg_status tcg_gemm_grouped(int num_problems, const tcg_problem* problems,
 tcg_status tcg_grouped_plan(int num_problems, const tcg_problem* problems, tcg_dtype ab_dtype, int out[10]);
 
 /*
+ * ---------------------------------------------------------------------------
+ * 8-bit operands with one fp32 scale per 128 elements, and the balance loss of
+ * a mixture-of-experts router: what a layer whose weights and activations are
+ * kept in 8 bits runs around its products.  Rules shared with the entry points
+ * above: device memory of the caller, row-major matrices with a leading
+ * dimension in elements, asynchronous on `stream`, host-detectable errors
+ * before anything is queued, TCG_ERR_ARCH on any other GPU.
+ *
+ * Codes and scales.  A block of 128 elements (or 128 x 128) with largest
+ * magnitude amax is kept as
+ *
+ *     s = max(amax, 2^-96) * fl(1 / top),  top = 448 (E4M3) or 57344 (E5M2)
+ *     q = round to nearest even of clamp(x * fl(1 / s), -top, top)
+ *
+ * in fp32 arithmetic; with pow2 != 0, s is rounded up to a power of two.  A
+ * block of zeros has the scale of amax = 2^-96 and codes 0.  A NaN gives a NaN
+ * code and takes no part in amax; a block with an infinity has an infinite
+ * scale, so all of it stands for NaN.  Elements past the matrix's edge do not
+ * exist; the blocks at the edge are shorter.
+ *
+ * x_dtype: TCG_BF16, TCG_F16 or TCG_F32.  q_dtype: TCG_E4M3 or TCG_E5M2.  Any
+ * leading dimensions and alignments (of the element) are taken; whole vectors
+ * are used where x and q start on 16 bytes and their pitches are multiples of
+ * 16 bytes.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * tcg_quantize_rows128 -- one scale per 128 consecutive elements of a row (the
+ * activations of a forward product or of an input gradient).
+ *   x: row-major with ldx >= cols.  Output row r is row row_index[r] of x (r
+ *     itself when row_index is NULL); an index outside [0, source_rows) gives a
+ *     row of zeros.  x has source_rows rows (rows without row_index).
+ *   q: rows x cols, ldq >= cols.
+ *   scales: scale of row r, block kb at scales[kb * ld_scales + r],
+ *     ld_scales >= rows.
+ */
+tcg_status tcg_quantize_rows128(int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx,
+                                const int* row_index, int source_rows,
+                                void* q, int ldq, tcg_dtype q_dtype, float* scales, int ld_scales,
+                                int pow2, void* stream);
+
+/*
+ * tcg_quantize_cols128 -- one scale per 128 rows of a column, written
+ * transposed: the operands of a weight gradient, whose sum runs over the rows.
+ * With num_groups > 0 and offsets (device, num_groups + 1 non-decreasing row
+ * numbers), group g is rows [offsets[g], offsets[g + 1]); the groups' rows are
+ * placed one after the other, each group starting on a multiple of 128, and
+ * every place that holds no row (up to padded_rows) holds code 0.
+ * padded_rows: a multiple of 128, at least the sum of the groups' lengths each
+ * rounded up to 128 (rows / 128 * 128 + 128 * num_groups always suffices; rows
+ * past it are dropped).  offsets NULL: one group of all rows.
+ *   q: cols x padded_rows, ldq >= padded_rows.
+ *   scales: scale of column c, block b at scales[b * ld_scales + c],
+ *     ld_scales >= cols.
+ *   x, row_index, source_rows: as in tcg_quantize_rows128.
+ * Offsets outside [0, rows] are clamped.  num_groups <= 1024, padded_rows <=
+ * 65535 * 128 (else TCG_ERR_UNSUPPORTED).
+ */
+tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx,
+                                const int* row_index, int source_rows,
+                                int num_groups, const int* offsets, int padded_rows,
+                                void* q, int ldq, tcg_dtype q_dtype, float* scales, int ld_scales,
+                                int pow2, void* stream);
+
+/*
+ * tcg_quantize_tiles128 -- one scale per 128 x 128 tile (weights): `batch`
+ * matrices of rows x cols, matrix b being rows [b * rows, (b + 1) * rows) of
+ * x.  q (rows x cols each, stacked the same way, ldq >= cols) and qt (the
+ * transposed codes, cols x rows each, ldqt >= rows): either may be NULL.
+ * scales: batch x ceil(rows / 128) x ceil(cols / 128), contiguous.
+ */
+tcg_status tcg_quantize_tiles128(int batch, int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx,
+                                 void* q, int ldq, void* qt, int ldqt, tcg_dtype q_dtype, float* scales,
+                                 int pow2, void* stream);
+
+/*
+ * One operand of a block-scaled product: 8-bit codes, row-major with K
+ * contiguous (data 16-byte aligned, ld a multiple of 16, else
+ * TCG_ERR_UNSUPPORTED), and fp32 scales in device memory.  The scale of row r,
+ * K block kb (128 elements), group g is
+ *     scales[(r / scale_rows) * row_stride + kb * k_stride + g * group_stride]
+ * with scale_rows = 1 (a scale per row) or 128 (per 128 rows), strides >= 0:
+ * both orders of a scale matrix, and the transposed weights of an input
+ * gradient, are addressed in place.
+ */
+typedef struct {
+    const void* data;
+    int ld;
+    int scale_rows;
+    const float* scales;
+    long long row_stride;
+    long long k_stride;
+    long long group_stride;
+} tcg_block_operand;
+
+/*
+ * tcg_block128_workspace_size -- device workspace of the three products
+ * below: a 256-byte status header plus, where few tiles share K among the SMs,
+ * counters and fp32 partial sums.  num_groups = 0: tcg_gemm_block128;
+ * otherwise tcg_gemm_block128_grouped with M rows in all
+ * (tcg_gemm_block128_grouped_k needs 256 bytes).  Zero-fill it once
+ * (tcg_workspace_init); the calls leave it so, and the workspace of several
+ * calls on one stream may be one.  0 for invalid sizes.
+ */
+size_t tcg_block128_workspace_size(int num_groups, int M, int N, int K);
+
+/*
+ * tcg_gemm_block128 -- D = act( A @ B^T + beta * C + bias ), A: M x K with
+ * scale_rows = 1, B: N x K with scale_rows = 1 or 128, both ab_dtype
+ * (TCG_E4M3 or TCG_E5M2); C, D, bias and act as in tcg_gemm.  Every 128 K the
+ * sum of products is multiplied by both scales and added in fp32; the result
+ * is rounded once.  A's scale_rows = 128: TCG_ERR_UNSUPPORTED.
+ *   Forward: activations by rows, weights by tiles.  Input gradient: the
+ *   output gradient by rows, the weights' transposed codes with their scale
+ *   strides exchanged.  Weight gradient: both operands from
+ *   tcg_quantize_cols128 (scale_rows = 1 both), beta = 1 to accumulate.
+ * D must not overlap A, B or bias; D == C is allowed when ldc == ldd and
+ * c_dtype == d_dtype.  K == 0 gives act(beta * C + bias).  Results do not
+ * depend on the order in which the SMs finish.  Wait timeouts: tcg_device_status.
+ */
+tcg_status tcg_gemm_block128(int M, int N, int K, tcg_dtype ab_dtype, tcg_block_operand A, tcg_block_operand B,
+                             float beta, const void* C, int ldc, tcg_dtype c_dtype,
+                             void* D, int ldd, tcg_dtype d_dtype, tcg_epilogue epi,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tcg_gemm_block128_grouped -- rows [offsets[g], offsets[g + 1]) of D are
+ * those rows of A times B_g^T: the experts of a layer on tokens in expert
+ * order.  A: rows x K (scale_rows = 1); B: the groups' N x K weights stacked
+ * (num_groups * N rows); D: rows x N.  offsets: device, num_groups + 1
+ * non-decreasing row numbers from 0 to at most rows (tcg_moe_balance writes
+ * them); they are read by the kernel, so the host never waits for the
+ * routing.  Rows of D outside every group are not written; offsets outside
+ * [0, rows] are clamped.  num_groups <= 1024 (else TCG_ERR_UNSUPPORTED).
+ */
+tcg_status tcg_gemm_block128_grouped(int num_groups, const int* offsets, int rows, int N, int K, tcg_dtype ab_dtype,
+                                     tcg_block_operand A, tcg_block_operand B,
+                                     void* D, int ldd, tcg_dtype d_dtype,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tcg_gemm_block128_grouped_k -- the weight gradients of every group:
+ * D_g = A[:, places of g] @ B[:, places of g]^T + beta * C_g, with A (M x
+ * padded_rows) and B (N x padded_rows) as tcg_quantize_cols128 writes them for
+ * the same offsets (scale_rows = 1 both).  D and C: num_groups matrices of M x
+ * N, stacked.  A group without rows gives beta * C_g.
+ */
+tcg_status tcg_gemm_block128_grouped_k(int num_groups, const int* offsets, int M, int N, int padded_rows,
+                                       tcg_dtype ab_dtype, tcg_block_operand A, tcg_block_operand B,
+                                       float beta, const void* C, int ldc, tcg_dtype c_dtype,
+                                       void* D, int ldd, tcg_dtype d_dtype,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tcg_moe_balance -- the balance loss of a router and its assignments per
+ * expert.  With p the softmax of each token's logits (tokens x experts, dtype
+ * TCG_BF16, TCG_F16 or TCG_F32), n the tokens with mask != 0 (all when mask is
+ * NULL; mask: one byte per token) and c_e how often those tokens' topk (tokens
+ * x k ints, ld_topk >= k) names expert e:
+ *
+ *     loss = coef * sum_e f_e P_e,  f_e = experts * c_e / (k n),  P_e = sum_t p_te / n
+ *
+ * (0 when n = 0).  Entries of topk outside [0, experts) are assignments that
+ * were dropped: they count for nobody.  A token whose logits are all -inf has
+ * p = 0.  Writes counts (experts), offsets (experts + 1: where each expert's
+ * rows start when the counted assignments are put in expert order; may be
+ * NULL), num_valid (n) and loss (fp32), all device memory.  The loss is the
+ * same every time (fixed order of summation).  experts <= 1024 (else
+ * TCG_ERR_UNSUPPORTED).  workspace: tcg_moe_balance_workspace_size bytes,
+ * zero-filled once; calls that share it must be ordered.
+ */
+size_t tcg_moe_balance_workspace_size(void);
+tcg_status tcg_moe_balance(int tokens, int experts, int k, tcg_dtype dtype, const void* logits, int ld,
+                           const int* topk, int ld_topk, const uint8_t* mask, float coef,
+                           int* counts, int* offsets, int* num_valid, float* loss,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tcg_moe_balance_backward -- dlogits_te = g * coef / n * p_te * (f_e - sum_j
+ * f_j p_tj) for g = *grad_loss (device), with counts and num_valid from the
+ * forward call; 0 for masked tokens.  The assignments are constants.  Every
+ * row of dlogits (tokens x experts, ldd >= experts, d_dtype TCG_BF16, TCG_F16
+ * or TCG_F32) is written; it may be the logits' own memory when the types and
+ * leading dimensions agree.
+ */
+tcg_status tcg_moe_balance_backward(int tokens, int experts, int k, tcg_dtype dtype, const void* logits, int ld,
+                                    const uint8_t* mask, float coef, const int* counts, const int* num_valid,
+                                    const float* grad_loss, void* dlogits, int ldd, tcg_dtype d_dtype,
+                                    void* stream);
+
+/*
  * tcg_debug_tma_swizzle128 -- TEST-ONLY: one TMA load of a rows x 128-byte
  * tile (row-major, 128-byte rows, device memory at src) into 1024-byte-aligned
  * shared memory with 128-byte swizzling, copied back unchanged to dst (rows x

@@ -36,7 +36,10 @@ STATUS = {0: "TCG_OK", 1: "TCG_ERR_INVALID_ARG", 2: "TCG_ERR_UNSUPPORTED", 3: "T
 EXPORTED = ["tcg_can_implement", "tcg_workspace_size", "tcg_workspace_size_for", "tcg_workspace_init", "tcg_gemm",
             "tcg_device_status", "tcg_last_error", "tcg_plan", "tcg_debug_set", "tcg_gemm_noalloc",
             "tcg_debug_schedule", "tcg_grouped_workspace_size", "tcg_gemm_grouped", "tcg_grouped_plan",
-            "tcg_debug_tma_swizzle128", "tcg_arch_status"]
+            "tcg_debug_tma_swizzle128", "tcg_arch_status", "tcg_quantize_rows128", "tcg_quantize_cols128",
+            "tcg_quantize_tiles128", "tcg_block128_workspace_size", "tcg_gemm_block128", "tcg_gemm_block128_grouped",
+            "tcg_gemm_block128_grouped_k", "tcg_moe_balance_workspace_size", "tcg_moe_balance",
+            "tcg_moe_balance_backward"]
 
 
 class TcgError(RuntimeError):
@@ -61,6 +64,13 @@ class Problem(ctypes.Structure):
                 ("A", ctypes.c_void_p), ("lda", ctypes.c_int), ("B", ctypes.c_void_p), ("ldb", ctypes.c_int),
                 ("C", ctypes.c_void_p), ("ldc", ctypes.c_int), ("D", ctypes.c_void_p), ("ldd", ctypes.c_int),
                 ("bias", ctypes.c_void_p)]
+
+
+class BlockOperand(ctypes.Structure):
+    """tcg_block_operand: 8-bit codes with one fp32 scale per 128 K (see block_operand)."""
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int), ("scale_rows", ctypes.c_int),
+                ("scales", ctypes.c_void_p), ("row_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+                ("group_stride", ctypes.c_longlong)]
 
 
 _lock = threading.Lock()
@@ -118,6 +128,29 @@ def lib() -> ctypes.CDLL:
         L.tcg_gemm_grouped.restype = i32
         L.tcg_grouped_plan.argtypes = [i32, ctypes.POINTER(Problem), i32, ctypes.POINTER(ctypes.c_int)]
         L.tcg_grouped_plan.restype = i32
+        L.tcg_quantize_rows128.argtypes = [i32, i32, i32, P, i32, P, i32, P, i32, i32, P, i32, i32, P]
+        L.tcg_quantize_rows128.restype = i32
+        L.tcg_quantize_cols128.argtypes = [i32, i32, i32, P, i32, P, i32, i32, P, i32, P, i32, i32, P, i32, i32, P]
+        L.tcg_quantize_cols128.restype = i32
+        L.tcg_quantize_tiles128.argtypes = [i32, i32, i32, i32, P, i32, P, i32, P, i32, i32, P, i32, P]
+        L.tcg_quantize_tiles128.restype = i32
+        L.tcg_block128_workspace_size.argtypes = [i32, i32, i32, i32]
+        L.tcg_block128_workspace_size.restype = sz
+        L.tcg_gemm_block128.argtypes = [i32, i32, i32, i32, BlockOperand, BlockOperand, f32, P, i32, i32, P, i32, i32,
+                                        Epilogue, P, sz, P]
+        L.tcg_gemm_block128.restype = i32
+        L.tcg_gemm_block128_grouped.argtypes = [i32, P, i32, i32, i32, i32, BlockOperand, BlockOperand, P, i32, i32,
+                                                P, sz, P]
+        L.tcg_gemm_block128_grouped.restype = i32
+        L.tcg_gemm_block128_grouped_k.argtypes = [i32, P, i32, i32, i32, i32, BlockOperand, BlockOperand, f32, P, i32,
+                                                  i32, P, i32, i32, P, sz, P]
+        L.tcg_gemm_block128_grouped_k.restype = i32
+        L.tcg_moe_balance_workspace_size.argtypes = []
+        L.tcg_moe_balance_workspace_size.restype = sz
+        L.tcg_moe_balance.argtypes = [i32, i32, i32, i32, P, i32, P, i32, P, f32, P, P, P, P, P, sz, P]
+        L.tcg_moe_balance.restype = i32
+        L.tcg_moe_balance_backward.argtypes = [i32, i32, i32, i32, P, i32, P, f32, P, P, P, P, i32, i32, P]
+        L.tcg_moe_balance_backward.restype = i32
         L.tcg_debug_tma_swizzle128.argtypes = [P, i32, P, P, P]
         L.tcg_debug_tma_swizzle128.restype = i32
         _lib = L
@@ -277,6 +310,109 @@ def grouped_plan(problems, ab_dtype="bf16") -> dict:
         raise TcgError(st, "tcg_grouped_plan", last_error())
     keys = ["BM", "BN", "BK", "stages", "splits", "grid", "cluster", "units", "group_m", "smem"]
     return dict(zip(keys, list(out)))
+
+
+# ------------------------------------- 8-bit operands with one scale per 128
+
+def quantize_rows128(rows, cols, x, ldx, x_dtype, q, ldq, q_dtype, scales, ld_scales, *, row_index=None,
+                     source_rows=0, pow2=False, stream=None) -> None:
+    """Queue the codes and scales of 1 x 128 blocks of (gathered) rows (tcg_quantize_rows128)."""
+    st = lib().tcg_quantize_rows128(rows, cols, _enum(x_dtype, DTYPES), _addr(x), ldx, _addr(row_index), source_rows,
+                                    _addr(q), ldq, _enum(q_dtype, DTYPES), _addr(scales), ld_scales, int(pow2),
+                                    _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_quantize_rows128", last_error())
+
+
+def quantize_cols128(rows, cols, x, ldx, x_dtype, q, ldq, q_dtype, scales, ld_scales, *, padded_rows, num_groups=0,
+                     offsets=None, row_index=None, source_rows=0, pow2=False, stream=None) -> None:
+    """Queue the transposed codes and scales of 128 x 1 blocks, each group's rows starting on a
+    multiple of 128 (tcg_quantize_cols128)."""
+    st = lib().tcg_quantize_cols128(rows, cols, _enum(x_dtype, DTYPES), _addr(x), ldx, _addr(row_index), source_rows,
+                                    num_groups, _addr(offsets), padded_rows, _addr(q), ldq, _enum(q_dtype, DTYPES),
+                                    _addr(scales), ld_scales, int(pow2), _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_quantize_cols128", last_error())
+
+
+def quantize_tiles128(batch, rows, cols, x, ldx, x_dtype, q, ldq, qt, ldqt, q_dtype, scales, *, pow2=False,
+                      stream=None) -> None:
+    """Queue the codes, transposed codes (either may be None) and scales of 128 x 128 tiles
+    (tcg_quantize_tiles128)."""
+    st = lib().tcg_quantize_tiles128(batch, rows, cols, _enum(x_dtype, DTYPES), _addr(x), ldx, _addr(q), ldq,
+                                     _addr(qt), ldqt, _enum(q_dtype, DTYPES), _addr(scales), int(pow2),
+                                     _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_quantize_tiles128", last_error())
+
+
+def block_operand(data, ld, scales, scale_rows, row_stride, k_stride, group_stride=0) -> BlockOperand:
+    """An operand of the block-scaled products: the scale of row r, K block kb, group g is
+    scales[(r // scale_rows) * row_stride + kb * k_stride + g * group_stride].  It holds addresses:
+    keep the tensors alive."""
+    return BlockOperand(_addr(data), ld, scale_rows, _addr(scales), row_stride, k_stride, group_stride)
+
+
+def block128_workspace_size(num_groups, M, N, K) -> int:
+    """Workspace bytes of gemm_block128 (num_groups 0) or gemm_block128_grouped (M rows in all)."""
+    return int(lib().tcg_block128_workspace_size(num_groups, M, N, K))
+
+
+def gemm_block128(M, N, K, A, B, beta, C, ldc, c_dtype, D, ldd, d_dtype, *, ab_dtype="e4m3", bias=None,
+                  bias_dtype="bf16", act="none", workspace=None, workspace_bytes=0, stream=None) -> None:
+    """Queue D = act(A @ B^T + beta*C + bias) on block-scaled operands (tcg_gemm_block128)."""
+    st = lib().tcg_gemm_block128(M, N, K, _enum(ab_dtype, DTYPES), A, B, beta, _addr(C), ldc, _enum(c_dtype, DTYPES),
+                                 _addr(D), ldd, _enum(d_dtype, DTYPES),
+                                 Epilogue(_addr(bias), _enum(bias_dtype, DTYPES), _enum(act, ACTS)),
+                                 _addr(workspace), workspace_bytes, _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_gemm_block128", last_error())
+
+
+def gemm_block128_grouped(num_groups, offsets, rows, N, K, A, B, D, ldd, d_dtype, *, ab_dtype="e4m3",
+                          workspace=None, workspace_bytes=0, stream=None) -> None:
+    """Queue the rows of every group times the group's weights (tcg_gemm_block128_grouped)."""
+    st = lib().tcg_gemm_block128_grouped(num_groups, _addr(offsets), rows, N, K, _enum(ab_dtype, DTYPES), A, B,
+                                         _addr(D), ldd, _enum(d_dtype, DTYPES), _addr(workspace), workspace_bytes,
+                                         _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_gemm_block128_grouped", last_error())
+
+
+def gemm_block128_grouped_k(num_groups, offsets, M, N, padded_rows, A, B, beta, C, ldc, c_dtype, D, ldd, d_dtype, *,
+                            ab_dtype="e4m3", workspace=None, workspace_bytes=0, stream=None) -> None:
+    """Queue the weight gradients of every group (tcg_gemm_block128_grouped_k)."""
+    st = lib().tcg_gemm_block128_grouped_k(num_groups, _addr(offsets), M, N, padded_rows, _enum(ab_dtype, DTYPES),
+                                           A, B, beta, _addr(C), ldc, _enum(c_dtype, DTYPES), _addr(D), ldd,
+                                           _enum(d_dtype, DTYPES), _addr(workspace), workspace_bytes, _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_gemm_block128_grouped_k", last_error())
+
+
+# ------------------------------------------------------- a router's balance
+
+def moe_balance_workspace_size() -> int:
+    return int(lib().tcg_moe_balance_workspace_size())
+
+
+def moe_balance(tokens, experts, k, logits, ld, dtype, topk, ld_topk, mask, coef, counts, offsets, num_valid, loss, *,
+                workspace=None, workspace_bytes=0, stream=None) -> None:
+    """Queue the balance loss, the assignments per expert and their offsets (tcg_moe_balance)."""
+    st = lib().tcg_moe_balance(tokens, experts, k, _enum(dtype, DTYPES), _addr(logits), ld, _addr(topk), ld_topk,
+                               _addr(mask), coef, _addr(counts), _addr(offsets), _addr(num_valid), _addr(loss),
+                               _addr(workspace), workspace_bytes, _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_moe_balance", last_error())
+
+
+def moe_balance_backward(tokens, experts, k, logits, ld, dtype, mask, coef, counts, num_valid, grad_loss, dlogits,
+                         ldd, d_dtype, *, stream=None) -> None:
+    """Queue the gradient of the balance loss with respect to the logits (tcg_moe_balance_backward)."""
+    st = lib().tcg_moe_balance_backward(tokens, experts, k, _enum(dtype, DTYPES), _addr(logits), ld, _addr(mask),
+                                        coef, _addr(counts), _addr(num_valid), _addr(grad_loss), _addr(dlogits), ldd,
+                                        _enum(d_dtype, DTYPES), _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_moe_balance_backward", last_error())
 
 
 def debug_tma_swizzle128(src, rows, dst, status, stream=None) -> None:

@@ -28,7 +28,8 @@ def debug_requested() -> bool:
 def so_path(debug: bool | None = None) -> str:
     return DEBUG_SO_PATH if (debug_requested() if debug is None else debug) else SO_PATH
 GENCODE = "arch=compute_103a,code=sm_103a"
-UNITS = ("tcgemm_host", "launch_block_scaled", "launch_grouped", "launch_narrow", "launch_swapped", "debug_tma")
+UNITS = ("tcgemm_host", "launch_block_scaled", "launch_grouped", "launch_narrow", "launch_swapped", "block128",
+         "quantize128", "moe_balance", "debug_tma")
 
 
 def _nvcc() -> str:
@@ -40,6 +41,7 @@ def _nvcc() -> str:
 
 def sources() -> list:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
+                  glob.glob(os.path.join(CSRC, "*.h")) +
                   [os.path.join(ROOT, "include", "tcgemm.h")])
 
 

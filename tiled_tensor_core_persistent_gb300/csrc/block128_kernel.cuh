@@ -1,0 +1,835 @@
+// block128_kernel.cuh -- the 8-bit matrix product whose operands carry one
+// fp32 scale per 128 consecutive K (per row of A; per row or per 128 rows of
+// B), for sm_103a:
+//
+//   D[m, n] = act( sum_kb sA[m, kb] sB[n, kb] T_kb[m, n] + beta C[m, n] + bias[n] )
+//   T_kb[m, n] = sum over the 128 k of block kb of A[m, k] B[n, k]
+//
+// T_kb is what the tensor cores sum exactly as fp32 in TMEM; the scales are
+// arbitrary fp32 numbers, which the MMA's own block scaling (powers of two or
+// 8-bit scales per 16 or 32) cannot hold.  So every k-block is one fresh TMEM
+// accumulation of four K = 32 MMAs, and the promote warps fold it into fp32
+// registers: acc += (sA sB) * T_kb.
+//
+// What bounds it.  A pair tile of 256 x 256 x 128 keeps each SM's tensor core
+// busy for 128 * 256 * 128 / 8192 = 512 cycles.  In that time the SM's promote
+// warps read 128 x 256 words from TMEM (256 cycles at 16 bytes per lane and
+// clock) and issue 128 * 256 FMAs (256 cycles of the 128 lanes, in f32x2
+// pairs), so the fold hides behind the MMAs as long as its latency does: two
+// TMEM buffers, eight promote warps (two per TMEM quadrant, so that one
+// loads while the other multiplies).  A per-column scale (both operands
+// scaled per row, the weight gradient) adds one multiply per element.
+//
+// Roles (one CTA or a CTA pair, persistent): warp 0 TMA producer, warp 1 MMA
+// issuer and TMEM owner, the others promote and store.  All waits are
+// bounded; on expiry the status word gets TCG_ERR_TIMEOUT, the roles drain
+// their copies and MMAs, free the TMEM and return.
+#pragma once
+
+#include "gemm_kernel.cuh"
+
+namespace tcg {
+namespace b128 {
+
+constexpr int kBlock = 128;                 // K elements per scale = bytes per swizzle row
+constexpr int kAtoms = 2;                   // k-blocks per pipeline stage
+constexpr int kMaxGroups = 1024;
+
+enum Mode : int { kDense = 0, kGroupedRows = 1, kGroupedK = 2 };
+
+// How the scales of one operand are addressed: row r, k-block kb, group g at
+// ptr[(r >> shift) * rs + kb * ks + g * gs].
+struct ScaleRef {
+    const float* ptr;
+    long long rs, ks, gs;
+    int shift;   // 0: one scale per row, 7: one per 128 rows
+    int rows;    // rows of one group (row indices are clamped below it)
+};
+
+struct Params {
+    CUtensorMap tmA, tmB;
+    ScaleRef sa, sb;
+    int mode;
+    int M, N, num_kb;          // grouped rows: M = all rows; grouped K: num_kb = all k-blocks
+    int num_m, num_n;          // tile grid of one problem (grouped rows: num_m unused)
+    int num_groups;
+    const int* offsets;        // device, num_groups + 1 (grouped modes)
+    int stream;                // k-block iterations dealt evenly to the workers (dense, grouped rows)
+    int raster_m;              // tile rows walked before the next tile column
+    int stages;
+    uint32_t ab_fmt;
+    float beta;
+    const void* C;
+    long long ldc;
+    int c_f32, c_vec;
+    const void* bias;
+    int bias_f32;
+    int act;
+    void* D;
+    long long ldd;
+    int d_f32;
+    int d_vec;                 // bytes of one vector store of D: 32, 16, or 0 (staged, element-wise)
+    float* partials;           // [2 * worker + which][column][128]
+    int* counters;             // [worker]
+    int* status;
+    long long timeout_ns;
+    int fault_inject;
+};
+
+struct alignas(16) Ctl {
+    uint64_t full[16];
+    uint64_t empty[16];
+    uint64_t tmem_full[4];
+    uint64_t tmem_empty[4];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int last;
+};
+
+__device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, const Params& p, Ctl* ctl, int where,
+                                     bool honor_abort) {
+    const uint32_t a = ptx::smem_u32(bar);
+    const uint64_t t0 = ptx::globaltimer_ns();
+    uint32_t n = 0;
+    while (true) {
+        if (ptx::mbar_try_wait(a, parity)) return true;
+        if ((++n & 31u) == 0) {
+            if (honor_abort && *reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
+            if (static_cast<long long>(ptx::globaltimer_ns() - t0) > p.timeout_ns) {
+                *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
+                if (atomicCAS(p.status, 0, kStatusTimeout) == 0) {
+                    p.status[1] = where;
+                    p.status[2] = static_cast<int>(blockIdx.x);
+                }
+                return false;
+            }
+        }
+    }
+}
+
+static __device__ __forceinline__ bool spin_slow(uint64_t* bar, uint32_t parity, const Params& p, Ctl* ctl, int where,
+                                              bool honor_abort) {
+    return spin(bar, parity, p, ctl, where, honor_abort);
+}
+
+// The whole warp waits, then agrees on the outcome.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Params& p, Ctl* ctl, int where,
+                                          bool honor_abort = true) {
+    bool ok = ptx::mbar_try_wait(ptx::smem_u32(bar), parity);
+    if (!ok) ok = spin_slow(bar, parity, p, ctl, where, honor_abort);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// 32 lanes x N consecutive TMEM columns, N = 16 or 32, the wait folded in.
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// ------------------------------------------------------------------ schedule
+
+// One piece of work: the output tile's place, its k-blocks, and its share of
+// the tile.  Row and k-block numbers are those of the operands in memory.
+struct Piece {
+    int g, m0, m_end, n0;      // rows [m0, m_end) may be stored
+    int b_row;                 // row of B's map where the tile starts
+    int d_row;                 // added to a row number for D and C (grouped K: g * M)
+    int kb0, kb1;              // k-blocks of this piece
+    int nsplit, split, first;  // pieces of the tile, this one's place, the first piece's worker
+    int tile;
+};
+
+// Group tables in shared memory, built once per CTA: first tile (grouped
+// rows) or first k-block (grouped K) of each group, and its rows.
+struct Groups {
+    const int* start;   // num_groups + 1
+    const int* row0;    // num_groups
+    const int* len;     // num_groups
+};
+
+// offsets are clamped into [0, rows], so a table that is not one (a negative
+// length, an offset past the operand) reads and writes nothing out of range.
+template <int kTileM>
+__device__ __forceinline__ void build_groups(const Params& p, int* start, int* row0, int* len, int lane) {
+    int base = 0;
+    for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
+        const int g = g0 + lane;
+        int n = 0, r = 0;
+        if (g < p.num_groups) {
+            const int cap = p.mode == kGroupedRows ? p.M : p.num_kb * kBlock;
+            r = min(max(__ldg(p.offsets + g), 0), cap);
+            n = max(min(max(__ldg(p.offsets + g + 1), 0), cap) - r, 0);
+            row0[g] = r;
+            len[g] = n;
+        }
+        int c = p.mode == kGroupedRows ? (n + kTileM - 1) / kTileM * p.num_n : (n + kBlock - 1) / kBlock;
+        int incl = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (g < p.num_groups) start[g] = base + incl - c;
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) start[p.num_groups] = base;
+}
+
+__device__ __forceinline__ int find_group(const Groups& gr, int n, int t) {
+    int lo = 0, hi = n - 1;   // the last group that starts at or before t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (gr.start[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int total_tiles(const Params& p, const Groups& gr) {
+    if (p.mode == kGroupedRows) return gr.start[p.num_groups];
+    return p.num_m * p.num_n * (p.mode == kGroupedK ? p.num_groups : 1);
+}
+
+template <int kTileM, int kTileN>
+__device__ __forceinline__ void decode_tile(const Params& p, const Groups& gr, int t, Piece& w) {
+    int local = t, nm = p.num_m;
+    w.tile = t;
+    w.g = 0;
+    w.d_row = 0;
+    int row0 = 0;
+    w.m_end = p.M;
+    w.kb0 = 0;
+    w.kb1 = p.num_kb;
+    int brow = 0;
+    if (p.mode == kGroupedRows) {
+        w.g = find_group(gr, p.num_groups, t);
+        local = t - gr.start[w.g];
+        row0 = gr.row0[w.g];
+        const int n = gr.len[w.g];
+        w.m_end = row0 + n;
+        nm = (n + kTileM - 1) / kTileM;
+        brow = w.g * p.N;
+    } else if (p.mode == kGroupedK) {
+        const int per = p.num_m * p.num_n;
+        w.g = t / per;
+        local = t - w.g * per;
+        w.kb0 = min(gr.start[w.g], p.num_kb);
+        w.kb1 = min(gr.start[w.g + 1], p.num_kb);
+        w.d_row = w.g * p.M;
+    }
+    // raster_m tile rows at a time, column by column ("CUTLASS", Part IV
+    // Stage 2: the tile order that lets co-resident tiles share operands in L2)
+    const int span = p.raster_m * p.num_n;
+    const int band = local / span;
+    const int rows = min(nm - band * p.raster_m, p.raster_m);
+    const int in = local - band * span;
+    const int mb = band * p.raster_m + in % rows;
+    const int nb = in / rows;
+    w.m0 = row0 + mb * kTileM;
+    w.n0 = nb * kTileN;
+    w.b_row = brow + w.n0;
+    w.nsplit = 1;
+    w.split = 0;
+    w.first = 0;
+}
+
+// The pieces of one worker.  Whole tiles: every workers-th one.  stream: the
+// k-block iterations of all tiles in one line, an equal run of them per
+// worker; a tile whose iterations fall to several workers is finished by the
+// last of them (one such tile at most begins in any worker's run, so the
+// first worker's number also names its arrival counter).
+struct Walk {
+    long long it, end;   // stream: iterations; otherwise tiles
+    long long total;
+    int wid, workers;
+};
+
+__device__ __forceinline__ Walk walk_begin(const Params& p, const Groups& gr, int wid, int workers) {
+    Walk s;
+    const int tiles = total_tiles(p, gr);
+    s.workers = workers;
+    s.wid = wid;
+    if (p.stream) {
+        s.total = static_cast<long long>(tiles) * p.num_kb;
+        // never more workers than iterations, so that every worker of a tile holds a piece of it
+        if (s.total < s.workers) s.workers = static_cast<int>(s.total);
+        s.it = wid < s.workers ? wid * s.total / s.workers : 0;
+        s.end = wid < s.workers ? (wid + 1) * s.total / s.workers : 0;
+    } else {
+        s.total = tiles;
+        s.it = wid;
+        s.end = tiles;
+    }
+    return s;
+}
+
+__device__ __forceinline__ int worker_of(const Walk& s, long long i) {
+    return static_cast<int>(((i + 1) * s.workers - 1) / s.total);
+}
+
+template <int kTileM, int kTileN>
+__device__ __forceinline__ bool walk_next(const Params& p, const Groups& gr, Walk& s, Piece& w) {
+    if (s.it >= s.end) return false;
+    if (!p.stream) {
+        decode_tile<kTileM, kTileN>(p, gr, static_cast<int>(s.it), w);
+        s.it += s.workers;
+        return true;
+    }
+    const int t = static_cast<int>(s.it / p.num_kb);
+    const long long t0 = static_cast<long long>(t) * p.num_kb;
+    decode_tile<kTileM, kTileN>(p, gr, t, w);
+    w.kb0 = static_cast<int>(s.it - t0);
+    const long long left = s.end - t0;
+    w.kb1 = left < p.num_kb ? static_cast<int>(left) : p.num_kb;
+    w.first = worker_of(s, t0);
+    w.nsplit = worker_of(s, t0 + p.num_kb - 1) - w.first + 1;
+    w.split = s.wid - w.first;
+    s.it = t0 + w.kb1;
+    return true;
+}
+
+// Partial slot of piece q of a shared tile: a worker's run holds the end of
+// at most one shared tile (slot 1) and the beginning of at most one (slot 0).
+__device__ __forceinline__ int slot_of(const Params& p, const Walk& s, const Piece& w, int q) {
+    const int c = w.first + q;
+    const bool begins = c * s.total / s.workers >= static_cast<long long>(w.tile) * p.num_kb;
+    return 2 * c + (begins ? 0 : 1);
+}
+
+__device__ __forceinline__ float scale_at(const ScaleRef& s, int row, int kb, int g) {
+    return __ldg(s.ptr + static_cast<long long>(min(row, s.rows - 1) >> s.shift) * s.rs + kb * s.ks + g * s.gs);
+}
+
+// ------------------------------------------------------------------ epilogue
+
+__device__ __forceinline__ float load_elem(const void* base, int is_f32, long long i) {
+    return is_f32 ? static_cast<const float*>(base)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(base)[i]);
+}
+
+// beta C + bias, activation, on CN (16 or 32) consecutive columns of one row
+template <int CN>
+__device__ __forceinline__ void finish_values(const Params& p, float (&v)[CN], long long row, int col0, bool row_ok) {
+    if (p.beta != 0.0f && row_ok) {
+        const long long at = row * p.ldc + col0;
+        if (p.c_vec && col0 + CN <= p.N) {
+            if (p.c_f32) {
+                const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.C) + at);
+#pragma unroll
+                for (int i = 0; i < CN / 4; ++i) {
+                    const float4 c = __ldcs(src + i);
+                    v[4 * i] = fmaf(p.beta, c.x, v[4 * i]);
+                    v[4 * i + 1] = fmaf(p.beta, c.y, v[4 * i + 1]);
+                    v[4 * i + 2] = fmaf(p.beta, c.z, v[4 * i + 2]);
+                    v[4 * i + 3] = fmaf(p.beta, c.w, v[4 * i + 3]);
+                }
+            } else {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.C) + at);
+#pragma unroll
+                for (int i = 0; i < CN / 8; ++i) {
+                    const uint4 c = __ldcs(src + i);
+                    const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        v[8 * i + 2 * h] = fmaf(p.beta, bf16_bits_to_float(u[h] & 0xFFFFu), v[8 * i + 2 * h]);
+                        v[8 * i + 2 * h + 1] = fmaf(p.beta, bf16_bits_to_float(u[h] >> 16), v[8 * i + 2 * h + 1]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < CN; ++i)
+                if (col0 + i < p.N) v[i] = fmaf(p.beta, load_elem(p.C, p.c_f32, at + i), v[i]);
+        }
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < CN; ++i)
+            if (col0 + i < p.N) v[i] += load_elem(p.bias, p.bias_f32, col0 + i);
+    }
+    if (p.act == 2) {
+#pragma unroll
+        for (int i = 0; i < CN / 2; ++i)
+            ptx::unpack2(gelu_erf2(ptx::pack2(v[2 * i], v[2 * i + 1])), v[2 * i], v[2 * i + 1]);
+    } else if (p.act == 1) {
+#pragma unroll
+        for (int i = 0; i < CN; ++i) v[i] = apply_act(1, v[i]);
+    }
+}
+
+constexpr int kStageWords = 32 * 17;   // per promote warp: 32 rows of 16 words, one word apart from the next row
+
+// Store CN columns of the warp's 32 rows.  Rows whose addresses allow it go
+// out from registers, 32 or 16 bytes at a time; otherwise (an odd pitch, a
+// ragged last chunk) the chunk turns through shared memory so that each store
+// instruction covers consecutive elements of one row.
+template <int CN>
+__device__ __forceinline__ void store_values(const Params& p, const float (&v)[CN], long long row, int col0,
+                                             int rows_ok, int lane, uint32_t* stage) {
+    if (p.d_vec && col0 + CN <= p.N) {
+        if (lane < rows_ok) {
+            char* dst = static_cast<char*>(p.D) + (row * p.ldd + col0) * (p.d_f32 ? 4 : 2);
+            uint32_t w[CN];
+            if (p.d_f32) {
+#pragma unroll
+                for (int i = 0; i < CN; ++i) w[i] = __float_as_uint(v[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < CN / 2; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            }
+            const int words = p.d_f32 ? CN : CN / 2;
+            if (p.d_vec == 32) {
+#pragma unroll
+                for (int i = 0; i < CN / 8; ++i) {
+                    if (8 * i < words) {
+                        const uint32_t q[8] = {w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
+                                               w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
+                        ptx::st_global_v8(dst + 32 * i, q);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < CN / 4; ++i)
+                    if (4 * i < words)
+                        *reinterpret_cast<uint4*>(dst + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
+        }
+        return;
+    }
+    const long long row_base = row - lane;
+    if (p.d_f32) {
+#pragma unroll
+        for (int h = 0; h < CN / 16; ++h) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) stage[lane * 17 + i] = __float_as_uint(v[16 * h + i]);
+            __syncwarp();
+            const int c = col0 + 16 * h + (lane & 15);
+            for (int r = lane >> 4; r < rows_ok; r += 2)
+                if (c < p.N) static_cast<float*>(p.D)[(row_base + r) * p.ldd + c] = __uint_as_float(stage[r * 17 + (lane & 15)]);
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < (CN + 31) / 32; ++h) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < (CN < 32 ? CN : 32) / 2; ++i)
+                stage[lane * 17 + i] = pack_bf16x2(v[32 * h + 2 * i], v[32 * h + 2 * i + 1]);
+            __syncwarp();
+            const int c = col0 + 32 * h + lane;
+            const uint16_t* s16 = reinterpret_cast<const uint16_t*>(stage);
+            if (lane < CN && c < p.N)
+                for (int r = 0; r < rows_ok; ++r)
+                    static_cast<uint16_t*>(p.D)[(row_base + r) * p.ldd + c] = s16[r * 34 + lane];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ kernels
+
+// kPair: 256 x 256 tiles on CTA pairs; otherwise kTileN columns per CTA.
+// kSwap: few rows of A.  B's rows take the 128 TMEM lanes and A's rows the
+// kTileN MMA columns, so that no lane computes padding; the tile is
+// D[m0 .. m0 + kTileN, n0 .. n0 + 128].
+// kColScale: one scale per B row (per MMA column), else one per 128.
+template <int kTileN, bool kPair, bool kSwap, bool kColScale>
+struct Shape {
+    static constexpr int kPromoteWarps = kSwap ? 4 : 8;
+    // The eight promote warps of a wide tile hold 128 (a pair) or 64 sums a
+    // thread; they take over registers that the four control warps give back
+    // (128 * 72 + 256 * 216 = 384 * 168, what the block is launched with).
+    static constexpr int kControlWarps = kSwap ? 2 : 4;
+    static constexpr bool kSplitRegs = !kSwap;
+    static constexpr int kControlRegs = 72, kPromoteRegs = 216, kLaunchRegs = 168;
+    static constexpr int kThreads = 32 * (kControlWarps + kPromoteWarps);
+    static_assert(!kSplitRegs || 32 * (kControlWarps * kControlRegs + kPromoteWarps * kPromoteRegs) <= kThreads * kLaunchRegs,
+                  "the shares add up to the launch's registers");
+    static constexpr int kLaneRows = 128;                          // rows of the lane operand per CTA
+    static constexpr int kColRows = kPair ? kTileN / 2 : kTileN;   // rows of the column operand per CTA
+    static constexpr int kAtomBytes = (kLaneRows + kColRows) * kBlock;
+    static constexpr int kStageBytes = kAtoms * kAtomBytes;
+    static constexpr int kBufs = kPair ? 2 : 4;
+    static constexpr int kTmemCols = kBufs * kTileN < 32 ? 32 : kBufs * kTileN;
+    static constexpr int kWarpCols = kSwap ? kTileN : kTileN / 2;  // MMA columns of one promote warp
+    // per promote warp: the store stage, and two buffers of column scales
+    static constexpr int kWarpWords = kStageWords + (kColScale || kSwap ? 2 * kWarpCols : 0);
+    static constexpr int kTileM = kSwap ? kTileN : (kPair ? 256 : 128);   // rows of D per tile
+    static constexpr int kTileNOut = kSwap ? 128 : kTileN;                // columns of D per tile
+    static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "TMEM columns are a power of two");
+    static_assert(kAtomBytes % 1024 == 0, "atoms stay 1024-byte aligned");
+    static int smem_bytes(int stages, int groups) {
+        return 1024 + stages * kStageBytes + kPromoteWarps * kWarpWords * 4 + static_cast<int>(sizeof(Ctl)) +
+               (groups > 0 ? (3 * groups + 1) * 4 : 0) + 64;
+    }
+};
+
+template <int kTileN, bool kPair, bool kSwap, bool kColScale>
+__global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThreads, 1)
+    block128_kernel(const __grid_constant__ Params p) {
+    using S = Shape<kTileN, kPair, kSwap, kColScale>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int stages = p.stages;
+    uint32_t* warp_words = reinterpret_cast<uint32_t*>(smem + stages * S::kStageBytes);
+    Ctl* ctl = reinterpret_cast<Ctl*>(warp_words + S::kPromoteWarps * S::kWarpWords);
+    int* tables = reinterpret_cast<int*>(ctl + 1);
+    const Groups gr{tables, tables + p.num_groups + 1, tables + 2 * p.num_groups + 1};
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = kPair ? ptx::cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int wid = kPair ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+    const int workers = kPair ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            ptx::mbar_init(&ctl->full[s], 1);
+            ptx::mbar_init(&ctl->empty[s], 1);
+        }
+        for (int b = 0; b < S::kBufs; ++b) {
+            ptx::mbar_init(&ctl->tmem_full[b], 1);
+            ptx::mbar_init(&ctl->tmem_empty[b], S::kPromoteWarps * (kPair ? 2 : 1));
+        }
+        ptx::mbar_init(&ctl->drain, 1);
+        ctl->abort_flag = 0;
+        ctl->last = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        if constexpr (kPair) {
+            ptx::tmem_alloc_pair(&ctl->tmem_base, S::kTmemCols);
+            ptx::tmem_relinquish_alloc_permit_pair();
+        } else {
+            ptx::tmem_alloc(&ctl->tmem_base, S::kTmemCols);
+            ptx::tmem_relinquish_alloc_permit();
+        }
+    }
+    if (warp == 0 && p.mode != kDense)
+        build_groups<S::kTileM>(p, tables, tables + p.num_groups + 1, tables + 2 * p.num_groups + 1, lane);
+    ptx::tc_fence_before_sync();
+    if constexpr (kPair) ptx::cluster_sync();   // the peer's barriers exist before anyone signals them
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = ctl->tmem_base;
+
+    Walk walk = walk_begin(p, gr, wid, workers);
+    Piece w;
+
+    if (warp < S::kControlWarps) {
+        if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kControlRegs));
+        if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        const bool issuer = lane == 0;
+        if (issuer && p.num_kb > 0) {
+            ptx::prefetch_tensormap(&p.tmA);
+            ptx::prefetch_tensormap(&p.tmB);
+        }
+        int stage = 0;
+        uint32_t phase = 0, armed = 0, armed_parity = 0;
+        bool first = true, ok = true;
+        while (ok && walk_next<S::kTileM, S::kTileNOut>(p, gr, walk, w)) {
+            const int a_row = w.m0 + (kPair ? static_cast<int>(rank) * 128 : 0);
+            const int b_row = w.b_row + (kPair ? static_cast<int>(rank) * S::kColRows : 0);
+            for (int kb = w.kb0; kb < w.kb1; kb += kAtoms) {
+                if (!wait_warp(&ctl->empty[stage], phase ^ 1u, p, ctl, 1)) { ok = false; break; }
+                const int atoms = min(kAtoms, w.kb1 - kb);
+                const bool skip = first && p.fault_inject == 1 && blockIdx.x == 0;
+                first = false;
+                if (!skip) {
+                    if (issuer) {
+                        uint64_t* fb = &ctl->full[stage];
+                        if (leader) ptx::mbar_arrive_expect_tx(fb, static_cast<uint32_t>((kPair ? 2 : 1) * atoms * S::kAtomBytes));
+                        const uint32_t fbc = kPair ? ptx::map_to_cta(ptx::smem_u32(fb), 0) : 0u;
+                        for (int at = 0; at < atoms; ++at) {
+                            uint8_t* sl = smem + stage * S::kStageBytes + at * S::kAtomBytes;
+                            uint8_t* sc = sl + S::kLaneRows * kBlock;
+                            const int x = (kb + at) * kBlock;
+                            const CUtensorMap* tl = kSwap ? &p.tmB : &p.tmA;
+                            const CUtensorMap* tc = kSwap ? &p.tmA : &p.tmB;
+                            const int yl = kSwap ? b_row : a_row, yc = kSwap ? a_row : b_row;
+                            if constexpr (kPair) {
+                                ptx::tma_load_2d_pair(sl, tl, fbc, x, yl);
+                                ptx::tma_load_2d_pair(sc, tc, fbc, x, yc);
+                            } else {
+                                ptx::tma_load_2d(sl, tl, fb, x, yl);
+                                ptx::tma_load_2d(sc, tc, fb, x, yc);
+                            }
+                        }
+                    }
+                    armed |= 1u << stage;
+                    armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                }
+                __syncwarp();
+                if (++stage == stages) { stage = 0; phase ^= 1u; }
+            }
+        }
+        // Every copy of this thread has landed before the CTA may leave: the
+        // leader sees it on its full barriers, the peer (whose copies count on
+        // the leader's) by their consumption.
+        for (int s = 0; s < stages; ++s) {
+            if (!(armed & (1u << s))) continue;
+            const uint32_t par = (armed_parity >> s) & 1u;
+            if (leader) wait_warp(&ctl->full[s], par, p, ctl, 11, false);
+            else wait_warp(&ctl->empty[s], par, p, ctl, 13, false);
+        }
+        } else if (warp == 1 && leader) {
+        // ------------------------------------------------------- MMA issuer
+        {
+            const bool issuer = lane == 0;
+            const uint32_t idesc = (1u << 4) | (p.ab_fmt << 7) | (p.ab_fmt << 10) |
+                                   (static_cast<uint32_t>(kTileN >> 3) << 17) |
+                                   (static_cast<uint32_t>((kPair ? 256 : 128) >> 4) << 24);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true, issued = false;
+            while (ok && walk_next<S::kTileM, S::kTileNOut>(p, gr, walk, w)) {
+                for (int kb = w.kb0; kb < w.kb1; kb += kAtoms) {
+                    if (!wait_warp(&ctl->full[stage], phase, p, ctl, 3)) { ok = false; break; }
+                    const int atoms = min(kAtoms, w.kb1 - kb);
+                    for (int at = 0; at < atoms; ++at) {
+                        if (!wait_warp(&ctl->tmem_empty[buf], bphase ^ 1u, p, ctl, 2)) { ok = false; break; }
+                        ptx::tc_fence_after_sync();
+                        if (issuer) {
+                            const uint32_t sl = ptx::smem_u32(smem + stage * S::kStageBytes + at * S::kAtomBytes);
+                            const uint64_t da = ptx::smem_desc_sw128(sl, 16, 1024);
+                            const uint64_t db = ptx::smem_desc_sw128(sl + S::kLaneRows * kBlock, 16, 1024);
+                            const uint32_t dt = tmem_base + static_cast<uint32_t>(buf * kTileN);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint64_t off = static_cast<uint64_t>(k * 32) >> 4;
+                                if constexpr (kPair) ptx::mma_f8_pair(dt, da + off, db + off, idesc, k > 0);
+                                else ptx::mma_f8(dt, da + off, db + off, idesc, k > 0);
+                            }
+                            if constexpr (kPair) ptx::mma_commit_pair(&ctl->tmem_full[buf], 0x3);
+                            else ptx::mma_commit(&ctl->tmem_full[buf]);
+                        }
+                        __syncwarp();
+                        issued = true;
+                        if (++buf == S::kBufs) { buf = 0; bphase ^= 1u; }
+                    }
+                    if (!ok) break;
+                    if (issuer) {
+                        if constexpr (kPair) ptx::mma_commit_pair(&ctl->empty[stage], 0x3);
+                        else ptx::mma_commit(&ctl->empty[stage]);
+                    }
+                    __syncwarp();
+                    if (++stage == stages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (issued) {   // every MMA has ended before the TMEM is freed
+                if (issuer) {
+                    if constexpr (kPair) ptx::mma_commit_pair(&ctl->drain, 0x1);
+                    else ptx::mma_commit(&ctl->drain);
+                }
+                __syncwarp();
+                wait_warp(&ctl->drain, 0, p, ctl, 12, false);
+            }
+        }
+        }
+    } else {
+        // ------------------------------------------------ promote and store
+        if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kPromoteRegs));
+        const int pw = warp - S::kControlWarps;
+        const int quad = warp & 3;               // the TMEM lanes this warp may read
+        const int col_base = kSwap ? 0 : (pw >> 2) * S::kWarpCols;
+        constexpr int WC = S::kWarpCols;
+        constexpr int kChunk = WC < 32 ? WC : 32;
+        constexpr int kChunks = WC / kChunk;
+        uint32_t* my_words = warp_words + pw * S::kWarpWords;
+        float* col_scale = reinterpret_cast<float*>(my_words + kStageWords);   // [2][WC]
+        constexpr bool kCols = kColScale || kSwap;                             // a scale per MMA column
+        constexpr int kPerLane = kCols ? (WC + 31) / 32 : 1;
+        int buf = 0, turn = 0;
+        uint32_t bphase = 0;
+        bool ok = true;
+        const int bar_threads = 32 * S::kPromoteWarps;
+        while (ok && walk_next<S::kTileM, S::kTileNOut>(p, gr, walk, w)) {
+            // this thread's row of the lane operand, and the scales' rows
+            const int lane_row = quad * 32 + lane;
+            const int m_row = w.m0 + static_cast<int>(rank) * 128 + lane_row;   // (not kSwap)
+            const ScaleRef& sl = kSwap ? p.sb : p.sa;
+            const ScaleRef& sc = kSwap ? p.sa : p.sb;
+            // rows past the operand (or past B's group) hold garbage or zeros that nobody stores
+            const int l_row = kSwap ? w.n0 + lane_row : m_row;
+            const int c_row = kSwap ? w.m0 : w.n0 + col_base;
+            const int lg = kSwap ? w.g : 0, cg = kSwap ? 0 : w.g;
+            uint64_t acc[WC / 2];
+#pragma unroll
+            for (int i = 0; i < WC / 2; ++i) acc[i] = 0;
+            // scales are fetched two k-blocks ahead of their use
+            float l_next[2], c_next[2][kPerLane];
+            auto fetch = [&](int slot, int kb) {
+                if (kb < w.kb1) {
+                    l_next[slot] = scale_at(sl, l_row, kb, lg);
+#pragma unroll
+                    for (int i = 0; i < kPerLane; ++i)
+                        c_next[slot][i] = scale_at(sc, kCols ? c_row + lane + 32 * i : c_row, kb, cg);
+                }
+            };
+            fetch(0, w.kb0);
+            fetch(1, w.kb0 + 1);
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                const float ls = l_next[0];
+                float cs[kPerLane];
+#pragma unroll
+                for (int i = 0; i < kPerLane; ++i) cs[i] = c_next[0][i];
+                l_next[0] = l_next[1];
+#pragma unroll
+                for (int i = 0; i < kPerLane; ++i) c_next[0][i] = c_next[1][i];
+                fetch(1, kb + 2);
+                float* my_cols = col_scale + (turn ^= 1) * WC;
+                if constexpr (kCols) {
+                    // (every lane has passed the other buffer's __syncwarp, so nobody reads this one any more)
+#pragma unroll
+                    for (int i = 0; i < kPerLane; ++i)
+                        if (lane + 32 * i < WC) my_cols[lane + 32 * i] = cs[i];
+                    __syncwarp();
+                }
+                if (!wait_warp(&ctl->tmem_full[buf], bphase, p, ctl, 4)) { ok = false; break; }
+                ptx::tc_fence_after_sync();
+                const uint32_t t0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                                    static_cast<uint32_t>(buf * kTileN + col_base);
+                const float s = kCols ? ls : ls * cs[0];
+                const uint64_t s2 = ptx::pack2(s, s);
+#pragma unroll
+                for (int j = 0; j < kChunks; ++j) {
+                    uint32_t r[kChunk];
+                    if constexpr (kChunk == 32) ptx::tmem_load_32cols(t0 + j * 32, r);
+                    else tmem_load_16cols(t0, r);
+                    if (j == kChunks - 1) {
+                        // the buffer is free for the next k-block's MMAs
+                        ptx::tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (kPair && !leader)
+                                ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(&ctl->tmem_empty[buf]), 0));
+                            else
+                                ptx::mbar_arrive(&ctl->tmem_empty[buf]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kChunk / 4; ++i) {
+                        uint64_t t2[2] = {ptx::pack2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])),
+                                          ptx::pack2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]))};
+                        if constexpr (kCols) {
+                            const float4 c4 = *reinterpret_cast<const float4*>(my_cols + j * kChunk + 4 * i);
+                            t2[0] = ptx::mul2(t2[0], ptx::pack2(c4.x, c4.y));
+                            t2[1] = ptx::mul2(t2[1], ptx::pack2(c4.z, c4.w));
+                        }
+                        const int a = (j * kChunk + 4 * i) / 2;
+                        acc[a] = ptx::fma2(t2[0], s2, acc[a]);
+                        acc[a + 1] = ptx::fma2(t2[1], s2, acc[a + 1]);
+                    }
+                }
+                if (++buf == S::kBufs) { buf = 0; bphase ^= 1u; }
+            }
+            if constexpr (!kPair) {
+                // all promote warps leave together: the barriers below need every thread
+                if (p.stream) ok = ptx::named_barrier_and(1, bar_threads, ok);
+            }
+            if (!ok) break;
+
+            bool finish = true;
+            if constexpr (!kPair) {
+                if (w.nsplit > 1) {
+                    // This piece's raw sums, column by column, 32 lanes on one line.
+                    // The barrier orders the CTA's stores before one thread's
+                    // acquire-release add; for the last arrival that add makes the
+                    // others' sums visible, and the second barrier passes it on.
+                    float* mine = p.partials + static_cast<size_t>(slot_of(p, walk, w, w.split)) * (128 * kTileN) +
+                                  static_cast<size_t>(col_base) * 128 + lane_row;
+#pragma unroll
+                    for (int i = 0; i < WC / 2; ++i) {
+                        float x, y;
+                        ptx::unpack2(acc[i], x, y);
+                        mine[(2 * i) * 128] = x;
+                        mine[(2 * i + 1) * 128] = y;
+                    }
+                    ptx::named_barrier_sync(1, bar_threads);
+                    if (threadIdx.x == 32 * S::kControlWarps) {
+                        const int old = ptx::atomic_add_acq_rel_gpu(p.counters + w.first, 1);
+                        ctl->last = old == w.nsplit - 1;
+                        if (ctl->last) atomicExch(p.counters + w.first, 0);   // ready for the next launch
+                    }
+                    ptx::named_barrier_sync(1, bar_threads);
+                    finish = ctl->last != 0;
+                    if (finish) {
+                        // in the order of the pieces, whoever finishes: the sum is the same every time
+#pragma unroll
+                        for (int i = 0; i < WC / 2; ++i) acc[i] = 0;
+                        for (int q = 0; q < w.nsplit; ++q) {
+                            const float* src = p.partials + static_cast<size_t>(slot_of(p, walk, w, q)) * (128 * kTileN) +
+                                               static_cast<size_t>(col_base) * 128 + lane_row;
+#pragma unroll
+                            for (int i = 0; i < WC / 2; ++i)
+                                acc[i] = ptx::add2(acc[i], ptx::pack2(__ldcg(src + (2 * i) * 128), __ldcg(src + (2 * i + 1) * 128)));
+                        }
+                    }
+                    // (ctl->last is not written again before every thread has passed this piece's
+                    // barriers and reached the next piece's first one)
+                }
+            }
+            if (!finish) continue;
+
+            if constexpr (kSwap) {
+                // lane_row is D's column n, the MMA columns are D's rows: 32 lanes store
+                // consecutive columns of one row
+                const int n = w.n0 + lane_row;
+                if (n < p.N) {
+                    const float bv = p.bias ? load_elem(p.bias, p.bias_f32, n) : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < WC; ++i) {
+                        float x, y;
+                        ptx::unpack2(acc[i / 2], x, y);
+                        float v = (i & 1) ? y : x;
+                        const int m = w.m0 + i;
+                        if (m < w.m_end) {
+                            const long long row = static_cast<long long>(w.d_row) + m;
+                            if (p.beta != 0.0f) v = fmaf(p.beta, load_elem(p.C, p.c_f32, row * p.ldc + n), v);
+                            v = apply_act(p.act, v + bv);
+                            if (p.d_f32) static_cast<float*>(p.D)[row * p.ldd + n] = v;
+                            else static_cast<__nv_bfloat16*>(p.D)[row * p.ldd + n] = __float2bfloat16_rn(v);
+                        }
+                    }
+                }
+            } else {
+                const int warp_row = w.m0 + static_cast<int>(rank) * 128 + quad * 32;
+                const int rows_ok = min(32, w.m_end - warp_row);
+                if (rows_ok > 0) {
+                    const long long row = static_cast<long long>(w.d_row) + m_row;
+#pragma unroll
+                    for (int j = 0; j < kChunks; ++j) {
+                        const int col0 = w.n0 + col_base + j * kChunk;
+                        if (col0 < p.N) {
+                            float v[kChunk];
+#pragma unroll
+                            for (int i = 0; i < kChunk / 2; ++i) ptx::unpack2(acc[j * kChunk / 2 + i], v[2 * i], v[2 * i + 1]);
+                            finish_values<kChunk>(p, v, row, col0, lane < rows_ok);
+                            store_values<kChunk>(p, v, row, col0, rows_ok, lane, my_words);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    ptx::tc_fence_before_sync();
+    if constexpr (kPair) ptx::cluster_sync();   // the leader's MMAs into the peer's TMEM are done
+    else __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after_sync();
+        if constexpr (kPair) ptx::tmem_dealloc_pair(tmem_base, S::kTmemCols);
+        else ptx::tmem_dealloc(tmem_base, S::kTmemCols);
+    }
+}
+
+}  // namespace b128
+}  // namespace tcg

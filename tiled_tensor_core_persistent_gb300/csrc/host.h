@@ -1,0 +1,38 @@
+// host.h -- what the library's translation units share on the host: error
+// text, device facts, tensor maps and the test knobs (defined in
+// tcgemm_host.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/tcgemm.h"
+
+namespace tcg {
+namespace host {
+
+struct Device {
+    int num_sms = 0;
+    int max_smem_optin = 0;
+};
+
+constexpr size_t kWorkspaceHeader = 256;   // status word and diagnostics at the start of a workspace
+
+// The current device; TCG_ERR_ARCH when it is not sm_103.
+tcg_status device(Device& out);
+// The text of tcg_last_error, and the code to return.
+tcg_status fail(tcg_status st, const char* text);
+tcg_status fail_launch(const char* what, cudaError_t e);
+// 2-D tensor map of an 8-bit matrix (inner contiguous bytes per row, outer
+// rows ld bytes apart), 128-byte swizzled boxes; cached as tcg_gemm's are.
+tcg_status map_bytes(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
+                     uint32_t box_inner, uint32_t box_outer);
+// Test knobs of tcg_debug_set.
+long long wait_timeout_ns();
+int fault_inject();
+
+}  // namespace host
+}  // namespace tcg

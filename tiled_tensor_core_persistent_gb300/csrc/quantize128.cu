@@ -1,0 +1,522 @@
+// quantize128.cu -- 8-bit codes and fp32 scales per block of 128, in the three
+// forms the block-scaled products read:
+//
+//   s = max(amax, 2^-96) / top        (times fl(1 / top); top = 448 or 57344;
+//                                      optionally rounded up to a power of two)
+//   q = rn8(clamp(x * fl(1 / s)))
+//
+// rows: a block is 128 consecutive elements of a row; cols: 128 rows of one
+// column, written transposed; tiles: 128 x 128, with an optional transposed
+// copy.  The arithmetic is fp32 with one rounding to 8 bits at the end, so
+// the codes are the same whatever the variant or the launch shape.
+//
+// All three are bound by memory: x is read once, the codes written once, and
+// the amax needs only the registers (rows), or one pass through shared memory
+// (cols and tiles, whose transposed codes turn there too).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "host.h"
+
+namespace {
+
+constexpr float kTiny = 0x1p-96f;   // keeps the scale and its reciprocal finite on a block of zeros
+constexpr int kMaxGroups = 1024;
+
+struct Quant {
+    const void* x;
+    long long ldx;
+    int rows, cols;
+    const int* index;      // rows of x to take, or NULL
+    int source;            // rows of x that index may name
+    uint8_t* q;
+    long long ldq;
+    uint8_t* qt;           // tiles: transposed copy, or NULL
+    long long ldqt;
+    float* scales;
+    long long lds;
+    float inv_top, top;
+    int pow2;
+    int e5m2;
+    int vec;               // x may be read, q written, in whole vectors
+    const int* offsets;
+    int groups;
+    int padded;
+};
+
+__device__ __forceinline__ float scale_of(const Quant& p, float amax) {
+    const float s = fmaxf(amax, kTiny) * p.inv_top;
+    if (!p.pow2) return s;
+    return __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0x7F800000u);
+}
+
+// Two values to two 8-bit codes, round to nearest even, saturating; NaN stays NaN.
+__device__ __forceinline__ uint32_t code2(float lo, float hi, int e5m2) {
+    uint16_t r;
+    if (e5m2) asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, int e5m2) {
+    return code2(a, b, e5m2) | (code2(c, d, e5m2) << 16);
+}
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+    static __device__ __forceinline__ float one(const void* p, long long i) {
+        return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+    }
+    static __device__ __forceinline__ void two(uint32_t w, float& a, float& b) {
+        a = __uint_as_float(w << 16);
+        b = __uint_as_float(w & 0xFFFF0000u);
+    }
+};
+template <>
+struct Elem<__half> {
+    static __device__ __forceinline__ float one(const void* p, long long i) {
+        return __half2float(static_cast<const __half*>(p)[i]);
+    }
+    static __device__ __forceinline__ void two(uint32_t w, float& a, float& b) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        a = f.x;
+        b = f.y;
+    }
+};
+template <>
+struct Elem<float> {
+    static __device__ __forceinline__ float one(const void* p, long long i) { return static_cast<const float*>(p)[i]; }
+};
+
+// N (8 or 16) consecutive elements from a 16-byte aligned address.
+template <typename T, int N>
+__device__ __forceinline__ void load_vec(const void* base, long long i, float (&v)[N]) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+            const uint4 w = __ldg(src + k);
+            v[4 * k] = __uint_as_float(w.x);
+            v[4 * k + 1] = __uint_as_float(w.y);
+            v[4 * k + 2] = __uint_as_float(w.z);
+            v[4 * k + 3] = __uint_as_float(w.w);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N / 8; ++k) {
+            const uint4 w = __ldg(src + k);
+            Elem<T>::two(w.x, v[8 * k], v[8 * k + 1]);
+            Elem<T>::two(w.y, v[8 * k + 2], v[8 * k + 3]);
+            Elem<T>::two(w.z, v[8 * k + 4], v[8 * k + 5]);
+            Elem<T>::two(w.w, v[8 * k + 6], v[8 * k + 7]);
+        }
+    }
+}
+
+// Elements [i, i + N) of a row of n, zeros past its end.
+template <typename T, int N>
+__device__ __forceinline__ void load_some(const Quant& p, long long row_at, int i, float (&v)[N]) {
+    if (p.vec && i + N <= p.cols) {
+        load_vec<T, N>(p.x, row_at + i, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = i + k < p.cols ? Elem<T>::one(p.x, row_at + i + k) : 0.0f;
+    }
+}
+
+// The row of x that output row r takes, or -1 (a row of zeros).
+__device__ __forceinline__ int source_row(const Quant& p, int r) {
+    if (!p.index) return r;
+    const int s = __ldg(p.index + r);
+    return s >= 0 && s < p.source ? s : -1;
+}
+
+template <int N>
+__device__ __forceinline__ float amax_of(const float (&v)[N]) {
+    float a = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) a = fmaxf(a, fabsf(v[k]));
+    return a;
+}
+
+// ------------------------------------------------------------------------ rows
+//
+// Eight lanes hold a block (16 elements each), a warp four rows of one block
+// column, a CTA 32 rows: the scales of a CTA are one 128-byte line.  kU blocks
+// along the row per warp keep that many loads in flight.
+template <typename T, int kU>
+__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Quant p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = blockIdx.y * 32 + warp * 4 + (lane >> 3);
+    const int kb0 = blockIdx.x * kU;
+    if (r >= p.rows) return;
+    const unsigned peers = 0xFFu << (lane & 24);
+    const int src = source_row(p, r);
+    const long long at = src * p.ldx;
+    const int blocks = (p.cols + 127) >> 7;
+    float v[kU][16];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        if (src >= 0 && kb0 + u < blocks) {
+            load_some<T, 16>(p, at, (kb0 + u) * 128 + (lane & 7) * 16, v[u]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[u][k] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        if (kb0 + u >= blocks) break;
+        float a = amax_of<16>(v[u]);
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) a = fmaxf(a, __shfl_xor_sync(peers, a, d));
+        const float s = scale_of(p, a);
+        const float inv = 1.0f / s;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            w[k] = code4(v[u][4 * k] * inv, v[u][4 * k + 1] * inv, v[u][4 * k + 2] * inv, v[u][4 * k + 3] * inv, p.e5m2);
+        const int c = (kb0 + u) * 128 + (lane & 7) * 16;
+        uint8_t* dst = p.q + r * p.ldq + c;
+        if (p.vec && c + 16 <= p.cols) {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (c + k < p.cols) dst[k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k % 4)));
+        }
+        if ((lane & 7) == 0) p.scales[(kb0 + u) * p.lds + r] = s;
+    }
+}
+
+// ------------------------------------------------------------------------ cols
+//
+// One CTA: the 128 rows of one block row, 64 columns.  A thread holds eight
+// columns of four consecutive rows, so that its codes of one column are one
+// word; the words turn through shared memory (33 words a column, so that a
+// warp's eight column groups meet two-way at worst) into 128-byte lines.
+constexpr int kColTile = 64;
+
+// The first row and the rows of padded block b: the groups' blocks one after
+// the other, each group's last block partly empty.  One warp; the same for
+// all its lanes.
+__device__ __forceinline__ void find_block(const Quant& p, int b, int lane, int& row, int& n) {
+    if (!p.offsets) {
+        row = b * 128;
+        n = min(128, p.rows - row);
+        return;
+    }
+    int base = 0;
+    row = 0;
+    n = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+        const int g = g0 + lane;
+        int r = 0, len = 0;
+        if (g < p.groups) {
+            r = min(max(__ldg(p.offsets + g), 0), p.rows);
+            len = max(min(max(__ldg(p.offsets + g + 1), 0), p.rows) - r, 0);
+        }
+        const int blocks = (len + 127) >> 7;
+        int incl = blocks;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        const int first = base + incl - blocks;
+        const unsigned hit = __ballot_sync(0xffffffffu, b >= first && b < first + blocks);
+        if (hit) {
+            const int who = __ffs(hit) - 1;
+            const int in = (b - __shfl_sync(0xffffffffu, first, who)) * 128;
+            row = __shfl_sync(0xffffffffu, r, who) + in;
+            n = min(128, __shfl_sync(0xffffffffu, len, who) - in);
+            return;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) cols_kernel(const __grid_constant__ Quant p) {
+    __shared__ float part[8][kColTile];
+    __shared__ float inv_s[kColTile];
+    __shared__ uint32_t words[kColTile * 33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int block = blockIdx.y, c0 = blockIdx.x * kColTile;
+    int row, n;
+    find_block(p, block, lane, row, n);
+    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;   // 8 columns, 4 rows
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = rg * 4 + i;
+        const int src = r < n ? source_row(p, row + r) : -1;
+        if (src >= 0) {
+            load_some<T, 8>(p, src * p.ldx, c0 + cg * 8, v[i]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float a = fmaxf(fmaxf(fabsf(v[0][k]), fabsf(v[1][k])), fmaxf(fabsf(v[2][k]), fabsf(v[3][k])));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
+        if (lane < 8) part[warp][cg * 8 + k] = a;
+    }
+    __syncthreads();
+    if (threadIdx.x < kColTile) {
+        float a = part[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) a = fmaxf(a, part[i][threadIdx.x]);
+        const float s = scale_of(p, a);
+        inv_s[threadIdx.x] = 1.0f / s;
+        const int c = c0 + threadIdx.x;
+        if (c < p.cols) p.scales[block * p.lds + c] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float inv = inv_s[cg * 8 + k];
+        words[(cg * 8 + k) * 33 + rg] = code4(v[0][k] * inv, v[1][k] * inv, v[2][k] * inv, v[3][k] * inv, p.e5m2);
+    }
+    __syncthreads();
+    const bool whole = p.ldq % 4 == 0 && reinterpret_cast<uintptr_t>(p.q) % 4 == 0;
+    for (int c = warp; c < kColTile && c0 + c < p.cols; c += 8) {
+        uint8_t* dst = p.q + (c0 + c) * p.ldq + block * 128LL;
+        const uint32_t w = words[c * 33 + lane];
+        if (whole) {
+            reinterpret_cast<uint32_t*>(dst)[lane] = w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) dst[4 * lane + k] = static_cast<uint8_t>(w >> (8 * k));
+        }
+    }
+}
+
+// ----------------------------------------------------------------------- tiles
+//
+// One CTA: one 128 x 128 tile of one matrix of the batch (matrix b is rows
+// [b rows, (b + 1) rows) of x).  A thread holds eight columns of eight rows
+// (two groups of four, 64 rows apart); the row-major codes leave from
+// registers, eight bytes a row, the transposed ones through shared memory.
+template <typename T>
+__global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ Quant p) {
+    __shared__ float part[8];
+    __shared__ uint32_t words[128 * 33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b = blockIdx.z, r0 = blockIdx.y * 128, c0 = blockIdx.x * 128;
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;   // 8 columns; rows 4 rg + {0..3} + {0, 64}
+    float v[8][8];
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = r0 + rg * 4 + (i & 3) + (i >> 2) * 64;
+        if (r < p.rows) {
+            load_some<T, 8>(p, (static_cast<long long>(b) * p.rows + r) * p.ldx, c0 + cg * 8, v[i]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
+        }
+        a = fmaxf(a, amax_of<8>(v[i]));
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+    if (lane == 0) part[warp] = a;
+    __syncthreads();
+    a = part[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) a = fmaxf(a, part[i]);
+    const float s = scale_of(p, a);
+    const float inv = 1.0f / s;
+    if (threadIdx.x == 0)
+        p.scales[(static_cast<long long>(b) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[i][k] *= inv;
+    if (p.q) {
+        const int c = c0 + cg * 8;
+        const bool whole = p.ldq % 8 == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && c + 8 <= p.cols;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + rg * 4 + (i & 3) + (i >> 2) * 64;
+            if (r >= p.rows) continue;
+            uint8_t* dst = p.q + (static_cast<long long>(b) * p.rows + r) * p.ldq + c;
+            const uint2 w = make_uint2(code4(v[i][0], v[i][1], v[i][2], v[i][3], p.e5m2),
+                                       code4(v[i][4], v[i][5], v[i][6], v[i][7], p.e5m2));
+            if (whole) {
+                *reinterpret_cast<uint2*>(dst) = w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c + k < p.cols) dst[k] = static_cast<uint8_t>((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
+            }
+        }
+    }
+    if (!p.qt) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            words[(cg * 8 + k) * 33 + h * 16 + rg] =
+                code4(v[4 * h][k], v[4 * h + 1][k], v[4 * h + 2][k], v[4 * h + 3][k], p.e5m2);
+    __syncthreads();
+    const bool whole = p.ldqt % 4 == 0 && reinterpret_cast<uintptr_t>(p.qt) % 4 == 0;
+    for (int c = warp; c < 128 && c0 + c < p.cols; c += 8) {
+        const int r = r0 + 4 * lane;
+        uint8_t* dst = p.qt + (static_cast<long long>(b) * p.cols + c0 + c) * p.ldqt + r;
+        const uint32_t w = words[c * 33 + lane];
+        if (whole && r + 4 <= p.rows) {
+            *reinterpret_cast<uint32_t*>(dst) = w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (r + k < p.rows) dst[k] = static_cast<uint8_t>(w >> (8 * k));
+        }
+    }
+}
+
+// ------------------------------------------------------------------------ host
+
+int x_bytes(tcg_dtype t) { return t == TCG_F32 ? 4 : 2; }
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// The rules the three forms share; fills everything but the outputs' shapes.
+tcg_status start(Quant& p, int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx, tcg_dtype q_dtype,
+                 float* scales, int pow2, const int* index, int source) {
+    if (rows < 0 || cols < 0 || source < 0) return TCG_ERR_INVALID_ARG;
+    if (x_dtype != TCG_BF16 && x_dtype != TCG_F16 && x_dtype != TCG_F32) return TCG_ERR_INVALID_ARG;
+    if (q_dtype != TCG_E4M3 && q_dtype != TCG_E5M2) return TCG_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return TCG_OK;
+    if ((!x && !(index && source == 0)) || !scales || ldx < cols) return TCG_ERR_INVALID_ARG;
+    if (!aligned(x, x_bytes(x_dtype)) || !aligned(scales, 4) || !aligned(index, 4)) return TCG_ERR_MISALIGNED;
+    p.x = x;
+    p.ldx = ldx;
+    p.rows = rows;
+    p.cols = cols;
+    p.index = index;
+    p.source = source;
+    p.scales = scales;
+    p.top = q_dtype == TCG_E5M2 ? 57344.0f : 448.0f;
+    p.inv_top = 1.0f / p.top;
+    p.pow2 = pow2 != 0;
+    p.e5m2 = q_dtype == TCG_E5M2;
+    p.vec = aligned(x, 16) && (static_cast<long long>(ldx) * x_bytes(x_dtype)) % 16 == 0;
+    return TCG_OK;
+}
+
+tcg_status launched(const char* what) {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch(what, e);
+}
+
+template <int kU>
+void launch_rows(const Quant& p, tcg_dtype t, dim3 grid, cudaStream_t s) {
+    if (t == TCG_BF16) rows_kernel<__nv_bfloat16, kU><<<grid, 256, 0, s>>>(p);
+    else if (t == TCG_F16) rows_kernel<__half, kU><<<grid, 256, 0, s>>>(p);
+    else rows_kernel<float, kU><<<grid, 256, 0, s>>>(p);
+}
+
+}  // namespace
+
+extern "C" {
+
+tcg_status tcg_quantize_rows128(int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx, const int* row_index,
+                                int source_rows, void* q, int ldq, tcg_dtype q_dtype, float* scales, int ld_scales,
+                                int pow2, void* stream) {
+    Quant p = {};
+    tcg_status st = start(p, rows, cols, x_dtype, x, ldx, q_dtype, scales, pow2, row_index, source_rows);
+    if (st != TCG_OK || rows == 0 || cols == 0) return st;
+    if (!q || ldq < cols || ld_scales < rows) return TCG_ERR_INVALID_ARG;
+    tcg::host::Device dev;
+    if ((st = tcg::host::device(dev)) != TCG_OK) return st;
+    p.q = static_cast<uint8_t*>(q);
+    p.ldq = ldq;
+    p.lds = ld_scales;
+    p.vec = p.vec && aligned(q, 16) && ldq % 16 == 0;
+    const int blocks = (cols + 127) / 128, row_ctas = (rows + 31) / 32;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    for (int done = 0; done < row_ctas; done += 65535) {   // gridDim.y's limit
+        const int n = std::min(row_ctas - done, 65535);
+        Quant part = p;
+        const long long first = static_cast<long long>(done) * 32;
+        part.rows = static_cast<int>(std::min<long long>(rows - first, static_cast<long long>(n) * 32));
+        if (p.index) part.index = p.index + first;
+        else part.x = static_cast<const char*>(p.x) + first * ldx * x_bytes(x_dtype);
+        part.q = p.q + first * ldq;
+        part.scales = p.scales + first;
+        // four blocks per warp once that still gives every SM several CTAs
+        if (static_cast<long long>(n) * ((blocks + 3) / 4) >= 4LL * dev.num_sms)
+            launch_rows<4>(part, x_dtype, dim3((blocks + 3) / 4, n), s);
+        else
+            launch_rows<1>(part, x_dtype, dim3(blocks, n), s);
+    }
+    return launched("tcg_quantize_rows128");
+}
+
+tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx, const int* row_index,
+                                int source_rows, int num_groups, const int* offsets, int padded_rows, void* q,
+                                int ldq, tcg_dtype q_dtype, float* scales, int ld_scales, int pow2, void* stream) {
+    Quant p = {};
+    if (padded_rows < 0 || padded_rows % 128 || num_groups < 0) return TCG_ERR_INVALID_ARG;
+    if (num_groups > kMaxGroups) return TCG_ERR_UNSUPPORTED;
+    if (padded_rows == 0 || cols == 0) return rows < 0 || cols < 0 ? TCG_ERR_INVALID_ARG : TCG_OK;
+    // (no rows at all still writes the padding)
+    tcg_status st = start(p, rows > 0 ? rows : rows == 0 ? 1 : -1, cols, x_dtype, rows == 0 ? scales : x, rows == 0 ? INT_MAX : ldx,
+                          q_dtype, scales, pow2, row_index, source_rows);
+    if (st != TCG_OK) return st;
+    p.rows = rows;
+    if (!q || ldq < padded_rows || ld_scales < cols) return TCG_ERR_INVALID_ARG;
+    if (num_groups > 1 && !offsets) return TCG_ERR_INVALID_ARG;
+    if (!offsets && padded_rows < rows) return TCG_ERR_INVALID_ARG;
+    if (!aligned(offsets, 4)) return TCG_ERR_MISALIGNED;
+    tcg::host::Device dev;
+    if ((st = tcg::host::device(dev)) != TCG_OK) return st;
+    p.q = static_cast<uint8_t*>(q);
+    p.ldq = ldq;
+    p.lds = ld_scales;
+    p.offsets = offsets;
+    p.groups = num_groups;
+    p.padded = padded_rows;
+    const int row_blocks = padded_rows / 128;
+    if (row_blocks > 65535) return TCG_ERR_UNSUPPORTED;
+    const dim3 grid((cols + kColTile - 1) / kColTile, row_blocks);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (x_dtype == TCG_BF16) cols_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
+    else if (x_dtype == TCG_F16) cols_kernel<__half><<<grid, 256, 0, s>>>(p);
+    else cols_kernel<float><<<grid, 256, 0, s>>>(p);
+    return launched("tcg_quantize_cols128");
+}
+
+tcg_status tcg_quantize_tiles128(int batch, int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx, void* q,
+                                 int ldq, void* qt, int ldqt, tcg_dtype q_dtype, float* scales, int pow2,
+                                 void* stream) {
+    Quant p = {};
+    if (batch < 0) return TCG_ERR_INVALID_ARG;
+    tcg_status st = start(p, rows, cols, x_dtype, x, ldx, q_dtype, scales, pow2, nullptr, 0);
+    if (st != TCG_OK || rows == 0 || cols == 0 || batch == 0) return st;
+    if ((!q && !qt) || (q && ldq < cols) || (qt && ldqt < rows)) return TCG_ERR_INVALID_ARG;
+    if (batch > 65535 || (rows + 127) / 128 > 65535) return TCG_ERR_UNSUPPORTED;
+    tcg::host::Device dev;
+    if ((st = tcg::host::device(dev)) != TCG_OK) return st;
+    p.q = static_cast<uint8_t*>(q);
+    p.ldq = ldq;
+    p.qt = static_cast<uint8_t*>(qt);
+    p.ldqt = ldqt;
+    const dim3 grid((cols + 127) / 128, (rows + 127) / 128, batch);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (x_dtype == TCG_BF16) tiles_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
+    else if (x_dtype == TCG_F16) tiles_kernel<__half><<<grid, 256, 0, s>>>(p);
+    else tiles_kernel<float><<<grid, 256, 0, s>>>(p);
+    return launched("tcg_quantize_tiles128");
+}
+
+}  // extern "C"

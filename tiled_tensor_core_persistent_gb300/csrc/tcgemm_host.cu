@@ -24,6 +24,7 @@
 
 #include "../../include/tcgemm.h"
 #include "gemm_kernel.cuh"
+#include "host.h"
 #include "launch.cuh"
 #include "pack_kernel.cuh"
 
@@ -1372,3 +1373,36 @@ extern "C" tcg_status tcg_gemm_grouped(int num_problems, const tcg_problem* prob
     e = tcg::launch_grouped(kp, launch_shape(pl), is_fp8(ab_dtype), stream, &what);
     return e == cudaSuccess ? TCG_OK : fail_launch(what, e);
 }
+
+// =================================================================== shared with the other units
+
+namespace tcg {
+namespace host {
+
+tcg_status device(Device& out) {
+    DeviceInfo d;
+    tcg_status st = device_info(d);
+    if (st == TCG_OK) st = arch_check(d);
+    out.num_sms = d.num_sms;
+    out.max_smem_optin = d.max_smem_optin;
+    return st;
+}
+
+tcg_status fail(tcg_status st, const char* text) {
+    g_last_error = text;
+    return st;
+}
+
+tcg_status fail_launch(const char* what, cudaError_t e) { return ::fail_launch(what, e); }
+
+tcg_status map_bytes(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
+                     uint32_t box_inner, uint32_t box_outer) {
+    return encode_2d(map, TCG_E4M3, base, inner, outer, ld, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+long long wait_timeout_ns() { return g_timeout_ns > 0 ? g_timeout_ns : kDefaultTimeoutNs; }
+
+int fault_inject() { return g_fault_inject; }
+
+}  // namespace host
+}  // namespace tcg
