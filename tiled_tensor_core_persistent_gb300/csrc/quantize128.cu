@@ -467,7 +467,7 @@ tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const voi
                                 int ldq, tcg_dtype q_dtype, float* scales, int ld_scales, int pow2, void* stream) {
     Quant p = {};
     if (padded_rows < 0 || padded_rows % 128 || num_groups < 0) return TCG_ERR_INVALID_ARG;
-    if (num_groups > kMaxGroups) return TCG_ERR_UNSUPPORTED;
+    if (num_groups > kMaxGroups || padded_rows / 128 > 65535) return TCG_ERR_UNSUPPORTED;
     if (padded_rows == 0 || cols == 0) return rows < 0 || cols < 0 ? TCG_ERR_INVALID_ARG : TCG_OK;
     // (no rows at all still writes the padding)
     tcg_status st = start(p, rows > 0 ? rows : rows == 0 ? 1 : -1, cols, x_dtype, rows == 0 ? scales : x, rows == 0 ? INT_MAX : ldx,
@@ -487,7 +487,6 @@ tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const voi
     p.groups = num_groups;
     p.padded = padded_rows;
     const int row_blocks = padded_rows / 128;
-    if (row_blocks > 65535) return TCG_ERR_UNSUPPORTED;
     const dim3 grid((cols + kColTile - 1) / kColTile, row_blocks);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (x_dtype == TCG_BF16) cols_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
