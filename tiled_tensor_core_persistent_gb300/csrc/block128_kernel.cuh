@@ -34,6 +34,7 @@ namespace b128 {
 constexpr int kBlock = 128;                 // K elements per scale = bytes per swizzle row
 constexpr int kAtoms = 2;                   // k-blocks per pipeline stage
 constexpr int kMaxGroups = 1024;
+constexpr int kScaleSlots = 8;              // k-blocks of scales in flight
 
 enum Mode : int { kDense = 0, kGroupedRows = 1, kGroupedK = 2 };
 
@@ -81,6 +82,8 @@ struct alignas(16) Ctl {
     uint64_t empty[16];
     uint64_t tmem_full[4];
     uint64_t tmem_empty[4];
+    uint64_t scale_full[kScaleSlots];
+    uint64_t scale_empty[kScaleSlots];
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -121,16 +124,62 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
     return __all_sync(0xffffffffu, ok);
 }
 
-// 32 lanes x N consecutive TMEM columns, N = 16 or 32, the wait folded in.
-__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+// 32 lanes x 16 or 32 consecutive TMEM columns.  The registers are valid
+// after tmem_wait, which takes them as operands so that no use moves ahead.
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+// 4-byte asynchronous copy global -> shared, and the arrival (one of the
+// barrier's expected ones) once this thread's copies so far have landed.
+__device__ __forceinline__ void copy4_async(uint32_t smem_addr, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Arrival on the pair leader's barrier.  It hands over TMEM columns that this
+// warp has read (tcgen05.wait::ld returned the values to registers), no
+// memory, so it needs no release at cluster scope: with one, the fence in
+// front of it held each k-block up for over a thousand cycles (8192^3: 1064 us).
+__device__ __forceinline__ void arrive_at_leader(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(ptx::map_to_cta(ptx::smem_u32(bar), 0)) : "memory");
 }
 
 // ------------------------------------------------------------------ schedule
@@ -303,8 +352,10 @@ __device__ __forceinline__ int slot_of(const Params& p, const Walk& s, const Pie
     return 2 * c + (begins ? 0 : 1);
 }
 
-__device__ __forceinline__ float scale_at(const ScaleRef& s, int row, int kb, int g) {
-    return __ldg(s.ptr + static_cast<long long>(min(row, s.rows - 1) >> s.shift) * s.rs + kb * s.ks + g * s.gs);
+// Where the scales of a row start (rows past the operand, or past B's group,
+// take the last one: nobody stores what they scale).
+__device__ __forceinline__ const float* scale_row(const ScaleRef& s, int row, int g) {
+    return s.ptr + static_cast<long long>(min(row, s.rows - 1) >> s.shift) * s.rs + g * s.gs;
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -444,7 +495,7 @@ struct Shape {
     // The eight promote warps of a wide tile hold 128 (a pair) or 64 sums a
     // thread; they take over registers that the four control warps give back
     // (128 * 72 + 256 * 216 = 384 * 168, what the block is launched with).
-    static constexpr int kControlWarps = kSwap ? 2 : 4;
+    static constexpr int kControlWarps = 4;
     static constexpr bool kSplitRegs = !kSwap;
     static constexpr int kControlRegs = 72, kPromoteRegs = 216, kLaunchRegs = 168;
     static constexpr int kThreads = 32 * (kControlWarps + kPromoteWarps);
@@ -457,14 +508,18 @@ struct Shape {
     static constexpr int kBufs = kPair ? 2 : 4;
     static constexpr int kTmemCols = kBufs * kTileN < 32 ? 32 : kBufs * kTileN;
     static constexpr int kWarpCols = kSwap ? kTileN : kTileN / 2;  // MMA columns of one promote warp
-    // per promote warp: the store stage, and two buffers of column scales
-    static constexpr int kWarpWords = kStageWords + (kColScale || kSwap ? 2 * kWarpCols : 0);
+    static constexpr int kWarpWords = kSwap ? 0 : kStageWords;     // store stage of one promote warp
+    // scales of one k-block: a word per lane row, then one per MMA column (or
+    // per 128 columns)
+    static constexpr bool kCols = kColScale || kSwap;
+    static constexpr int kColWords = kCols ? kTileN : 4;
+    static constexpr int kSlotWords = 128 + kColWords;
     static constexpr int kTileM = kSwap ? kTileN : (kPair ? 256 : 128);   // rows of D per tile
     static constexpr int kTileNOut = kSwap ? 128 : kTileN;                // columns of D per tile
     static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "TMEM columns are a power of two");
     static_assert(kAtomBytes % 1024 == 0, "atoms stay 1024-byte aligned");
     static int smem_bytes(int stages, int groups) {
-        return 1024 + stages * kStageBytes + kPromoteWarps * kWarpWords * 4 + static_cast<int>(sizeof(Ctl)) +
+        return 1024 + stages * kStageBytes + (kPromoteWarps * kWarpWords + kScaleSlots * kSlotWords) * 4 + static_cast<int>(sizeof(Ctl)) +
                (groups > 0 ? (3 * groups + 1) * 4 : 0) + 64;
     }
 };
@@ -477,7 +532,8 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int stages = p.stages;
     uint32_t* warp_words = reinterpret_cast<uint32_t*>(smem + stages * S::kStageBytes);
-    Ctl* ctl = reinterpret_cast<Ctl*>(warp_words + S::kPromoteWarps * S::kWarpWords);
+    float* scale_words = reinterpret_cast<float*>(warp_words + S::kPromoteWarps * S::kWarpWords);
+    Ctl* ctl = reinterpret_cast<Ctl*>(scale_words + kScaleSlots * S::kSlotWords);
     int* tables = reinterpret_cast<int*>(ctl + 1);
     const Groups gr{tables, tables + p.num_groups + 1, tables + 2 * p.num_groups + 1};
 
@@ -496,6 +552,10 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         for (int b = 0; b < S::kBufs; ++b) {
             ptx::mbar_init(&ctl->tmem_full[b], 1);
             ptx::mbar_init(&ctl->tmem_empty[b], S::kPromoteWarps * (kPair ? 2 : 1));
+        }
+        for (int s = 0; s < kScaleSlots; ++s) {
+            ptx::mbar_init(&ctl->scale_full[s], 32);
+            ptx::mbar_init(&ctl->scale_empty[s], S::kPromoteWarps);
         }
         ptx::mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
@@ -632,6 +692,43 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                 wait_warp(&ctl->drain, 0, p, ctl, 12, false);
             }
         }
+        } else if (warp == 2) {
+        // ---------------------------------------------------- scales, ahead
+        const ScaleRef& sl = kSwap ? p.sb : p.sa;
+        const ScaleRef& sc = kSwap ? p.sa : p.sb;
+        constexpr int kColLoads = S::kCols ? (kTileN + 31) / 32 : 1;
+        const bool col_lane = S::kCols ? lane < kTileN : lane < kTileN / 128;
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && walk_next<S::kTileM, S::kTileNOut>(p, gr, walk, w)) {
+            const int l0 = kSwap ? w.n0 : w.m0 + static_cast<int>(rank) * 128;
+            const int c0 = kSwap ? w.m0 : w.n0;
+            const float* lp[4];
+            const float* cp[kColLoads];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lp[i] = scale_row(sl, l0 + lane + 32 * i, kSwap ? w.g : 0) + w.kb0 * sl.ks;
+#pragma unroll
+            for (int i = 0; i < kColLoads; ++i)
+                cp[i] = scale_row(sc, c0 + (S::kCols ? lane + 32 * i : 128 * lane), kSwap ? 0 : w.g) + w.kb0 * sc.ks;
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                if (!wait_warp(&ctl->scale_empty[slot], phase ^ 1u, p, ctl, 6)) { ok = false; break; }
+                const uint32_t dst = ptx::smem_u32(scale_words + slot * S::kSlotWords + lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    copy4_async(dst + 128 * i, lp[i]);
+                    lp[i] += sl.ks;
+                }
+#pragma unroll
+                for (int i = 0; i < kColLoads; ++i) {
+                    if (col_lane) copy4_async(dst + 512 + 128 * i, cp[i]);
+                    cp[i] += sc.ks;
+                }
+                copies_arrive(&ctl->scale_full[slot]);
+                if (++slot == kScaleSlots) { slot = 0; phase ^= 1u; }
+            }
+        }
+        copies_wait_all();
         }
     } else {
         // ------------------------------------------------ promote and store
@@ -643,83 +740,51 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         constexpr int kChunk = WC < 32 ? WC : 32;
         constexpr int kChunks = WC / kChunk;
         uint32_t* my_words = warp_words + pw * S::kWarpWords;
-        float* col_scale = reinterpret_cast<float*>(my_words + kStageWords);   // [2][WC]
-        constexpr bool kCols = kColScale || kSwap;                             // a scale per MMA column
-        constexpr int kPerLane = kCols ? (WC + 31) / 32 : 1;
-        int buf = 0, turn = 0;
-        uint32_t bphase = 0;
+        int buf = 0, slot = 0;
+        uint32_t bphase = 0, sphase = 0;
         bool ok = true;
         const int bar_threads = 32 * S::kPromoteWarps;
+        const int lane_row = quad * 32 + lane;   // this thread's row of the lane operand's tile
         while (ok && walk_next<S::kTileM, S::kTileNOut>(p, gr, walk, w)) {
-            // this thread's row of the lane operand, and the scales' rows
-            const int lane_row = quad * 32 + lane;
-            const int m_row = w.m0 + static_cast<int>(rank) * 128 + lane_row;   // (not kSwap)
-            const ScaleRef& sl = kSwap ? p.sb : p.sa;
-            const ScaleRef& sc = kSwap ? p.sa : p.sb;
-            // rows past the operand (or past B's group) hold garbage or zeros that nobody stores
-            const int l_row = kSwap ? w.n0 + lane_row : m_row;
-            const int c_row = kSwap ? w.m0 : w.n0 + col_base;
-            const int lg = kSwap ? w.g : 0, cg = kSwap ? 0 : w.g;
             uint64_t acc[WC / 2];
 #pragma unroll
             for (int i = 0; i < WC / 2; ++i) acc[i] = 0;
-            // scales are fetched two k-blocks ahead of their use
-            float l_next[2], c_next[2][kPerLane];
-            auto fetch = [&](int slot, int kb) {
-                if (kb < w.kb1) {
-                    l_next[slot] = scale_at(sl, l_row, kb, lg);
-#pragma unroll
-                    for (int i = 0; i < kPerLane; ++i)
-                        c_next[slot][i] = scale_at(sc, kCols ? c_row + lane + 32 * i : c_row, kb, cg);
-                }
-            };
-            fetch(0, w.kb0);
-            fetch(1, w.kb0 + 1);
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                const float ls = l_next[0];
-                float cs[kPerLane];
-#pragma unroll
-                for (int i = 0; i < kPerLane; ++i) cs[i] = c_next[0][i];
-                l_next[0] = l_next[1];
-#pragma unroll
-                for (int i = 0; i < kPerLane; ++i) c_next[0][i] = c_next[1][i];
-                fetch(1, kb + 2);
-                float* my_cols = col_scale + (turn ^= 1) * WC;
-                if constexpr (kCols) {
-                    // (every lane has passed the other buffer's __syncwarp, so nobody reads this one any more)
-#pragma unroll
-                    for (int i = 0; i < kPerLane; ++i)
-                        if (lane + 32 * i < WC) my_cols[lane + 32 * i] = cs[i];
-                    __syncwarp();
-                }
+                if (!wait_warp(&ctl->scale_full[slot], sphase, p, ctl, 5)) { ok = false; break; }
+                const float* sw = scale_words + slot * S::kSlotWords;
+                float s = sw[lane_row];
+                if constexpr (!S::kCols) s *= sw[128 + col_base / 128];
+                const uint64_t s2 = ptx::pack2(s, s);
                 if (!wait_warp(&ctl->tmem_full[buf], bphase, p, ctl, 4)) { ok = false; break; }
                 ptx::tc_fence_after_sync();
                 const uint32_t t0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                                     static_cast<uint32_t>(buf * kTileN + col_base);
-                const float s = kCols ? ls : ls * cs[0];
-                const uint64_t s2 = ptx::pack2(s, s);
+                // one chunk is on its way from TMEM while the one before is folded in
+                uint32_t r[2][kChunk];
+                tmem_load(t0, r[0]);
 #pragma unroll
                 for (int j = 0; j < kChunks; ++j) {
-                    uint32_t r[kChunk];
-                    if constexpr (kChunk == 32) ptx::tmem_load_32cols(t0 + j * 32, r);
-                    else tmem_load_16cols(t0, r);
-                    if (j == kChunks - 1) {
+                    tmem_wait(r[j & 1]);
+                    if (j + 1 < kChunks) {
+                        tmem_load(t0 + (j + 1) * kChunk, r[(j + 1) & 1]);
+                    } else {
                         // the buffer is free for the next k-block's MMAs
                         ptx::tc_fence_before_sync();
                         __syncwarp();
                         if (lane == 0) {
                             if (kPair && !leader)
-                                ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(&ctl->tmem_empty[buf]), 0));
+                                arrive_at_leader(&ctl->tmem_empty[buf]);
                             else
                                 ptx::mbar_arrive(&ctl->tmem_empty[buf]);
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < kChunk / 4; ++i) {
-                        uint64_t t2[2] = {ptx::pack2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])),
-                                          ptx::pack2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]))};
-                        if constexpr (kCols) {
-                            const float4 c4 = *reinterpret_cast<const float4*>(my_cols + j * kChunk + 4 * i);
+                        const uint32_t(&q)[kChunk] = r[j & 1];
+                        uint64_t t2[2] = {ptx::pack2(__uint_as_float(q[4 * i]), __uint_as_float(q[4 * i + 1])),
+                                          ptx::pack2(__uint_as_float(q[4 * i + 2]), __uint_as_float(q[4 * i + 3]))};
+                        if constexpr (S::kCols) {
+                            const float4 c4 = *reinterpret_cast<const float4*>(sw + 128 + col_base + j * kChunk + 4 * i);
                             t2[0] = ptx::mul2(t2[0], ptx::pack2(c4.x, c4.y));
                             t2[1] = ptx::mul2(t2[1], ptx::pack2(c4.z, c4.w));
                         }
@@ -728,7 +793,10 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                         acc[a + 1] = ptx::fma2(t2[1], s2, acc[a + 1]);
                     }
                 }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&ctl->scale_empty[slot]);
                 if (++buf == S::kBufs) { buf = 0; bphase ^= 1u; }
+                if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
             }
             if constexpr (!kPair) {
                 // all promote warps leave together: the barriers below need every thread
@@ -803,7 +871,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                 const int warp_row = w.m0 + static_cast<int>(rank) * 128 + quad * 32;
                 const int rows_ok = min(32, w.m_end - warp_row);
                 if (rows_ok > 0) {
-                    const long long row = static_cast<long long>(w.d_row) + m_row;
+                    const long long row = static_cast<long long>(w.d_row) + warp_row + lane;
 #pragma unroll
                     for (int j = 0; j < kChunks; ++j) {
                         const int col0 = w.n0 + col_base + j * kChunk;
