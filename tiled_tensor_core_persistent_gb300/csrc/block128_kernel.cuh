@@ -147,22 +147,26 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
+#ifndef FOLD
+#define FOLD 3
+#endif
+#ifndef WAITS
+#define WAITS 1
+#endif
+#if FOLD == 3
+// (volatile, so that none moves ahead of the wait for its operand)
+__device__ __forceinline__ void fold(float& acc, uint32_t t, float s) {
+    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "r"(t), "f"(s));
 }
+#else
+__device__ __forceinline__ void fold2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s2) {
+    asm volatile("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s2));
+}
+#endif
 
 // 4-byte asynchronous copy global -> shared, and the arrival (one of the
 // barrier's expected ones) once this thread's copies so far have landed.
@@ -178,8 +182,8 @@ __device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_
 // warp has read (tcgen05.wait::ld returned the values to registers), no
 // memory, so it needs no release at cluster scope: with one, the fence in
 // front of it held each k-block up for over a thousand cycles (8192^3: 1064 us).
-__device__ __forceinline__ void arrive_at_leader(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(ptx::map_to_cta(ptx::smem_u32(bar), 0)) : "memory");
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // ------------------------------------------------------------------ schedule
@@ -294,59 +298,64 @@ __device__ __forceinline__ void decode_tile(const Params& p, const Groups& gr, i
 // worker; a tile whose iterations fall to several workers is finished by the
 // last of them (one such tile at most begins in any worker's run, so the
 // first worker's number also names its arrival counter).
+template <bool kMayStream>
 struct Walk {
+    int it, end, step;   // tiles
+    __device__ __forceinline__ Walk(const Params& p, const Groups& gr, int wid, int workers)
+        : it(wid), end(total_tiles(p, gr)), step(workers) {}
+    template <int kTileM, int kTileN>
+    __device__ __forceinline__ bool next(const Params& p, const Groups& gr, Piece& w) {
+        if (it >= end) return false;
+        decode_tile<kTileM, kTileN>(p, gr, it, w);
+        it += step;
+        return true;
+    }
+};
+template <>
+struct Walk<true> {
     long long it, end;   // stream: iterations; otherwise tiles
     long long total;
     int wid, workers;
-};
-
-__device__ __forceinline__ Walk walk_begin(const Params& p, const Groups& gr, int wid, int workers) {
-    Walk s;
-    const int tiles = total_tiles(p, gr);
-    s.workers = workers;
-    s.wid = wid;
-    if (p.stream) {
-        s.total = static_cast<long long>(tiles) * p.num_kb;
-        // never more workers than iterations, so that every worker of a tile holds a piece of it
-        if (s.total < s.workers) s.workers = static_cast<int>(s.total);
-        s.it = wid < s.workers ? wid * s.total / s.workers : 0;
-        s.end = wid < s.workers ? (wid + 1) * s.total / s.workers : 0;
-    } else {
-        s.total = tiles;
-        s.it = wid;
-        s.end = tiles;
+    __device__ __forceinline__ Walk(const Params& p, const Groups& gr, int wid_, int workers_) : wid(wid_), workers(workers_) {
+        const int tiles = total_tiles(p, gr);
+        if (p.stream) {
+            total = static_cast<long long>(tiles) * p.num_kb;
+            // never more workers than iterations, so that every worker of a tile holds a piece of it
+            if (total < workers) workers = static_cast<int>(total);
+            it = wid < workers ? wid * total / workers : 0;
+            end = wid < workers ? (wid + 1) * total / workers : 0;
+        } else {
+            total = tiles;
+            it = wid;
+            end = tiles;
+        }
     }
-    return s;
-}
-
-__device__ __forceinline__ int worker_of(const Walk& s, long long i) {
-    return static_cast<int>(((i + 1) * s.workers - 1) / s.total);
-}
-
-template <int kTileM, int kTileN>
-__device__ __forceinline__ bool walk_next(const Params& p, const Groups& gr, Walk& s, Piece& w) {
-    if (s.it >= s.end) return false;
-    if (!p.stream) {
-        decode_tile<kTileM, kTileN>(p, gr, static_cast<int>(s.it), w);
-        s.it += s.workers;
+    __device__ __forceinline__ int worker_of(long long i) const { return static_cast<int>(((i + 1) * workers - 1) / total); }
+    template <int kTileM, int kTileN>
+    __device__ __forceinline__ bool next(const Params& p, const Groups& gr, Piece& w) {
+        if (it >= end) return false;
+        if (!p.stream) {
+            decode_tile<kTileM, kTileN>(p, gr, static_cast<int>(it), w);
+            it += workers;
+            return true;
+        }
+        const int t = static_cast<int>(it / p.num_kb);
+        const long long t0 = static_cast<long long>(t) * p.num_kb;
+        decode_tile<kTileM, kTileN>(p, gr, t, w);
+        w.kb0 = static_cast<int>(it - t0);
+        const long long left = end - t0;
+        w.kb1 = left < p.num_kb ? static_cast<int>(left) : p.num_kb;
+        w.first = worker_of(t0);
+        w.nsplit = worker_of(t0 + p.num_kb - 1) - w.first + 1;
+        w.split = wid - w.first;
+        it = t0 + w.kb1;
         return true;
     }
-    const int t = static_cast<int>(s.it / p.num_kb);
-    const long long t0 = static_cast<long long>(t) * p.num_kb;
-    decode_tile<kTileM, kTileN>(p, gr, t, w);
-    w.kb0 = static_cast<int>(s.it - t0);
-    const long long left = s.end - t0;
-    w.kb1 = left < p.num_kb ? static_cast<int>(left) : p.num_kb;
-    w.first = worker_of(s, t0);
-    w.nsplit = worker_of(s, t0 + p.num_kb - 1) - w.first + 1;
-    w.split = s.wid - w.first;
-    s.it = t0 + w.kb1;
-    return true;
-}
+};
 
 // Partial slot of piece q of a shared tile: a worker's run holds the end of
 // at most one shared tile (slot 1) and the beginning of at most one (slot 0).
-__device__ __forceinline__ int slot_of(const Params& p, const Walk& s, const Piece& w, int q) {
+__device__ __forceinline__ int slot_of(const Params& p, const Walk<true>& s, const Piece& w, int q) {
     const int c = w.first + q;
     const bool begins = c * s.total / s.workers >= static_cast<long long>(w.tile) * p.num_kb;
     return 2 * c + (begins ? 0 : 1);
@@ -541,6 +550,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
     const int lane = threadIdx.x & 31;
     const uint32_t rank = kPair ? ptx::cluster_ctarank() : 0u;
     const bool leader = rank == 0;
+    using WalkT = Walk<!kPair>;
     const int wid = kPair ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
     const int workers = kPair ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
 
@@ -579,13 +589,12 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
     ptx::tc_fence_after_sync();
     const uint32_t tmem_base = ctl->tmem_base;
 
-    Walk walk = walk_begin(p, gr, wid, workers);
-    Piece w;
-
     if (warp < S::kControlWarps) {
         if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kControlRegs));
         if (warp == 0) {
         // ------------------------------------------------------ TMA producer
+        WalkT walk(p, gr, wid, workers);
+        Piece w;
         const bool issuer = lane == 0;
         if (issuer && p.num_kb > 0) {
             ptx::prefetch_tensormap(&p.tmA);
@@ -594,7 +603,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         int stage = 0;
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         bool first = true, ok = true;
-        while (ok && walk_next<S::kTileM, S::kTileNOut>(p, gr, walk, w)) {
+        while (ok && walk.template next<S::kTileM, S::kTileNOut>(p, gr, w)) {
             const int a_row = w.m0 + (kPair ? static_cast<int>(rank) * 128 : 0);
             const int b_row = w.b_row + (kPair ? static_cast<int>(rank) * S::kColRows : 0);
             for (int kb = w.kb0; kb < w.kb1; kb += kAtoms) {
@@ -642,6 +651,8 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         } else if (warp == 1 && leader) {
         // ------------------------------------------------------- MMA issuer
         {
+        WalkT walk(p, gr, wid, workers);
+        Piece w;
             const bool issuer = lane == 0;
             const uint32_t idesc = (1u << 4) | (p.ab_fmt << 7) | (p.ab_fmt << 10) |
                                    (static_cast<uint32_t>(kTileN >> 3) << 17) |
@@ -649,7 +660,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true, issued = false;
-            while (ok && walk_next<S::kTileM, S::kTileNOut>(p, gr, walk, w)) {
+            while (ok && walk.template next<S::kTileM, S::kTileNOut>(p, gr, w)) {
                 for (int kb = w.kb0; kb < w.kb1; kb += kAtoms) {
                     if (!wait_warp(&ctl->full[stage], phase, p, ctl, 3)) { ok = false; break; }
                     const int atoms = min(kAtoms, w.kb1 - kb);
@@ -694,6 +705,8 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         }
         } else if (warp == 2) {
         // ---------------------------------------------------- scales, ahead
+        WalkT walk(p, gr, wid, workers);
+        Piece w;
         const ScaleRef& sl = kSwap ? p.sb : p.sa;
         const ScaleRef& sc = kSwap ? p.sa : p.sb;
         constexpr int kColLoads = S::kCols ? (kTileN + 31) / 32 : 1;
@@ -701,7 +714,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
-        while (ok && walk_next<S::kTileM, S::kTileNOut>(p, gr, walk, w)) {
+        while (ok && walk.template next<S::kTileM, S::kTileNOut>(p, gr, w)) {
             const int l0 = kSwap ? w.n0 : w.m0 + static_cast<int>(rank) * 128;
             const int c0 = kSwap ? w.m0 : w.n0;
             const float* lp[4];
@@ -733,6 +746,8 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
     } else {
         // ------------------------------------------------ promote and store
         if constexpr (S::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kPromoteRegs));
+        WalkT walk(p, gr, wid, workers);
+        Piece w;
         const int pw = warp - S::kControlWarps;
         const int quad = warp & 3;               // the TMEM lanes this warp may read
         const int col_base = kSwap ? 0 : (pw >> 2) * S::kWarpCols;
@@ -744,18 +759,28 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         uint32_t bphase = 0, sphase = 0;
         bool ok = true;
         const int bar_threads = 32 * S::kPromoteWarps;
+        // the barriers this warp arrives on: the leader's TMEM buffers, its own CTA's scale slots
+        const uint32_t empty_addr = kPair ? ptx::map_to_cta(ptx::smem_u32(&ctl->tmem_empty[0]), 0) : ptx::smem_u32(&ctl->tmem_empty[0]);
+        const uint32_t scale_addr = kPair ? ptx::map_to_cta(ptx::smem_u32(&ctl->scale_empty[0]), rank) : ptx::smem_u32(&ctl->scale_empty[0]);
         const int lane_row = quad * 32 + lane;   // this thread's row of the lane operand's tile
-        while (ok && walk_next<S::kTileM, S::kTileNOut>(p, gr, walk, w)) {
-            uint64_t acc[WC / 2];
+        while (ok && walk.template next<S::kTileM, S::kTileNOut>(p, gr, w)) {
+            float acc[WC];
 #pragma unroll
-            for (int i = 0; i < WC / 2; ++i) acc[i] = 0;
+            for (int i = 0; i < WC; ++i) acc[i] = 0.0f;
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                if (!wait_warp(&ctl->scale_full[slot], sphase, p, ctl, 5)) { ok = false; break; }
+                // both barriers are asked before either answer is needed
+                const bool have_s = ptx::mbar_try_wait(ptx::smem_u32(&ctl->scale_full[slot]), sphase);
+                const bool have_t = ptx::mbar_try_wait(ptx::smem_u32(&ctl->tmem_full[buf]), bphase);
+                if (!__all_sync(0xffffffffu, have_s && have_t)) {
+                    if (!wait_warp(&ctl->scale_full[slot], sphase, p, ctl, 5) ||
+                        !wait_warp(&ctl->tmem_full[buf], bphase, p, ctl, 4)) {
+                        ok = false;
+                        break;
+                    }
+                }
                 const float* sw = scale_words + slot * S::kSlotWords;
                 float s = sw[lane_row];
                 if constexpr (!S::kCols) s *= sw[128 + col_base / 128];
-                const uint64_t s2 = ptx::pack2(s, s);
-                if (!wait_warp(&ctl->tmem_full[buf], bphase, p, ctl, 4)) { ok = false; break; }
                 ptx::tc_fence_after_sync();
                 const uint32_t t0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                                     static_cast<uint32_t>(buf * kTileN + col_base);
@@ -768,33 +793,33 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                     if (j + 1 < kChunks) {
                         tmem_load(t0 + (j + 1) * kChunk, r[(j + 1) & 1]);
                     } else {
-                        // the buffer is free for the next k-block's MMAs
+                        // the buffer is free for the next k-block's MMAs (and the
+                        // scales, which this thread holds unless every column has one)
                         ptx::tc_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) {
-                            if (kPair && !leader)
-                                arrive_at_leader(&ctl->tmem_empty[buf]);
-                            else
-                                ptx::mbar_arrive(&ctl->tmem_empty[buf]);
-                        }
+                        if (lane < (S::kCols ? 1 : 2))
+                            arrive_cluster(lane == 0 ? empty_addr + 8 * buf : scale_addr + 8 * slot);
                     }
 #pragma unroll
                     for (int i = 0; i < kChunk / 4; ++i) {
                         const uint32_t(&q)[kChunk] = r[j & 1];
-                        uint64_t t2[2] = {ptx::pack2(__uint_as_float(q[4 * i]), __uint_as_float(q[4 * i + 1])),
-                                          ptx::pack2(__uint_as_float(q[4 * i + 2]), __uint_as_float(q[4 * i + 3]))};
+                        float* a = acc + j * kChunk + 4 * i;
                         if constexpr (S::kCols) {
                             const float4 c4 = *reinterpret_cast<const float4*>(sw + 128 + col_base + j * kChunk + 4 * i);
-                            t2[0] = ptx::mul2(t2[0], ptx::pack2(c4.x, c4.y));
-                            t2[1] = ptx::mul2(t2[1], ptx::pack2(c4.z, c4.w));
+                            fold(a[0], q[4 * i], s * c4.x);
+                            fold(a[1], q[4 * i + 1], s * c4.y);
+                            fold(a[2], q[4 * i + 2], s * c4.z);
+                            fold(a[3], q[4 * i + 3], s * c4.w);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) fold(a[k], q[4 * i + k], s);
                         }
-                        const int a = (j * kChunk + 4 * i) / 2;
-                        acc[a] = ptx::fma2(t2[0], s2, acc[a]);
-                        acc[a + 1] = ptx::fma2(t2[1], s2, acc[a + 1]);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&ctl->scale_empty[slot]);
+                if constexpr (S::kCols) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&ctl->scale_empty[slot]);
+                }
                 if (++buf == S::kBufs) { buf = 0; bphase ^= 1u; }
                 if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
             }
@@ -814,12 +839,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                     float* mine = p.partials + static_cast<size_t>(slot_of(p, walk, w, w.split)) * (128 * kTileN) +
                                   static_cast<size_t>(col_base) * 128 + lane_row;
 #pragma unroll
-                    for (int i = 0; i < WC / 2; ++i) {
-                        float x, y;
-                        ptx::unpack2(acc[i], x, y);
-                        mine[(2 * i) * 128] = x;
-                        mine[(2 * i + 1) * 128] = y;
-                    }
+                    for (int i = 0; i < WC; ++i) mine[i * 128] = acc[i];
                     ptx::named_barrier_sync(1, bar_threads);
                     if (threadIdx.x == 32 * S::kControlWarps) {
                         const int old = ptx::atomic_add_acq_rel_gpu(p.counters + w.first, 1);
@@ -831,13 +851,12 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                     if (finish) {
                         // in the order of the pieces, whoever finishes: the sum is the same every time
 #pragma unroll
-                        for (int i = 0; i < WC / 2; ++i) acc[i] = 0;
+                        for (int i = 0; i < WC; ++i) acc[i] = 0.0f;
                         for (int q = 0; q < w.nsplit; ++q) {
                             const float* src = p.partials + static_cast<size_t>(slot_of(p, walk, w, q)) * (128 * kTileN) +
                                                static_cast<size_t>(col_base) * 128 + lane_row;
 #pragma unroll
-                            for (int i = 0; i < WC / 2; ++i)
-                                acc[i] = ptx::add2(acc[i], ptx::pack2(__ldcg(src + (2 * i) * 128), __ldcg(src + (2 * i + 1) * 128)));
+                            for (int i = 0; i < WC; ++i) acc[i] += __ldcg(src + i * 128);
                         }
                     }
                     // (ctl->last is not written again before every thread has passed this piece's
@@ -854,9 +873,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                     const float bv = p.bias ? load_elem(p.bias, p.bias_f32, n) : 0.0f;
 #pragma unroll
                     for (int i = 0; i < WC; ++i) {
-                        float x, y;
-                        ptx::unpack2(acc[i / 2], x, y);
-                        float v = (i & 1) ? y : x;
+                        float v = acc[i];
                         const int m = w.m0 + i;
                         if (m < w.m_end) {
                             const long long row = static_cast<long long>(w.d_row) + m;
@@ -878,7 +895,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                         if (col0 < p.N) {
                             float v[kChunk];
 #pragma unroll
-                            for (int i = 0; i < kChunk / 2; ++i) ptx::unpack2(acc[j * kChunk / 2 + i], v[2 * i], v[2 * i + 1]);
+                            for (int i = 0; i < kChunk; ++i) v[i] = acc[j * kChunk + i];
                             finish_values<kChunk>(p, v, row, col0, lane < rows_ok);
                             store_values<kChunk>(p, v, row, col0, rows_ok, lane, my_words);
                         }
