@@ -90,16 +90,19 @@ struct alignas(16) Ctl {
     int last;
 };
 
+// (the clock is read once every 64 tries: reading it takes longer than most waits)
 __device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, const Params& p, Ctl* ctl, int where,
                                      bool honor_abort) {
     const uint32_t a = ptx::smem_u32(bar);
-    const uint64_t t0 = ptx::globaltimer_ns();
+    uint64_t t0 = 0;
     uint32_t n = 0;
     while (true) {
         if (ptx::mbar_try_wait(a, parity)) return true;
-        if ((++n & 31u) == 0) {
+        if ((++n & 63u) == 0) {
             if (honor_abort && *reinterpret_cast<volatile int*>(&ctl->abort_flag)) return false;
-            if (static_cast<long long>(ptx::globaltimer_ns() - t0) > p.timeout_ns) {
+            const uint64_t now = ptx::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (static_cast<long long>(now - t0) > p.timeout_ns) {
                 *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
                 if (atomicCAS(p.status, 0, kStatusTimeout) == 0) {
                     p.status[1] = where;
@@ -111,16 +114,18 @@ __device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, const Param
     }
 }
 
-static __device__ __forceinline__ bool spin_slow(uint64_t* bar, uint32_t parity, const Params& p, Ctl* ctl, int where,
-                                              bool honor_abort) {
-    return spin(bar, parity, p, ctl, where, honor_abort);
+// Every lane waits by itself (the MMA warp, where only lane 0 issues: without
+// the vote below a wait that is over costs it half as much).
+__device__ __forceinline__ bool wait_lanes(uint64_t* bar, uint32_t parity, const Params& p, Ctl* ctl, int where) {
+    if (ptx::mbar_try_wait(ptx::smem_u32(bar), parity)) return true;
+    return spin(bar, parity, p, ctl, where, true);
 }
 
 // The whole warp waits, then agrees on the outcome.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const Params& p, Ctl* ctl, int where,
                                           bool honor_abort = true) {
     bool ok = ptx::mbar_try_wait(ptx::smem_u32(bar), parity);
-    if (!ok) ok = spin_slow(bar, parity, p, ctl, where, honor_abort);
+    if (!ok) ok = spin(bar, parity, p, ctl, where, honor_abort);
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -167,6 +172,47 @@ __device__ __forceinline__ void fold2(uint64_t& acc, uint32_t lo, uint32_t hi, u
     asm volatile("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s2));
 }
 #endif
+
+// The four K = 32 MMAs of one k-block into fresh accumulator columns, and the
+// arrival on `full` (of both CTAs of a pair) when they have ended.  One block
+// of instructions, operand descriptors as 32-bit halves: the issuing thread
+// spends 390 cycles here of the 512 that the MMAs of a pair tile take, and
+// everything else it does per k-block has to fit into the rest.
+template <bool kPair>
+__device__ __forceinline__ void mma_kblock(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                           uint64_t* full) {
+    if constexpr (kPair) {
+        asm volatile(
+            "{\n\t.reg .pred z, o;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t.reg .b16 m;\n\t"
+            "setp.ne.b32 z, 0, 0;\n\tsetp.eq.b32 o, 0, 0;\n\tmov.b16 m, 3;\n\t"
+            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %4, z;\n\t"
+            "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %4, o;\n\t"
+            "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %4, o;\n\t"
+            "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %4, o;\n\t"
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], m;\n\t}" ::"r"(d_tmem),
+            "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(ptx::smem_u32(full))
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred z, o;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+            "setp.ne.b32 z, 0, 0;\n\tsetp.eq.b32 o, 0, 0;\n\t"
+            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, z;\n\t"
+            "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, o;\n\t"
+            "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, o;\n\t"
+            "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, o;\n\t"
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d_tmem),
+            "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(ptx::smem_u32(full))
+            : "memory");
+    }
+}
 
 // 4-byte asynchronous copy global -> shared, and the arrival (one of the
 // barrier's expected ones) once this thread's copies so far have landed.
@@ -657,43 +703,33 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
             const uint32_t idesc = (1u << 4) | (p.ab_fmt << 7) | (p.ab_fmt << 10) |
                                    (static_cast<uint32_t>(kTileN >> 3) << 17) |
                                    (static_cast<uint32_t>((kPair ? 256 : 128) >> 4) << 24);
+            // descriptor halves: 128-byte swizzle, 8-row groups 1024 bytes apart
+            constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+            const uint32_t desc0 = (ptx::smem_u32(smem) >> 4) | (1u << 16);
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true, issued = false;
             while (ok && walk.template next<S::kTileM, S::kTileNOut>(p, gr, w)) {
                 for (int kb = w.kb0; kb < w.kb1; kb += kAtoms) {
-                    if (!wait_warp(&ctl->full[stage], phase, p, ctl, 3)) { ok = false; break; }
-                    const int atoms = min(kAtoms, w.kb1 - kb);
-                    for (int at = 0; at < atoms; ++at) {
-                        if (!wait_warp(&ctl->tmem_empty[buf], bphase ^ 1u, p, ctl, 2)) { ok = false; break; }
+                    if (!wait_lanes(&ctl->full[stage], phase, p, ctl, 3)) { ok = false; break; }
+#pragma unroll
+                    for (int at = 0; at < kAtoms; ++at) {
+                        if (kb + at >= w.kb1) break;
+                        if (!wait_lanes(&ctl->tmem_empty[buf], bphase ^ 1u, p, ctl, 2)) { ok = false; break; }
                         ptx::tc_fence_after_sync();
                         if (issuer) {
-                            const uint32_t sl = ptx::smem_u32(smem + stage * S::kStageBytes + at * S::kAtomBytes);
-                            const uint64_t da = ptx::smem_desc_sw128(sl, 16, 1024);
-                            const uint64_t db = ptx::smem_desc_sw128(sl + S::kLaneRows * kBlock, 16, 1024);
-                            const uint32_t dt = tmem_base + static_cast<uint32_t>(buf * kTileN);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint64_t off = static_cast<uint64_t>(k * 32) >> 4;
-                                if constexpr (kPair) ptx::mma_f8_pair(dt, da + off, db + off, idesc, k > 0);
-                                else ptx::mma_f8(dt, da + off, db + off, idesc, k > 0);
-                            }
-                            if constexpr (kPair) ptx::mma_commit_pair(&ctl->tmem_full[buf], 0x3);
-                            else ptx::mma_commit(&ctl->tmem_full[buf]);
+                            const uint32_t a_lo = desc0 + static_cast<uint32_t>(stage * S::kStageBytes + at * S::kAtomBytes) / 16;
+                            mma_kblock<kPair>(tmem_base + static_cast<uint32_t>(buf * kTileN), a_lo,
+                                              a_lo + S::kLaneRows * kBlock / 16, kDescHi, idesc, &ctl->tmem_full[buf]);
                         }
-                        __syncwarp();
                         issued = true;
                         if (++buf == S::kBufs) { buf = 0; bphase ^= 1u; }
                     }
                     if (!ok) break;
-                    if (issuer) {
-                        if constexpr (kPair) ptx::mma_commit_pair(&ctl->empty[stage], 0x3);
-                        else ptx::mma_commit(&ctl->empty[stage]);
-                    }
-                    __syncwarp();
                     if (++stage == stages) { stage = 0; phase ^= 1u; }
                 }
             }
+            __syncwarp();
             if (issued) {   // every MMA has ended before the TMEM is freed
                 if (issuer) {
                     if constexpr (kPair) ptx::mma_commit_pair(&ctl->drain, 0x1);
@@ -755,7 +791,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         constexpr int kChunk = WC < 32 ? WC : 32;
         constexpr int kChunks = WC / kChunk;
         uint32_t* my_words = warp_words + pw * S::kWarpWords;
-        int buf = 0, slot = 0;
+        int buf = 0, slot = 0, stage = 0;
         uint32_t bphase = 0, sphase = 0;
         bool ok = true;
         const int bar_threads = 32 * S::kPromoteWarps;
@@ -777,6 +813,13 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                         ok = false;
                         break;
                     }
+                }
+                // The k-block's MMAs have ended, so the stage is free once that was
+                // its last one.  (The first promote warp says so: a second
+                // tcgen05.commit per stage held the MMA warp up for 380 cycles.)
+                if (((kb - w.kb0) % kAtoms) == kAtoms - 1 || kb + 1 == w.kb1) {
+                    if (pw == 0 && lane == 0) ptx::mbar_arrive(&ctl->empty[stage]);
+                    if (++stage == stages) stage = 0;
                 }
                 const float* sw = scale_words + slot * S::kSlotWords;
                 float s = sw[lane_row];
