@@ -114,11 +114,27 @@ __device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, const Param
     }
 }
 
-// Every lane waits by itself (the MMA warp, where only lane 0 issues: without
-// the vote below a wait that is over costs it half as much).
-__device__ __forceinline__ bool wait_lanes(uint64_t* bar, uint32_t parity, const Params& p, Ctl* ctl, int where) {
-    if (ptx::mbar_try_wait(ptx::smem_u32(bar), parity)) return true;
-    return spin(bar, parity, p, ctl, where, true);
+// Two barriers in one question: the even lanes ask about the first, the odd
+// ones about the second.
+__device__ __forceinline__ bool wait_pair(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1, int lane,
+                                          const Params& p, Ctl* ctl, int where) {
+    const bool odd = lane & 1;
+    const uint32_t a = ptx::smem_u32(odd ? bar1 : bar0), parity = odd ? parity1 : parity0;
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(a, parity))) return true;
+    return __all_sync(0xffffffffu, spin(odd ? bar1 : bar0, parity, p, ctl, where, true));
+}
+
+// One lane of the converged warp, chosen by the hardware: the compiler knows
+// that a single thread runs what follows and keeps the MMA's operands in
+// uniform registers (issuing a k-block takes 200 cycles; 390 with `lane == 0`).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "elect.sync _|P, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, P;\n\t}"
+        : "=r"(r));
+    return r != 0;
 }
 
 // The whole warp waits, then agrees on the outcome.
@@ -552,7 +568,7 @@ struct Shape {
     // (128 * 72 + 256 * 216 = 384 * 168, what the block is launched with).
     static constexpr int kControlWarps = 4;
     static constexpr bool kSplitRegs = !kSwap;
-    static constexpr int kControlRegs = 72, kPromoteRegs = 216, kLaunchRegs = 168;
+    static constexpr int kControlRegs = 56, kPromoteRegs = 224, kLaunchRegs = 168;
     static constexpr int kThreads = 32 * (kControlWarps + kPromoteWarps);
     static_assert(!kSplitRegs || 32 * (kControlWarps * kControlRegs + kPromoteWarps * kPromoteRegs) <= kThreads * kLaunchRegs,
                   "the shares add up to the launch's registers");
@@ -699,7 +715,6 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         {
         WalkT walk(p, gr, wid, workers);
         Piece w;
-            const bool issuer = lane == 0;
             const uint32_t idesc = (1u << 4) | (p.ab_fmt << 7) | (p.ab_fmt << 10) |
                                    (static_cast<uint32_t>(kTileN >> 3) << 17) |
                                    (static_cast<uint32_t>((kPair ? 256 : 128) >> 4) << 24);
@@ -711,16 +726,21 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
             bool ok = true, issued = false;
             while (ok && walk.template next<S::kTileM, S::kTileNOut>(p, gr, w)) {
                 for (int kb = w.kb0; kb < w.kb1; kb += kAtoms) {
-                    if (!wait_lanes(&ctl->full[stage], phase, p, ctl, 3)) { ok = false; break; }
 #pragma unroll
                     for (int at = 0; at < kAtoms; ++at) {
                         if (kb + at >= w.kb1) break;
-                        if (!wait_lanes(&ctl->tmem_empty[buf], bphase ^ 1u, p, ctl, 2)) { ok = false; break; }
+                        ok = at == 0 ? wait_pair(&ctl->full[stage], phase, &ctl->tmem_empty[buf], bphase ^ 1u, lane, p, ctl, 3)
+                                     : wait_warp(&ctl->tmem_empty[buf], bphase ^ 1u, p, ctl, 2);
+                        if (!ok) break;
                         ptx::tc_fence_after_sync();
-                        if (issuer) {
+                        if (elect_one()) {
                             const uint32_t a_lo = desc0 + static_cast<uint32_t>(stage * S::kStageBytes + at * S::kAtomBytes) / 16;
                             mma_kblock<kPair>(tmem_base + static_cast<uint32_t>(buf * kTileN), a_lo,
                                               a_lo + S::kLaneRows * kBlock / 16, kDescHi, idesc, &ctl->tmem_full[buf]);
+                            if (at == kAtoms - 1 || kb + at + 1 == w.kb1) {   // the stage's last k-block
+                                if constexpr (kPair) ptx::mma_commit_pair(&ctl->empty[stage], 0x3);
+                                else ptx::mma_commit(&ctl->empty[stage]);
+                            }
                         }
                         issued = true;
                         if (++buf == S::kBufs) { buf = 0; bphase ^= 1u; }
@@ -731,7 +751,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
             }
             __syncwarp();
             if (issued) {   // every MMA has ended before the TMEM is freed
-                if (issuer) {
+                if (elect_one()) {
                     if constexpr (kPair) ptx::mma_commit_pair(&ctl->drain, 0x1);
                     else ptx::mma_commit(&ctl->drain);
                 }
@@ -788,10 +808,13 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         const int quad = warp & 3;               // the TMEM lanes this warp may read
         const int col_base = kSwap ? 0 : (pw >> 2) * S::kWarpCols;
         constexpr int WC = S::kWarpCols;
-        constexpr int kChunk = WC < 32 ? WC : 32;
+        // (16 on a pair tile: with two chunks of 32 next to 128 sums the compiler
+        // spills in the loop, and with next to no L1 left a reload comes from L2)
+        constexpr int kChunk = WC < 32 ? WC : (kPair ? 16 : 32);
         constexpr int kChunks = WC / kChunk;
+        constexpr int kOut = WC < 32 ? WC : 32;   // columns stored at a time
         uint32_t* my_words = warp_words + pw * S::kWarpWords;
-        int buf = 0, slot = 0, stage = 0;
+        int buf = 0, slot = 0;
         uint32_t bphase = 0, sphase = 0;
         bool ok = true;
         const int bar_threads = 32 * S::kPromoteWarps;
@@ -803,33 +826,36 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
             float acc[WC];
 #pragma unroll
             for (int i = 0; i < WC; ++i) acc[i] = 0.0f;
-            for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                // both barriers are asked before either answer is needed
-                const bool have_s = ptx::mbar_try_wait(ptx::smem_u32(&ctl->scale_full[slot]), sphase);
-                const bool have_t = ptx::mbar_try_wait(ptx::smem_u32(&ctl->tmem_full[buf]), bphase);
-                if (!__all_sync(0xffffffffu, have_s && have_t)) {
-                    if (!wait_warp(&ctl->scale_full[slot], sphase, p, ctl, 5) ||
-                        !wait_warp(&ctl->tmem_full[buf], bphase, p, ctl, 4)) {
-                        ok = false;
-                        break;
-                    }
+            float l_next = 0.0f, c_next = 0.0f;
+            auto read_scale = [&](int sl) {
+                const float* sw = scale_words + sl * S::kSlotWords;
+                l_next = sw[lane_row];
+                if constexpr (!S::kCols) c_next = sw[128 + col_base / 128];
+            };
+            if (w.kb0 < w.kb1) {
+                ok = wait_warp(&ctl->scale_full[slot], sphase, p, ctl, 5);
+                if (ok) read_scale(slot);
+            }
+            for (int kb = w.kb0; ok && kb < w.kb1; ++kb) {
+                // The k-block's sums, and with them the next one's scales: those are
+                // there long before, and read a whole k-block ahead of their use.
+                const int nslot = slot + 1 == kScaleSlots ? 0 : slot + 1;
+                const uint32_t nphase = sphase ^ (nslot == 0 ? 1u : 0u);
+                const bool more = kb + 1 < w.kb1;
+                if (!wait_pair(&ctl->tmem_full[buf], bphase, more ? &ctl->scale_full[nslot] : &ctl->tmem_full[buf],
+                               more ? nphase : bphase, lane, p, ctl, 4)) {
+                    ok = false;
+                    break;
                 }
-                // The k-block's MMAs have ended, so the stage is free once that was
-                // its last one.  (The first promote warp says so: a second
-                // tcgen05.commit per stage held the MMA warp up for 380 cycles.)
-                if (((kb - w.kb0) % kAtoms) == kAtoms - 1 || kb + 1 == w.kb1) {
-                    if (pw == 0 && lane == 0) ptx::mbar_arrive(&ctl->empty[stage]);
-                    if (++stage == stages) stage = 0;
-                }
-                const float* sw = scale_words + slot * S::kSlotWords;
-                float s = sw[lane_row];
-                if constexpr (!S::kCols) s *= sw[128 + col_base / 128];
                 ptx::tc_fence_after_sync();
                 const uint32_t t0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                                     static_cast<uint32_t>(buf * kTileN + col_base);
                 // one chunk is on its way from TMEM while the one before is folded in
                 uint32_t r[2][kChunk];
                 tmem_load(t0, r[0]);
+                const float* sw = scale_words + slot * S::kSlotWords;
+                const float s = S::kCols ? l_next : l_next * c_next;
+                if (more) read_scale(nslot);
 #pragma unroll
                 for (int j = 0; j < kChunks; ++j) {
                     tmem_wait(r[j & 1]);
@@ -864,7 +890,8 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                     if (lane == 0) ptx::mbar_arrive(&ctl->scale_empty[slot]);
                 }
                 if (++buf == S::kBufs) { buf = 0; bphase ^= 1u; }
-                if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
+                slot = nslot;
+                sphase = nphase;
             }
             if constexpr (!kPair) {
                 // all promote warps leave together: the barriers below need every thread
@@ -933,14 +960,14 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                 if (rows_ok > 0) {
                     const long long row = static_cast<long long>(w.d_row) + warp_row + lane;
 #pragma unroll
-                    for (int j = 0; j < kChunks; ++j) {
-                        const int col0 = w.n0 + col_base + j * kChunk;
+                    for (int j = 0; j < WC / kOut; ++j) {
+                        const int col0 = w.n0 + col_base + j * kOut;
                         if (col0 < p.N) {
-                            float v[kChunk];
+                            float v[kOut];
 #pragma unroll
-                            for (int i = 0; i < kChunk; ++i) v[i] = acc[j * kChunk + i];
-                            finish_values<kChunk>(p, v, row, col0, lane < rows_ok);
-                            store_values<kChunk>(p, v, row, col0, rows_ok, lane, my_words);
+                            for (int i = 0; i < kOut; ++i) v[i] = acc[j * kOut + i];
+                            finish_values<kOut>(p, v, row, col0, lane < rows_ok);
+                            store_values<kOut>(p, v, row, col0, rows_ok, lane, my_words);
                         }
                     }
                 }
