@@ -435,9 +435,11 @@ __device__ __forceinline__ float load_elem(const void* base, int is_f32, long lo
     return is_f32 ? static_cast<const float*>(base)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(base)[i]);
 }
 
-// beta C + bias, activation, on CN (16 or 32) consecutive columns of one row
+// beta C + bias (the columns' values in shared memory), activation, on CN (16
+// or 32) consecutive columns of one row
 template <int CN>
-__device__ __forceinline__ void finish_values(const Params& p, float (&v)[CN], long long row, int col0, bool row_ok) {
+__device__ __forceinline__ void finish_values(const Params& p, float (&v)[CN], long long row, int col0, bool row_ok,
+                                              const float* bias) {
     if (p.beta != 0.0f && row_ok) {
         const long long at = row * p.ldc + col0;
         if (p.c_vec && col0 + CN <= p.N) {
@@ -472,8 +474,13 @@ __device__ __forceinline__ void finish_values(const Params& p, float (&v)[CN], l
     }
     if (p.bias) {
 #pragma unroll
-        for (int i = 0; i < CN; ++i)
-            if (col0 + i < p.N) v[i] += load_elem(p.bias, p.bias_f32, col0 + i);
+        for (int i = 0; i < CN / 4; ++i) {
+            const float4 b = reinterpret_cast<const float4*>(bias)[i];
+            v[4 * i] += b.x;
+            v[4 * i + 1] += b.y;
+            v[4 * i + 2] += b.z;
+            v[4 * i + 3] += b.w;
+        }
     }
     if (p.act == 2) {
 #pragma unroll
@@ -579,7 +586,8 @@ struct Shape {
     static constexpr int kBufs = kPair ? 2 : 4;
     static constexpr int kTmemCols = kBufs * kTileN < 32 ? 32 : kBufs * kTileN;
     static constexpr int kWarpCols = kSwap ? kTileN : kTileN / 2;  // MMA columns of one promote warp
-    static constexpr int kWarpWords = kSwap ? 0 : kStageWords;     // store stage of one promote warp
+    // store stage and bias of one promote warp
+    static constexpr int kWarpWords = kSwap ? 0 : kStageWords + kWarpCols;
     // scales of one k-block: a word per lane row, then one per MMA column (or
     // per 128 columns)
     static constexpr bool kCols = kColScale || kSwap;
@@ -814,6 +822,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         constexpr int kChunks = WC / kChunk;
         constexpr int kOut = WC < 32 ? WC : 32;   // columns stored at a time
         uint32_t* my_words = warp_words + pw * S::kWarpWords;
+        float* bias_cols = reinterpret_cast<float*>(my_words + kStageWords);
         int buf = 0, slot = 0;
         uint32_t bphase = 0, sphase = 0;
         bool ok = true;
@@ -823,6 +832,27 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         const uint32_t scale_addr = kPair ? ptx::map_to_cta(ptx::smem_u32(&ctl->scale_empty[0]), rank) : ptx::smem_u32(&ctl->scale_empty[0]);
         const int lane_row = quad * 32 + lane;   // this thread's row of the lane operand's tile
         while (ok && walk.template next<S::kTileM, S::kTileNOut>(p, gr, w)) {
+            if constexpr (!kSwap) {
+                // The epilogue's operands set out while the tile is computed: the
+                // bias of this warp's columns to shared memory, this thread's row
+                // of C to L2.
+                if (p.bias) {
+                    __syncwarp();   // (the last tile's readers are done)
+#pragma unroll
+                    for (int i = 0; i < WC / 32; ++i) {
+                        const int n = w.n0 + col_base + lane + 32 * i;
+                        bias_cols[lane + 32 * i] = n < p.N ? load_elem(p.bias, p.bias_f32, n) : 0.0f;
+                    }
+                }
+                const int row = w.m0 + static_cast<int>(rank) * 128 + lane_row;
+                if (p.beta != 0.0f && row < w.m_end) {
+                    const long long at = (static_cast<long long>(w.d_row) + row) * p.ldc + w.n0 + col_base;
+                    const int size = p.c_f32 ? 4 : 2;
+                    const char* c = static_cast<const char*>(p.C) + at * size;
+                    const char* end = c + min(WC, p.N - w.n0 - col_base) * size;
+                    for (; c < end; c += 128) ptx::prefetch_l2(c);
+                }
+            }
             float acc[WC];
 #pragma unroll
             for (int i = 0; i < WC; ++i) acc[i] = 0.0f;
@@ -875,10 +905,13 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                         float* a = acc + j * kChunk + 4 * i;
                         if constexpr (S::kCols) {
                             const float4 c4 = *reinterpret_cast<const float4*>(sw + 128 + col_base + j * kChunk + 4 * i);
-                            fold(a[0], q[4 * i], s * c4.x);
-                            fold(a[1], q[4 * i + 1], s * c4.y);
-                            fold(a[2], q[4 * i + 2], s * c4.z);
-                            fold(a[3], q[4 * i + 3], s * c4.w);
+                            float s0, s1, s2, s3;   // (two products an instruction)
+                            ptx::unpack2(ptx::mul2(ptx::pack2(s, s), ptx::pack2(c4.x, c4.y)), s0, s1);
+                            ptx::unpack2(ptx::mul2(ptx::pack2(s, s), ptx::pack2(c4.z, c4.w)), s2, s3);
+                            fold(a[0], q[4 * i], s0);
+                            fold(a[1], q[4 * i + 1], s1);
+                            fold(a[2], q[4 * i + 2], s2);
+                            fold(a[3], q[4 * i + 3], s3);
                         } else {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) fold(a[k], q[4 * i + k], s);
@@ -893,6 +926,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                 slot = nslot;
                 sphase = nphase;
             }
+            __syncwarp();
             if constexpr (!kPair) {
                 // all promote warps leave together: the barriers below need every thread
                 if (p.stream) ok = ptx::named_barrier_and(1, bar_threads, ok);
@@ -966,7 +1000,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                             float v[kOut];
 #pragma unroll
                             for (int i = 0; i < kOut; ++i) v[i] = acc[j * kOut + i];
-                            finish_values<kOut>(p, v, row, col0, lane < rows_ok);
+                            finish_values<kOut>(p, v, row, col0, lane < rows_ok, bias_cols + j * kOut);
                             store_values<kOut>(p, v, row, col0, rows_ok, lane, my_words);
                         }
                     }
