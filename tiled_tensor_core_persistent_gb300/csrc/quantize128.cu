@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include "host.h"
 
@@ -56,77 +57,97 @@ __device__ __forceinline__ float scale_of(const Quant& p, float amax) {
 }
 
 // Two values to two 8-bit codes, round to nearest even, saturating; NaN stays NaN.
-__device__ __forceinline__ uint32_t code2(float lo, float hi, int e5m2) {
+template <bool kE5m2>
+__device__ __forceinline__ uint32_t code2(float lo, float hi) {
     uint16_t r;
-    if (e5m2) asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    if constexpr (kE5m2) asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     else asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, int e5m2) {
-    return code2(a, b, e5m2) | (code2(c, d, e5m2) << 16);
+template <bool kE5m2>
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
+    return code2<kE5m2>(a, b) | (code2<kE5m2>(c, d) << 16);
 }
 
+// N elements as they are stored: 16-bit types stay packed in pairs, which
+// halves the registers of a load in flight and the steps of an amax.
+template <typename T, int N>
+struct Raw {
+    static constexpr int kPer = 4 / static_cast<int>(sizeof(T));   // elements per word
+    static constexpr int kWords = N / kPer;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ float at(int i) const;
+};
 template <typename T>
-struct Elem;
+__device__ __forceinline__ float widen(uint32_t word, int i);   // element i of a word
 template <>
-struct Elem<__nv_bfloat16> {
-    static __device__ __forceinline__ float one(const void* p, long long i) {
-        return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    }
-    static __device__ __forceinline__ void two(uint32_t w, float& a, float& b) {
-        a = __uint_as_float(w << 16);
-        b = __uint_as_float(w & 0xFFFF0000u);
-    }
-};
+__device__ __forceinline__ float widen<__nv_bfloat16>(uint32_t word, int i) {
+    return __uint_as_float(i ? word & 0xFFFF0000u : word << 16);
+}
 template <>
-struct Elem<__half> {
-    static __device__ __forceinline__ float one(const void* p, long long i) {
-        return __half2float(static_cast<const __half*>(p)[i]);
-    }
-    static __device__ __forceinline__ void two(uint32_t w, float& a, float& b) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        a = f.x;
-        b = f.y;
-    }
-};
+__device__ __forceinline__ float widen<__half>(uint32_t word, int i) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(i ? word >> 16 : word & 0xFFFFu)));
+}
 template <>
-struct Elem<float> {
-    static __device__ __forceinline__ float one(const void* p, long long i) { return static_cast<const float*>(p)[i]; }
-};
-
-// N (8 or 16) consecutive elements from a 16-byte aligned address.
+__device__ __forceinline__ float widen<float>(uint32_t word, int) { return __uint_as_float(word); }
 template <typename T, int N>
-__device__ __forceinline__ void load_vec(const void* base, long long i, float (&v)[N]) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int k = 0; k < N / 4; ++k) {
-            const uint4 w = __ldg(src + k);
-            v[4 * k] = __uint_as_float(w.x);
-            v[4 * k + 1] = __uint_as_float(w.y);
-            v[4 * k + 2] = __uint_as_float(w.z);
-            v[4 * k + 3] = __uint_as_float(w.w);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N / 8; ++k) {
-            const uint4 w = __ldg(src + k);
-            Elem<T>::two(w.x, v[8 * k], v[8 * k + 1]);
-            Elem<T>::two(w.y, v[8 * k + 2], v[8 * k + 3]);
-            Elem<T>::two(w.z, v[8 * k + 4], v[8 * k + 5]);
-            Elem<T>::two(w.w, v[8 * k + 6], v[8 * k + 7]);
-        }
-    }
+__device__ __forceinline__ float Raw<T, N>::at(int i) const { return widen<T>(w[i / kPer], i % kPer); }
+
+// Element-wise largest magnitude of two words; NaN is ignored.
+template <typename T>
+__device__ __forceinline__ uint32_t amax_word(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t amax_word<__nv_bfloat16>(uint32_t a, uint32_t b) {
+    b &= 0x7FFF7FFFu;
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+template <>
+__device__ __forceinline__ uint32_t amax_word<__half>(uint32_t a, uint32_t b) {
+    b &= 0x7FFF7FFFu;
+    const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+template <>
+__device__ __forceinline__ uint32_t amax_word<float>(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), fabsf(__uint_as_float(b))));
+}
+template <typename T>
+__device__ __forceinline__ float amax_of(uint32_t word) {   // the larger element of a word
+    return sizeof(T) == 4 ? widen<T>(word, 0) : fmaxf(widen<T>(word, 0), widen<T>(word, 1));
 }
 
-// Elements [i, i + N) of a row of n, zeros past its end.
+// Elements [i, i + N) of a row of x, zeros past its end.
 template <typename T, int N>
-__device__ __forceinline__ void load_some(const Quant& p, long long row_at, int i, float (&v)[N]) {
+__device__ __forceinline__ void load_some(const Quant& p, long long row_at, int i, Raw<T, N>& v) {
+    using R = Raw<T, N>;
+    const T* src = static_cast<const T*>(p.x) + row_at + i;
     if (p.vec && i + N <= p.cols) {
-        load_vec<T, N>(p.x, row_at + i, v);
+#pragma unroll
+        for (int k = 0; k < R::kWords / 4; ++k) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + k);
+            v.w[4 * k] = q.x;
+            v.w[4 * k + 1] = q.y;
+            v.w[4 * k + 2] = q.z;
+            v.w[4 * k + 3] = q.w;
+        }
     } else {
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = i + k < p.cols ? Elem<T>::one(p.x, row_at + i + k) : 0.0f;
+        for (int k = 0; k < R::kWords; ++k) {
+            uint32_t word = 0u;
+            if constexpr (sizeof(T) == 4) {
+                if (i + k < p.cols) word = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
+            } else {
+                const unsigned short* s16 = reinterpret_cast<const unsigned short*>(src);
+                if (i + 2 * k < p.cols) word = __ldg(s16 + 2 * k);
+                if (i + 2 * k + 1 < p.cols) word |= static_cast<uint32_t>(__ldg(s16 + 2 * k + 1)) << 16;
+            }
+            v.w[k] = word;
+        }
     }
 }
 
@@ -137,20 +158,12 @@ __device__ __forceinline__ int source_row(const Quant& p, int r) {
     return s >= 0 && s < p.source ? s : -1;
 }
 
-template <int N>
-__device__ __forceinline__ float amax_of(const float (&v)[N]) {
-    float a = 0.0f;
-#pragma unroll
-    for (int k = 0; k < N; ++k) a = fmaxf(a, fabsf(v[k]));
-    return a;
-}
-
 // ------------------------------------------------------------------------ rows
 //
 // Eight lanes hold a block (16 elements each), a warp four rows of one block
 // column, a CTA 32 rows: the scales of a CTA are one 128-byte line.  kU blocks
 // along the row per warp keep that many loads in flight.
-template <typename T, int kU>
+template <typename T, int kU, bool kE5m2>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Quant p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = blockIdx.y * 32 + warp * 4 + (lane >> 3);
@@ -160,20 +173,19 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Quant
     const int src = source_row(p, r);
     const long long at = src * p.ldx;
     const int blocks = (p.cols + 127) >> 7;
-    float v[kU][16];
+    Raw<T, 16> v[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-        if (src >= 0 && kb0 + u < blocks) {
-            load_some<T, 16>(p, at, (kb0 + u) * 128 + (lane & 7) * 16, v[u]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[u][k] = 0.0f;
-        }
+        if (src >= 0 && kb0 + u < blocks) load_some<T, 16>(p, at, (kb0 + u) * 128 + (lane & 7) * 16, v[u]);
+        else v[u].zero();
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
         if (kb0 + u >= blocks) break;
-        float a = amax_of<16>(v[u]);
+        uint32_t m = 0u;
+#pragma unroll
+        for (int k = 0; k < Raw<T, 16>::kWords; ++k) m = amax_word<T>(m, v[u].w[k]);
+        float a = amax_of<T>(m);
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) a = fmaxf(a, __shfl_xor_sync(peers, a, d));
         const float s = scale_of(p, a);
@@ -181,7 +193,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Quant
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            w[k] = code4(v[u][4 * k] * inv, v[u][4 * k + 1] * inv, v[u][4 * k + 2] * inv, v[u][4 * k + 3] * inv, p.e5m2);
+            w[k] = code4<kE5m2>(v[u].at(4 * k) * inv, v[u].at(4 * k + 1) * inv, v[u].at(4 * k + 2) * inv, v[u].at(4 * k + 3) * inv);
         const int c = (kb0 + u) * 128 + (lane & 7) * 16;
         uint8_t* dst = p.q + r * p.ldq + c;
         if (p.vec && c + 16 <= p.cols) {
@@ -195,13 +207,42 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Quant
     }
 }
 
+// A 128 x 128 tile of codes turning in shared memory, as words of four rows of
+// one column.  Thread (cg, rg) of 16 x 16 holds columns 8 cg .. 8 cg + 7 of rows
+// 8 rg .. 8 rg + 7; the words of a column are rotated by turn(cg), which puts
+// the 32 words that a warp writes at once into 32 banks (and a column's words,
+// read together, stay in 32 banks too).
+__device__ __forceinline__ int turn(int cg) { return ((cg >> 1) << 2) | (cg & 1); }
+
+template <bool kE5m2>
+__device__ __forceinline__ void put_words(uint32_t* words, int cg, int rg, int k, const float (&v)[8]) {
+    uint32_t* col = words + (cg * 8 + k) * 32;
+    col[(2 * rg + turn(cg)) & 31] = code4<kE5m2>(v[0], v[1], v[2], v[3]);
+    col[(2 * rg + 1 + turn(cg)) & 31] = code4<kE5m2>(v[4], v[5], v[6], v[7]);
+}
+
+// Rows [r, r + n) of the transposed tile (n of its 128 columns) to 128-byte lines.
+__device__ __forceinline__ void write_columns(const uint32_t* words, uint8_t* dst, long long ld, int cols, int rows, int warp,
+                                              int lane) {
+    const bool whole = ld % 4 == 0 && reinterpret_cast<uintptr_t>(dst) % 4 == 0 && 4 * lane + 4 <= rows;
+#pragma unroll 4
+    for (int c = warp; c < cols; c += 8) {
+        const uint32_t w = words[c * 32 + ((lane + turn(c >> 3)) & 31)];
+        uint8_t* at = dst + c * ld + 4 * lane;
+        if (whole) {
+            *reinterpret_cast<uint32_t*>(at) = w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (4 * lane + k < rows) at[k] = static_cast<uint8_t>(w >> (8 * k));
+        }
+    }
+}
+
 // ------------------------------------------------------------------------ cols
 //
-// One CTA: the 128 rows of one block row, 64 columns.  A thread holds eight
-// columns of four consecutive rows, so that its codes of one column are one
-// word; the words turn through shared memory (33 words a column, so that a
-// warp's eight column groups meet two-way at worst) into 128-byte lines.
-constexpr int kColTile = 64;
+// One CTA: the 128 rows of one block row, 128 columns.  The amax of a column
+// goes over a thread's eight rows, two lanes and eight warps.
 
 // The first row and the rows of padded block b: the groups' blocks one after
 // the other, each group's last block partly empty.  One warp; the same for
@@ -242,37 +283,40 @@ __device__ __forceinline__ void find_block(const Quant& p, int b, int lane, int&
     }
 }
 
-template <typename T>
+template <typename T, bool kE5m2>
 __global__ void __launch_bounds__(256) cols_kernel(const __grid_constant__ Quant p) {
-    __shared__ float part[8][kColTile];
-    __shared__ float inv_s[kColTile];
-    __shared__ uint32_t words[kColTile * 33];
+    using R = Raw<T, 8>;
+    __shared__ float part[8][128];
+    __shared__ float inv_s[128];
+    __shared__ uint32_t words[128 * 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int block = blockIdx.y, c0 = blockIdx.x * kColTile;
+    const int block = blockIdx.y, c0 = blockIdx.x * 128;
     int row, n;
     find_block(p, block, lane, row, n);
-    const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;   // 8 columns, 4 rows
-    float v[4][8];
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+    R v[8];
+    uint32_t m[R::kWords];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = rg * 4 + i;
+    for (int k = 0; k < R::kWords; ++k) m[k] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = rg * 8 + i;
         const int src = r < n ? source_row(p, row + r) : -1;
-        if (src >= 0) {
-            load_some<T, 8>(p, src * p.ldx, c0 + cg * 8, v[i]);
-        } else {
+        if (src >= 0) load_some<T, 8>(p, src * p.ldx, c0 + cg * 8, v[i]);
+        else v[i].zero();
+    }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
+    for (int k = 0; k < R::kWords; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[k] = amax_word<T>(m[k], v[i].w[k]);
+        m[k] = amax_word<T>(m[k], __shfl_xor_sync(0xffffffffu, m[k], 16));
+        if (lane < 16) {
+#pragma unroll
+            for (int e = 0; e < R::kPer; ++e) part[warp][cg * 8 + k * R::kPer + e] = widen<T>(m[k], e);
         }
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float a = fmaxf(fmaxf(fabsf(v[0][k]), fabsf(v[1][k])), fmaxf(fabsf(v[2][k]), fabsf(v[3][k])));
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
-        if (lane < 8) part[warp][cg * 8 + k] = a;
-    }
     __syncthreads();
-    if (threadIdx.x < kColTile) {
+    if (threadIdx.x < 128) {
         float a = part[0][threadIdx.x];
 #pragma unroll
         for (int i = 1; i < 8; ++i) a = fmaxf(a, part[i][threadIdx.x]);
@@ -285,48 +329,42 @@ __global__ void __launch_bounds__(256) cols_kernel(const __grid_constant__ Quant
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const float inv = inv_s[cg * 8 + k];
-        words[(cg * 8 + k) * 33 + rg] = code4(v[0][k] * inv, v[1][k] * inv, v[2][k] * inv, v[3][k] * inv, p.e5m2);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = v[i].at(k) * inv;
+        put_words<kE5m2>(words, cg, rg, k, x);
     }
     __syncthreads();
-    const bool whole = p.ldq % 4 == 0 && reinterpret_cast<uintptr_t>(p.q) % 4 == 0;
-    for (int c = warp; c < kColTile && c0 + c < p.cols; c += 8) {
-        uint8_t* dst = p.q + (c0 + c) * p.ldq + block * 128LL;
-        const uint32_t w = words[c * 33 + lane];
-        if (whole) {
-            reinterpret_cast<uint32_t*>(dst)[lane] = w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) dst[4 * lane + k] = static_cast<uint8_t>(w >> (8 * k));
-        }
-    }
+    write_columns(words, p.q + c0 * p.ldq + block * 128LL, p.ldq, min(128, p.cols - c0), 128, warp, lane);
 }
 
 // ----------------------------------------------------------------------- tiles
 //
 // One CTA: one 128 x 128 tile of one matrix of the batch (matrix b is rows
-// [b rows, (b + 1) rows) of x).  A thread holds eight columns of eight rows
-// (two groups of four, 64 rows apart); the row-major codes leave from
-// registers, eight bytes a row, the transposed ones through shared memory.
-template <typename T>
+// [b rows, (b + 1) rows) of x).  The row-major codes leave from registers,
+// eight bytes a row and 128 a half warp, the transposed ones through shared
+// memory.
+template <typename T, bool kE5m2>
 __global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ Quant p) {
+    using R = Raw<T, 8>;
     __shared__ float part[8];
-    __shared__ uint32_t words[128 * 33];
+    __shared__ uint32_t words[128 * 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.z, r0 = blockIdx.y * 128, c0 = blockIdx.x * 128;
-    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;   // 8 columns; rows 4 rg + {0..3} + {0, 64}
-    float v[8][8];
-    float a = 0.0f;
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+    R v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int r = r0 + rg * 4 + (i & 3) + (i >> 2) * 64;
-        if (r < p.rows) {
-            load_some<T, 8>(p, (static_cast<long long>(b) * p.rows + r) * p.ldx, c0 + cg * 8, v[i]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
-        }
-        a = fmaxf(a, amax_of<8>(v[i]));
+        const int r = r0 + rg * 8 + i;
+        if (r < p.rows) load_some<T, 8>(p, (static_cast<long long>(b) * p.rows + r) * p.ldx, c0 + cg * 8, v[i]);
+        else v[i].zero();
     }
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < R::kWords; ++k) m = amax_word<T>(m, v[i].w[k]);
+    float a = amax_of<T>(m);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
     if (lane == 0) part[warp] = a;
@@ -338,20 +376,16 @@ __global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ Quan
     const float inv = 1.0f / s;
     if (threadIdx.x == 0)
         p.scales[(static_cast<long long>(b) * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x] = s;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[i][k] *= inv;
     if (p.q) {
         const int c = c0 + cg * 8;
         const bool whole = p.ldq % 8 == 0 && reinterpret_cast<uintptr_t>(p.q) % 8 == 0 && c + 8 <= p.cols;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int r = r0 + rg * 4 + (i & 3) + (i >> 2) * 64;
+            const int r = r0 + rg * 8 + i;
             if (r >= p.rows) continue;
             uint8_t* dst = p.q + (static_cast<long long>(b) * p.rows + r) * p.ldq + c;
-            const uint2 w = make_uint2(code4(v[i][0], v[i][1], v[i][2], v[i][3], p.e5m2),
-                                       code4(v[i][4], v[i][5], v[i][6], v[i][7], p.e5m2));
+            const uint2 w = make_uint2(code4<kE5m2>(v[i].at(0) * inv, v[i].at(1) * inv, v[i].at(2) * inv, v[i].at(3) * inv),
+                                       code4<kE5m2>(v[i].at(4) * inv, v[i].at(5) * inv, v[i].at(6) * inv, v[i].at(7) * inv));
             if (whole) {
                 *reinterpret_cast<uint2*>(dst) = w;
             } else {
@@ -363,25 +397,15 @@ __global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ Quan
     }
     if (!p.qt) return;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int k = 0; k < 8; ++k) {
+        float x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            words[(cg * 8 + k) * 33 + h * 16 + rg] =
-                code4(v[4 * h][k], v[4 * h + 1][k], v[4 * h + 2][k], v[4 * h + 3][k], p.e5m2);
-    __syncthreads();
-    const bool whole = p.ldqt % 4 == 0 && reinterpret_cast<uintptr_t>(p.qt) % 4 == 0;
-    for (int c = warp; c < 128 && c0 + c < p.cols; c += 8) {
-        const int r = r0 + 4 * lane;
-        uint8_t* dst = p.qt + (static_cast<long long>(b) * p.cols + c0 + c) * p.ldqt + r;
-        const uint32_t w = words[c * 33 + lane];
-        if (whole && r + 4 <= p.rows) {
-            *reinterpret_cast<uint32_t*>(dst) = w;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (r + k < p.rows) dst[k] = static_cast<uint8_t>(w >> (8 * k));
-        }
+        for (int i = 0; i < 8; ++i) x[i] = v[i].at(k) * inv;
+        put_words<kE5m2>(words, cg, rg, k, x);
     }
+    __syncthreads();
+    write_columns(words, p.qt + (static_cast<long long>(b) * p.cols + c0) * p.ldqt + r0, p.ldqt, min(128, p.cols - c0),
+                  min(128, p.rows - r0), warp, lane);
 }
 
 // ------------------------------------------------------------------------ host
@@ -418,11 +442,16 @@ tcg_status launched(const char* what) {
     return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch(what, e);
 }
 
-template <int kU>
-void launch_rows(const Quant& p, tcg_dtype t, dim3 grid, cudaStream_t s) {
-    if (t == TCG_BF16) rows_kernel<__nv_bfloat16, kU><<<grid, 256, 0, s>>>(p);
-    else if (t == TCG_F16) rows_kernel<__half, kU><<<grid, 256, 0, s>>>(p);
-    else rows_kernel<float, kU><<<grid, 256, 0, s>>>(p);
+// f(element type, whether the codes are e5m2) for the types of a call
+template <typename F>
+void with_types(tcg_dtype x, bool e5m2, F f) {
+    auto go = [&](auto element) {
+        if (e5m2) f(element, std::true_type{});
+        else f(element, std::false_type{});
+    };
+    if (x == TCG_BF16) go(__nv_bfloat16{});
+    else if (x == TCG_F16) go(__half{});
+    else go(float{});
 }
 
 }  // namespace
@@ -455,9 +484,13 @@ tcg_status tcg_quantize_rows128(int rows, int cols, tcg_dtype x_dtype, const voi
         part.scales = p.scales + first;
         // four blocks per warp once that still gives every SM several CTAs
         if (static_cast<long long>(n) * ((blocks + 3) / 4) >= 4LL * dev.num_sms)
-            launch_rows<4>(part, x_dtype, dim3((blocks + 3) / 4, n), s);
+            with_types(x_dtype, p.e5m2, [&](auto x0, auto e) {
+                rows_kernel<decltype(x0), 4, decltype(e)::value><<<dim3((blocks + 3) / 4, n), 256, 0, s>>>(part);
+            });
         else
-            launch_rows<1>(part, x_dtype, dim3(blocks, n), s);
+            with_types(x_dtype, p.e5m2, [&](auto x0, auto e) {
+                rows_kernel<decltype(x0), 1, decltype(e)::value><<<dim3(blocks, n), 256, 0, s>>>(part);
+            });
     }
     return launched("tcg_quantize_rows128");
 }
@@ -487,11 +520,9 @@ tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const voi
     p.groups = num_groups;
     p.padded = padded_rows;
     const int row_blocks = padded_rows / 128;
-    const dim3 grid((cols + kColTile - 1) / kColTile, row_blocks);
+    const dim3 grid((cols + 127) / 128, row_blocks);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (x_dtype == TCG_BF16) cols_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-    else if (x_dtype == TCG_F16) cols_kernel<__half><<<grid, 256, 0, s>>>(p);
-    else cols_kernel<float><<<grid, 256, 0, s>>>(p);
+    with_types(x_dtype, p.e5m2, [&](auto x0, auto e) { cols_kernel<decltype(x0), decltype(e)::value><<<grid, 256, 0, s>>>(p); });
     return launched("tcg_quantize_cols128");
 }
 
@@ -512,9 +543,7 @@ tcg_status tcg_quantize_tiles128(int batch, int rows, int cols, tcg_dtype x_dtyp
     p.ldqt = ldqt;
     const dim3 grid((cols + 127) / 128, (rows + 127) / 128, batch);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (x_dtype == TCG_BF16) tiles_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-    else if (x_dtype == TCG_F16) tiles_kernel<__half><<<grid, 256, 0, s>>>(p);
-    else tiles_kernel<float><<<grid, 256, 0, s>>>(p);
+    with_types(x_dtype, p.e5m2, [&](auto x0, auto e) { tiles_kernel<decltype(x0), decltype(e)::value><<<grid, 256, 0, s>>>(p); });
     return launched("tcg_quantize_tiles128");
 }
 
