@@ -162,7 +162,10 @@ __device__ __forceinline__ int source_row(const Quant& p, int r) {
 //
 // Eight lanes hold a block (16 elements each), a warp four rows of one block
 // column, a CTA 32 rows: the scales of a CTA are one 128-byte line.  kU blocks
-// along the row per warp keep that many loads in flight.
+// along the row per warp keep that many loads in flight.  The codes are stored
+// to leave the L2 first: rows gathered twice then find more of x there (32768 x
+// 4096 from 16384 rows: 61.4 -> 55.3 us with kU = 2, 61.3 with kU = 4; without
+// the hint 61.4 either way).
 template <typename T, int kU, bool kE5m2>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Quant p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Quant
         const int c = (kb0 + u) * 128 + (lane & 7) * 16;
         uint8_t* dst = p.q + r * p.ldq + c;
         if (p.vec && c + 16 <= p.cols) {
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
         } else {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
@@ -482,10 +485,10 @@ tcg_status tcg_quantize_rows128(int rows, int cols, tcg_dtype x_dtype, const voi
         else part.x = static_cast<const char*>(p.x) + first * ldx * x_bytes(x_dtype);
         part.q = p.q + first * ldq;
         part.scales = p.scales + first;
-        // four blocks per warp once that still gives every SM several CTAs
-        if (static_cast<long long>(n) * ((blocks + 3) / 4) >= 4LL * dev.num_sms)
+        // two blocks per warp once that still gives every SM several CTAs
+        if (static_cast<long long>(n) * ((blocks + 1) / 2) >= 4LL * dev.num_sms)
             with_types(x_dtype, p.e5m2, [&](auto x0, auto e) {
-                rows_kernel<decltype(x0), 4, decltype(e)::value><<<dim3((blocks + 3) / 4, n), 256, 0, s>>>(part);
+                rows_kernel<decltype(x0), 2, decltype(e)::value><<<dim3((blocks + 1) / 2, n), 256, 0, s>>>(part);
             });
         else
             with_types(x_dtype, p.e5m2, [&](auto x0, auto e) {
