@@ -12,7 +12,7 @@ namespace {
 
 using tcg::b128::Params;
 
-enum Tile { kPairTile, kOneTile, kFew16, kFew32, kFew64 };
+enum Tile { kPairTile, kOneTile, kFew16, kFew32 };
 
 struct Plan {
     Tile tile = kOneTile;
@@ -22,8 +22,8 @@ struct Plan {
 
 constexpr size_t kCounterBytes = 8192;
 
-int tile_cols(Tile t) { return t == kPairTile ? 256 : t == kOneTile ? 128 : t == kFew16 ? 16 : t == kFew32 ? 32 : 64; }
-bool few(Tile t) { return t == kFew16 || t == kFew32 || t == kFew64; }
+int tile_cols(Tile t) { return t == kPairTile ? 256 : t == kOneTile ? 128 : t == kFew16 ? 16 : 32; }
+bool few(Tile t) { return t == kFew16 || t == kFew32; }
 
 size_t workspace_bytes(const Plan& pl) {
     size_t n = tcg::host::kWorkspaceHeader;
@@ -45,10 +45,12 @@ Plan make_plan(int mode, long long rows, int groups, int M, int N, int num_kb, i
         pl.workers = static_cast<int>(std::max(1LL, std::min<long long>(tiles, pl.tile == kPairTile ? sms / 2 : sms)));
         return pl;
     }
-    if (per <= 64) {
-        // a grouped call does not know its longest group: room for twice the mean
-        const long long want = mode == tcg::b128::kGroupedRows ? 2 * per : per;
-        pl.tile = want <= 16 ? kFew16 : want <= 32 ? kFew32 : kFew64;
+    // Few rows take the MMA's columns.  A grouped call does not know its longest
+    // group: room for twice the mean.  Past 32 rows the 128-row tile is ahead
+    // (64 x 4096 x 4096: 21 us; with 64 columns 28 us).
+    const long long want = mode == tcg::b128::kGroupedRows ? 2 * per : per;
+    if (want <= 32) {
+        pl.tile = want <= 16 ? kFew16 : kFew32;
     } else if (per > 128 && N > 128 && pair_tiles * 2 >= sms) {
         pl.tile = kPairTile;
     }
@@ -104,7 +106,6 @@ tcg_status launch_plan(Params& p, const Plan& pl, bool col, const tcg::host::Dev
         case kOneTile: return col ? launch<128, false, false, true>(p, pl, dev, s) : launch<128, false, false, false>(p, pl, dev, s);
         case kFew16: return launch<16, false, true, false>(p, pl, dev, s);
         case kFew32: return launch<32, false, true, false>(p, pl, dev, s);
-        case kFew64: return launch<64, false, true, false>(p, pl, dev, s);
     }
     return TCG_ERR_INVALID_ARG;
 }

@@ -942,8 +942,11 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                     // others' sums visible, and the second barrier passes it on.
                     float* mine = p.partials + static_cast<size_t>(slot_of(p, walk, w, w.split)) * (128 * kTileN) +
                                   static_cast<size_t>(col_base) * 128 + lane_row;
+                    // (kSwap: the columns of rows that exist; one token has one)
+                    const int used_cols = kSwap ? min(WC, w.m_end - w.m0) : WC;
 #pragma unroll
-                    for (int i = 0; i < WC; ++i) mine[i * 128] = acc[i];
+                    for (int i = 0; i < WC; ++i)
+                        if (i < used_cols) mine[i * 128] = acc[i];
                     ptx::named_barrier_sync(1, bar_threads);
                     if (threadIdx.x == 32 * S::kControlWarps) {
                         const int old = ptx::atomic_add_acq_rel_gpu(p.counters + w.first, 1);
@@ -956,11 +959,21 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                         // in the order of the pieces, whoever finishes: the sum is the same every time
 #pragma unroll
                         for (int i = 0; i < WC; ++i) acc[i] = 0.0f;
-                        for (int q = 0; q < w.nsplit; ++q) {
-                            const float* src = p.partials + static_cast<size_t>(slot_of(p, walk, w, q)) * (128 * kTileN) +
-                                               static_cast<size_t>(col_base) * 128 + lane_row;
+                        // (kQ pieces' values are on their way at once)
+                        constexpr int kQ = WC <= 16 ? 4 : WC <= 32 ? 2 : 1;
+                        for (int q = 0; q < w.nsplit; q += kQ) {
+                            float got[kQ][WC];
 #pragma unroll
-                            for (int i = 0; i < WC; ++i) acc[i] += __ldcg(src + i * 128);
+                            for (int h = 0; h < kQ; ++h) {
+                                const float* src = p.partials + static_cast<size_t>(slot_of(p, walk, w, min(q + h, w.nsplit - 1))) * (128 * kTileN) +
+                                                   static_cast<size_t>(col_base) * 128 + lane_row;
+#pragma unroll
+                                for (int i = 0; i < WC; ++i) got[h][i] = i < used_cols && q + h < w.nsplit ? __ldcg(src + i * 128) : 0.0f;
+                            }
+#pragma unroll
+                            for (int h = 0; h < kQ; ++h)
+#pragma unroll
+                                for (int i = 0; i < WC; ++i) acc[i] += got[h][i];
                         }
                     }
                     // (ctl->last is not written again before every thread has passed this piece's
