@@ -438,38 +438,62 @@ __device__ __forceinline__ float load_elem(const void* base, int is_f32, long lo
 // beta C + bias (the columns' values in shared memory), activation, on CN (16
 // or 32) consecutive columns of one row
 template <int CN>
-__device__ __forceinline__ void finish_values(const Params& p, float (&v)[CN], long long row, int col0, bool row_ok,
-                                              const float* bias) {
-    if (p.beta != 0.0f && row_ok) {
+__device__ __forceinline__ void finish_values(const Params& p, float (&v)[CN], long long row, int col0, int rows_ok, int lane,
+                                              const float* bias, uint32_t* stage) {
+    if (p.beta != 0.0f) {
         const long long at = row * p.ldc + col0;
         if (p.c_vec && col0 + CN <= p.N) {
-            if (p.c_f32) {
-                const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.C) + at);
+            if (lane < rows_ok) {
+                if (p.c_f32) {
+                    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.C) + at);
 #pragma unroll
-                for (int i = 0; i < CN / 4; ++i) {
-                    const float4 c = __ldcs(src + i);
-                    v[4 * i] = fmaf(p.beta, c.x, v[4 * i]);
-                    v[4 * i + 1] = fmaf(p.beta, c.y, v[4 * i + 1]);
-                    v[4 * i + 2] = fmaf(p.beta, c.z, v[4 * i + 2]);
-                    v[4 * i + 3] = fmaf(p.beta, c.w, v[4 * i + 3]);
-                }
-            } else {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.C) + at);
+                    for (int i = 0; i < CN / 4; ++i) {
+                        const float4 c = __ldcs(src + i);
+                        v[4 * i] = fmaf(p.beta, c.x, v[4 * i]);
+                        v[4 * i + 1] = fmaf(p.beta, c.y, v[4 * i + 1]);
+                        v[4 * i + 2] = fmaf(p.beta, c.z, v[4 * i + 2]);
+                        v[4 * i + 3] = fmaf(p.beta, c.w, v[4 * i + 3]);
+                    }
+                } else {
+                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.C) + at);
 #pragma unroll
-                for (int i = 0; i < CN / 8; ++i) {
-                    const uint4 c = __ldcs(src + i);
-                    const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+                    for (int i = 0; i < CN / 8; ++i) {
+                        const uint4 c = __ldcs(src + i);
+                        const uint32_t u[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        v[8 * i + 2 * h] = fmaf(p.beta, bf16_bits_to_float(u[h] & 0xFFFFu), v[8 * i + 2 * h]);
-                        v[8 * i + 2 * h + 1] = fmaf(p.beta, bf16_bits_to_float(u[h] >> 16), v[8 * i + 2 * h + 1]);
+                        for (int h = 0; h < 4; ++h) {
+                            v[8 * i + 2 * h] = fmaf(p.beta, bf16_bits_to_float(u[h] & 0xFFFFu), v[8 * i + 2 * h]);
+                            v[8 * i + 2 * h + 1] = fmaf(p.beta, bf16_bits_to_float(u[h] >> 16), v[8 * i + 2 * h + 1]);
+                        }
                     }
                 }
             }
         } else {
+            // Rows that do not start on 16 bytes turn through shared memory: 16
+            // lanes read consecutive elements of one row (a thread reading its own
+            // row element by element fetches a sector for each: 16 x 1280 x 522
+            // f32, 210 us).
+            const long long base = (row - lane) * p.ldc + col0 + (lane & 15);
+            float* st = reinterpret_cast<float*>(stage);
 #pragma unroll
-            for (int i = 0; i < CN; ++i)
-                if (col0 + i < p.N) v[i] = fmaf(p.beta, load_elem(p.C, p.c_f32, at + i), v[i]);
+            for (int h = 0; h < CN / 16; ++h) {
+                const bool in = col0 + 16 * h + (lane & 15) < p.N;
+                float got[16];   // (every load first: the compiler moves none past a store)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int r = 2 * i + (lane >> 4);
+                    got[i] = in && r < rows_ok ? load_elem(p.C, p.c_f32, base + r * p.ldc + 16 * h) : 0.0f;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) st[(2 * i + (lane >> 4)) * 17 + (lane & 15)] = got[i];
+                __syncwarp();
+                if (lane < rows_ok) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (col0 + 16 * h + i < p.N) v[16 * h + i] = fmaf(p.beta, st[lane * 17 + i], v[16 * h + i]);
+                }
+            }
         }
     }
     if (p.bias) {
@@ -540,6 +564,7 @@ __device__ __forceinline__ void store_values(const Params& p, const float (&v)[C
             for (int i = 0; i < 16; ++i) stage[lane * 17 + i] = __float_as_uint(v[16 * h + i]);
             __syncwarp();
             const int c = col0 + 16 * h + (lane & 15);
+#pragma unroll 4
             for (int r = lane >> 4; r < rows_ok; r += 2)
                 if (c < p.N) static_cast<float*>(p.D)[(row_base + r) * p.ldd + c] = __uint_as_float(stage[r * 17 + (lane & 15)]);
         }
@@ -554,6 +579,7 @@ __device__ __forceinline__ void store_values(const Params& p, const float (&v)[C
             const int c = col0 + 32 * h + lane;
             const uint16_t* s16 = reinterpret_cast<const uint16_t*>(stage);
             if (lane < CN && c < p.N)
+#pragma unroll 4
                 for (int r = 0; r < rows_ok; ++r)
                     static_cast<uint16_t*>(p.D)[(row_base + r) * p.ldd + c] = s16[r * 34 + lane];
         }
@@ -1013,7 +1039,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                             float v[kOut];
 #pragma unroll
                             for (int i = 0; i < kOut; ++i) v[i] = acc[j * kOut + i];
-                            finish_values<kOut>(p, v, row, col0, lane < rows_ok, bias_cols + j * kOut);
+                            finish_values<kOut>(p, v, row, col0, rows_ok, lane, bias_cols + j * kOut, my_words);
                             store_values<kOut>(p, v, row, col0, rows_ok, lane, my_words);
                         }
                     }
