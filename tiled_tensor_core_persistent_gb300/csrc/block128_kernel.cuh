@@ -32,7 +32,6 @@ namespace tcg {
 namespace b128 {
 
 constexpr int kBlock = 128;                 // K elements per scale = bytes per swizzle row
-constexpr int kAtoms = 2;                   // k-blocks per pipeline stage
 constexpr int kMaxGroups = 1024;
 constexpr int kScaleSlots = 8;              // k-blocks of scales in flight
 
@@ -608,6 +607,7 @@ struct Shape {
     static constexpr int kLaneRows = 128;                          // rows of the lane operand per CTA
     static constexpr int kColRows = kPair ? kTileN / 2 : kTileN;   // rows of the column operand per CTA
     static constexpr int kAtomBytes = (kLaneRows + kColRows) * kBlock;
+    static constexpr int kAtoms = kSwap ? 1 : 2;                   // k-blocks per pipeline stage
     static constexpr int kStageBytes = kAtoms * kAtomBytes;
     static constexpr int kBufs = kPair ? 2 : 4;
     static constexpr int kTmemCols = kBufs * kTileN < 32 ? 32 : kBufs * kTileN;
@@ -633,6 +633,7 @@ template <int kTileN, bool kPair, bool kSwap, bool kColScale>
 __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThreads, 1)
     block128_kernel(const __grid_constant__ Params p) {
     using S = Shape<kTileN, kPair, kSwap, kColScale>;
+    constexpr int kAtoms = S::kAtoms;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int stages = p.stages;
@@ -677,6 +678,10 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
             ptx::tmem_relinquish_alloc_permit();
         }
     }
+    // Blocks of the next call may start as this one's end, and set up so far;
+    // what the call before has written is read only from here on.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 0 && p.mode != kDense)
         build_groups<S::kTileM>(p, tables, tables + p.num_groups + 1, tables + 2 * p.num_groups + 1, lane);
     ptx::tc_fence_before_sync();
