@@ -85,6 +85,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load libtcgemm.so (it must have been built, e.g. by __graft_entry__.build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

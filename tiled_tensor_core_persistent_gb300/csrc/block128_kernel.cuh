@@ -27,6 +27,7 @@
 #pragma once
 
 #include "gemm_kernel.cuh"
+#include "host.h"
 
 namespace tcg {
 namespace b128 {
@@ -680,8 +681,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
     }
     // Blocks of the next call may start as this one's end, and set up so far;
     // what the call before has written is read only from here on.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    host::wait_for_kernel_ahead();
     if (warp == 0 && p.mode != kDense)
         build_groups<S::kTileM>(p, tables, tables + p.num_groups + 1, tables + 2 * p.num_groups + 1, lane);
     ptx::tc_fence_before_sync();

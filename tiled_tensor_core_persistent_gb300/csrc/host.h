@@ -30,6 +30,26 @@ tcg_status fail_launch(const char* what, cudaError_t e);
 // rows ld bytes apart), 128-byte swizzled boxes; cached as tcg_gemm's are.
 tcg_status map_bytes(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
                      uint32_t box_inner, uint32_t box_outer);
+// Launch with leave to start while the kernel ahead ends; the kernel calls
+// wait_for_kernel_ahead() before it reads or writes anything.
+template <typename P>
+cudaError_t launch_early(void (*kernel)(P), dim3 grid, unsigned threads, cudaStream_t stream, const P& p) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+__device__ __forceinline__ void wait_for_kernel_ahead() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // and the next one may do the same
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Test knobs of tcg_debug_set.
 long long wait_timeout_ns();
 int fault_inject();

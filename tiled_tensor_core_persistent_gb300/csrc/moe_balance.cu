@@ -179,6 +179,7 @@ __device__ __forceinline__ float exp_row(float (&x)[kC][8]) {
 
 template <typename T, int kL, int kC>
 __global__ void __launch_bounds__(kThreads) balance_kernel(const __grid_constant__ Balance p) {
+    tcg::host::wait_for_kernel_ahead();
     constexpr int kR = rows_in_flight(kC);
     __shared__ float sums[kWarps / 2 * kMaxExperts];
     __shared__ int hist[kMaxExperts];
@@ -339,6 +340,7 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(const __grid_constant
 
 template <typename T, int kL, int kC>
 __global__ void __launch_bounds__(256) balance_grad_kernel(const __grid_constant__ Balance p) {
+    tcg::host::wait_for_kernel_ahead();
     constexpr int kR = rows_in_flight(kC);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane & (kL - 1), slot = lane / kL, per_warp = 32 / kL;
@@ -445,10 +447,7 @@ void with_types(tcg_dtype dtype, int experts, F f) {
     else with_shape<float>(experts, f);
 }
 
-tcg_status launched(const char* what) {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch(what, e);
-}
+tcg_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch(what, e); }
 
 }  // namespace
 
@@ -484,10 +483,11 @@ tcg_status tcg_moe_balance(int tokens, int experts, int k, tcg_dtype dtype, cons
     const int per_cta = kWarps * (32 / lanes_of(experts)) * rows_in_flight(chunks);
     const int ctas = std::max(1, std::min(dev.num_sms, (tokens + per_cta - 1) / per_cta));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaSuccess;
     with_types(dtype, experts, [&](auto x, auto l, auto c) {
-        balance_kernel<decltype(x), decltype(l)::value, decltype(c)::value><<<ctas, kThreads, 0, s>>>(p);
+        err = tcg::host::launch_early(balance_kernel<decltype(x), decltype(l)::value, decltype(c)::value>, dim3(ctas), kThreads, s, p);
     });
-    return launched("tcg_moe_balance");
+    return launched(err, "tcg_moe_balance");
 }
 
 tcg_status tcg_moe_balance_backward(int tokens, int experts, int k, tcg_dtype dtype, const void* logits, int ld,
@@ -513,10 +513,11 @@ tcg_status tcg_moe_balance_backward(int tokens, int experts, int k, tcg_dtype dt
     const long long per_cta = 8LL * (32 / lanes_of(experts)) * rows_in_flight(chunks_of(experts));
     const int ctas = static_cast<int>(std::max(1LL, std::min<long long>(4LL * dev.num_sms, (tokens + per_cta - 1) / per_cta)));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaSuccess;
     with_types(dtype, experts, [&](auto x, auto l, auto c) {
-        balance_grad_kernel<decltype(x), decltype(l)::value, decltype(c)::value><<<ctas, 256, 0, s>>>(p);
+        err = tcg::host::launch_early(balance_grad_kernel<decltype(x), decltype(l)::value, decltype(c)::value>, dim3(ctas), 256, s, p);
     });
-    return launched("tcg_moe_balance_backward");
+    return launched(err, "tcg_moe_balance_backward");
 }
 
 }  // extern "C"

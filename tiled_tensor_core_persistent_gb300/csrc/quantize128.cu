@@ -168,6 +168,7 @@ __device__ __forceinline__ int source_row(const Quant& p, int r) {
 // the hint 61.4 either way).
 template <typename T, int kU, bool kE5m2>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Quant p) {
+    tcg::host::wait_for_kernel_ahead();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = blockIdx.y * 32 + warp * 4 + (lane >> 3);
     const int kb0 = blockIdx.x * kU;
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(256) cols_kernel(const __grid_constant__ Quant
     __shared__ float part[8][128];
     __shared__ float inv_s[128];
     __shared__ uint32_t words[128 * 32];
+    tcg::host::wait_for_kernel_ahead();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int block = blockIdx.y, c0 = blockIdx.x * 128;
     int row, n;
@@ -352,6 +354,7 @@ __global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ Quan
     using R = Raw<T, 8>;
     __shared__ float part[8];
     __shared__ uint32_t words[128 * 32];
+    tcg::host::wait_for_kernel_ahead();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.z, r0 = blockIdx.y * 128, c0 = blockIdx.x * 128;
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
@@ -440,10 +443,7 @@ tcg_status start(Quant& p, int rows, int cols, tcg_dtype x_dtype, const void* x,
     return TCG_OK;
 }
 
-tcg_status launched(const char* what) {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch(what, e);
-}
+tcg_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch(what, e); }
 
 // f(element type, whether the codes are e5m2) for the types of a call
 template <typename F>
@@ -476,7 +476,8 @@ tcg_status tcg_quantize_rows128(int rows, int cols, tcg_dtype x_dtype, const voi
     p.vec = p.vec && aligned(q, 16) && ldq % 16 == 0;
     const int blocks = (cols + 127) / 128, row_ctas = (rows + 31) / 32;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    for (int done = 0; done < row_ctas; done += 65535) {   // gridDim.y's limit
+    cudaError_t err = cudaSuccess;
+    for (int done = 0; done < row_ctas && err == cudaSuccess; done += 65535) {   // gridDim.y's limit
         const int n = std::min(row_ctas - done, 65535);
         Quant part = p;
         const long long first = static_cast<long long>(done) * 32;
@@ -488,14 +489,14 @@ tcg_status tcg_quantize_rows128(int rows, int cols, tcg_dtype x_dtype, const voi
         // two blocks per warp once that still gives every SM several CTAs
         if (static_cast<long long>(n) * ((blocks + 1) / 2) >= 4LL * dev.num_sms)
             with_types(x_dtype, p.e5m2, [&](auto x0, auto e) {
-                rows_kernel<decltype(x0), 2, decltype(e)::value><<<dim3((blocks + 1) / 2, n), 256, 0, s>>>(part);
+                err = tcg::host::launch_early(rows_kernel<decltype(x0), 2, decltype(e)::value>, dim3((blocks + 1) / 2, n), 256, s, part);
             });
         else
             with_types(x_dtype, p.e5m2, [&](auto x0, auto e) {
-                rows_kernel<decltype(x0), 1, decltype(e)::value><<<dim3(blocks, n), 256, 0, s>>>(part);
+                err = tcg::host::launch_early(rows_kernel<decltype(x0), 1, decltype(e)::value>, dim3(blocks, n), 256, s, part);
             });
     }
-    return launched("tcg_quantize_rows128");
+    return launched(err, "tcg_quantize_rows128");
 }
 
 tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx, const int* row_index,
@@ -525,8 +526,9 @@ tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const voi
     const int row_blocks = padded_rows / 128;
     const dim3 grid((cols + 127) / 128, row_blocks);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    with_types(x_dtype, p.e5m2, [&](auto x0, auto e) { cols_kernel<decltype(x0), decltype(e)::value><<<grid, 256, 0, s>>>(p); });
-    return launched("tcg_quantize_cols128");
+    cudaError_t err = cudaSuccess;
+    with_types(x_dtype, p.e5m2, [&](auto x0, auto e) { err = tcg::host::launch_early(cols_kernel<decltype(x0), decltype(e)::value>, grid, 256, s, p); });
+    return launched(err, "tcg_quantize_cols128");
 }
 
 tcg_status tcg_quantize_tiles128(int batch, int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx, void* q,
@@ -546,8 +548,9 @@ tcg_status tcg_quantize_tiles128(int batch, int rows, int cols, tcg_dtype x_dtyp
     p.ldqt = ldqt;
     const dim3 grid((cols + 127) / 128, (rows + 127) / 128, batch);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    with_types(x_dtype, p.e5m2, [&](auto x0, auto e) { tiles_kernel<decltype(x0), decltype(e)::value><<<grid, 256, 0, s>>>(p); });
-    return launched("tcg_quantize_tiles128");
+    cudaError_t err = cudaSuccess;
+    with_types(x_dtype, p.e5m2, [&](auto x0, auto e) { err = tcg::host::launch_early(tiles_kernel<decltype(x0), decltype(e)::value>, grid, 256, s, p); });
+    return launched(err, "tcg_quantize_tiles128");
 }
 
 }  // extern "C"
