@@ -11,14 +11,23 @@
 // accumulation of four K = 32 MMAs, and the promote warps fold it into fp32
 // registers: acc += (sA sB) * T_kb.
 //
-// What bounds it.  A pair tile of 256 x 256 x 128 keeps each SM's tensor core
-// busy for 128 * 256 * 128 / 8192 = 512 cycles.  In that time the SM's promote
-// warps read 128 x 256 words from TMEM (256 cycles at 16 bytes per lane and
-// clock) and issue 128 * 256 FMAs (256 cycles of the 128 lanes, in f32x2
-// pairs), so the fold hides behind the MMAs as long as its latency does: two
-// TMEM buffers, eight promote warps (two per TMEM quadrant, so that one
-// loads while the other multiplies).  A per-column scale (both operands
-// scaled per row, the weight gradient) adds one multiply per element.
+// What bounds it.  A k-block of a 256 x 256 pair tile keeps each SM's tensor
+// core busy for 128 * 256 * 128 / 8192 = 512 cycles; its fold is 128 x 256 words
+// from TMEM (256 cycles at 16 bytes per lane and clock) and as many FMAs (256
+// issue cycles of each scheduler, next to the waits and the hand-overs).  Two
+// accumulators of 256 columns fill the TMEM, so the chain MMAs -> commit ->
+// fold -> hand-back closes over two k-blocks, and one takes about 950 cycles:
+// 8192^3 in 513-526 us, 2.09-2.14 PFLOP/s, 1.1 times the bf16 rate of the
+// library on this GPU.  Measured at 8192^3 and slower: FMAs of two sums an
+// instruction (the pairs cost a move each), 128-column accumulators with an
+// issuer each or one issuer for both (513-565 us beside 498-520), the next
+// k-block's first chunk read ahead of the fold's end (574-589), 256 x 192
+// tiles under twelve promote warps (613-640), 128 x 256 tiles on one CTA (557).
+// A per-column scale (both operands scaled per row, the weight gradients) adds
+// one multiply per element, and fp32 C and D their traffic: 4096 x 4096 over
+// 16384 rows of K in 8 groups, 878 us, 2.6 TB/s.  Few rows are bound by B's
+// bytes and a launch's start and end (1 x 8192 x 8192: 19.6 us, 3.4 TB/s; 32
+// rows over 16 experts of 4096 x 4096: 45.7 us, 5.1 TB/s).
 //
 // Roles (one CTA or a CTA pair, persistent): warp 0 TMA producer, warp 1 MMA
 // issuer and TMEM owner, the others promote and store.  All waits are
@@ -35,6 +44,7 @@ namespace b128 {
 constexpr int kBlock = 128;                 // K elements per scale = bytes per swizzle row
 constexpr int kMaxGroups = 1024;
 constexpr int kScaleSlots = 8;              // k-blocks of scales in flight
+constexpr int kMaxPromoteWarps = 8;
 
 enum Mode : int { kDense = 0, kGroupedRows = 1, kGroupedK = 2 };
 
@@ -77,6 +87,17 @@ struct Params {
     int fault_inject;
 };
 
+// One piece of work: the output tile's place, its k-blocks, and its share of
+// the tile.  Row and k-block numbers are those of the operands in memory.
+struct Piece {
+    int g, m0, m_end, n0;      // rows [m0, m_end) may be stored
+    int b_row;                 // row of B's map where the tile starts
+    int d_row;                 // added to a row number for D and C (grouped K: g * M)
+    int kb0, kb1;              // k-blocks of this piece
+    int nsplit, split, first;  // pieces of the tile, this one's place, the first piece's worker
+    int tile;
+};
+
 struct alignas(16) Ctl {
     uint64_t full[16];
     uint64_t empty[16];
@@ -88,6 +109,7 @@ struct alignas(16) Ctl {
     uint32_t tmem_base;
     int abort_flag;
     int last;
+    Piece piece[kMaxPromoteWarps];
 };
 
 // (the clock is read once every 64 tries: reading it takes longer than most waits)
@@ -250,16 +272,22 @@ __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
 
 // ------------------------------------------------------------------ schedule
 
-// One piece of work: the output tile's place, its k-blocks, and its share of
-// the tile.  Row and k-block numbers are those of the operands in memory.
-struct Piece {
-    int g, m0, m_end, n0;      // rows [m0, m_end) may be stored
-    int b_row;                 // row of B's map where the tile starts
-    int d_row;                 // added to a row number for D and C (grouped K: g * M)
-    int kb0, kb1;              // k-blocks of this piece
-    int nsplit, split, first;  // pieces of the tile, this one's place, the first piece's worker
-    int tile;
-};
+__device__ __forceinline__ Piece load_piece(const volatile Piece* s) {
+    Piece w;
+    w.g = s->g;
+    w.m0 = s->m0;
+    w.m_end = s->m_end;
+    w.n0 = s->n0;
+    w.b_row = s->b_row;
+    w.d_row = s->d_row;
+    w.kb0 = s->kb0;
+    w.kb1 = s->kb1;
+    w.nsplit = s->nsplit;
+    w.split = s->split;
+    w.first = s->first;
+    w.tile = s->tile;
+    return w;
+}
 
 // Group tables in shared memory, built once per CTA: first tile (grouped
 // rows) or first k-block (grouped K) of each group, and its rows.
@@ -595,10 +623,11 @@ __device__ __forceinline__ void store_values(const Params& p, const float (&v)[C
 // kColScale: one scale per B row (per MMA column), else one per 128.
 template <int kTileN, bool kPair, bool kSwap, bool kColScale>
 struct Shape {
-    static constexpr int kPromoteWarps = kSwap ? 4 : 8;
+    static constexpr int kPromoteWarps = kSwap ? 4 : kMaxPromoteWarps;
     // The eight promote warps of a wide tile hold 128 (a pair) or 64 sums a
     // thread; they take over registers that the four control warps give back
-    // (128 * 72 + 256 * 216 = 384 * 168, what the block is launched with).
+    // (128 * 56 + 256 * 224 = 384 * 168, what the block is launched with; 40 and
+    // 232 or 72 and 216: 8192^3 the same, weight gradients 1 and 4 % slower).
     static constexpr int kControlWarps = 4;
     static constexpr bool kSplitRegs = !kSwap;
     static constexpr int kControlRegs = 56, kPromoteRegs = 224, kLaunchRegs = 168;
@@ -853,6 +882,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         constexpr int kChunks = WC / kChunk;
         constexpr int kOut = WC < 32 ? WC : 32;   // columns stored at a time
         uint32_t* my_words = warp_words + pw * S::kWarpWords;
+        Piece* my_piece = &ctl->piece[pw];
         float* bias_cols = reinterpret_cast<float*>(my_words + kStageWords);
         int buf = 0, slot = 0;
         uint32_t bphase = 0, sphase = 0;
@@ -884,6 +914,11 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                     for (; c < end; c += 128) ptx::prefetch_l2(c);
                 }
             }
+            // (the piece waits in shared memory: the loop needs the registers; weight
+            // gradients of 4096 x 4096 over 16384 rows: 904 -> 878 us)
+            const int kb0 = w.kb0, kb1 = w.kb1;
+            __syncwarp();   // (no lane still reads the piece before)
+            if (lane == 0) *my_piece = w;
             float acc[WC];
 #pragma unroll
             for (int i = 0; i < WC; ++i) acc[i] = 0.0f;
@@ -893,16 +928,16 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                 l_next = sw[lane_row];
                 if constexpr (!S::kCols) c_next = sw[128 + col_base / 128];
             };
-            if (w.kb0 < w.kb1) {
+            if (kb0 < kb1) {
                 ok = wait_warp(&ctl->scale_full[slot], sphase, p, ctl, 5);
                 if (ok) read_scale(slot);
             }
-            for (int kb = w.kb0; ok && kb < w.kb1; ++kb) {
+            for (int kb = kb0; ok && kb < kb1; ++kb) {
                 // The k-block's sums, and with them the next one's scales: those are
                 // there long before, and read a whole k-block ahead of their use.
                 const int nslot = slot + 1 == kScaleSlots ? 0 : slot + 1;
                 const uint32_t nphase = sphase ^ (nslot == 0 ? 1u : 0u);
-                const bool more = kb + 1 < w.kb1;
+                const bool more = kb + 1 < kb1;
                 if (!wait_pair(&ctl->tmem_full[buf], bphase, more ? &ctl->scale_full[nslot] : &ctl->tmem_full[buf],
                                more ? nphase : bphase, lane, p, ctl, 4)) {
                     ok = false;
@@ -958,6 +993,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                 sphase = nphase;
             }
             __syncwarp();
+            w = load_piece(my_piece);
             if constexpr (!kPair) {
                 // all promote warps leave together: the barriers below need every thread
                 if (p.stream) ok = ptx::named_barrier_and(1, bar_threads, ok);
