@@ -402,7 +402,8 @@ tcg_status tcg_grouped_plan(int num_problems, const tcg_problem* problems, tcg_d
  * x_dtype: TCG_BF16, TCG_F16 or TCG_F32.  q_dtype: TCG_E4M3 or TCG_E5M2.  Any
  * leading dimensions and alignments (of the element) are taken; whole vectors
  * are used where x and q start on 16 bytes and their pitches are multiples of
- * 16 bytes.
+ * 16 bytes.  In these calls, the block-scaled products and the balance loss an
+ * extent above 2^31 - 4096 is refused with TCG_ERR_UNSUPPORTED.
  * ---------------------------------------------------------------------------
  */
 
@@ -547,7 +548,7 @@ tcg_status tcg_gemm_block128_grouped_k(int num_groups, const int* offsets, int M
  * p = 0.  Writes counts (experts), offsets (experts + 1: where each expert's
  * rows start when the counted assignments are put in expert order; may be
  * NULL), num_valid (n) and loss (fp32), all device memory.  The loss is the
- * same every time (fixed order of summation).  experts <= 1024 (else
+ * same every time (the sums are integers).  experts <= 1024 (else
  * TCG_ERR_UNSUPPORTED).  workspace: tcg_moe_balance_workspace_size bytes,
  * zero-filled once; calls that share it must be ordered.
  */

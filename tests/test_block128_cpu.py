@@ -162,3 +162,25 @@ def test_balance_refusals():
     assert code(lambda: balance(topk=P + 2)) == MISALIGNED
     assert code(lambda: balance_grad(d=P + 2)) == MISALIGNED
     assert code(lambda: balance_grad(t=0, x=None)) == 0
+
+
+def test_extents_past_the_index_range():
+    """An index rounded up to a tile or a step has to fit an int: 2^31 - 4096 is taken, more is refused."""
+    top = 2 ** 31 - 4096
+    big = 2 ** 31 - 1
+    for call in (rows, cols, tiles):
+        assert code(lambda: call(c=top + 1, ldx=big, ldq=big, **({"lds": big} if call is cols else {}))) == UNSUPPORTED
+    assert code(lambda: rows(r=top + 1, lds=big)) == UNSUPPORTED
+    assert no_gpu(lambda: rows(r=top, lds=big))
+    assert no_gpu(lambda: rows(c=top, ldx=big, ldq=big))
+    for bad in (dict(M=top + 1), dict(N=top + 1, ldd=big), dict(K=top + 1, A=op(ld=big - 15), B=op(ld=big - 15))):
+        assert code(lambda: gemm(**bad)) == UNSUPPORTED, bad
+    assert code(lambda: grouped(rows=top + 1)) == UNSUPPORTED
+    assert code(lambda: grouped(G=1, N=top + 1, ldd=big)) == UNSUPPORTED
+    assert code(lambda: grouped(K=top + 1, A=op(ld=big - 15), B=op(ld=big - 15))) == UNSUPPORTED
+    assert code(lambda: grouped_k(G=1, M=top + 1)) == UNSUPPORTED
+    assert code(lambda: grouped_k(G=1, N=top + 1, ldd=big)) == UNSUPPORTED
+    assert code(lambda: grouped_k(padded=2 ** 31 - 128, A=op(ld=big - 15), B=op(ld=big - 15))) == UNSUPPORTED
+    assert code(lambda: balance(t=top + 1)) == UNSUPPORTED
+    assert code(lambda: balance_grad(t=top + 1)) == UNSUPPORTED
+    assert no_gpu(lambda: balance_grad(t=top))

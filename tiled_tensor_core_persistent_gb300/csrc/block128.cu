@@ -227,6 +227,7 @@ tcg_status tcg_gemm_block128(int M, int N, int K, tcg_dtype ab_dtype, tcg_block_
     if (epi.act != TCG_ACT_NONE && epi.act != TCG_ACT_RELU && epi.act != TCG_ACT_GELU) return TCG_ERR_INVALID_ARG;
     if (epi.bias && epi.bias_dtype != TCG_BF16 && epi.bias_dtype != TCG_F32) return TCG_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return TCG_OK;
+    if (std::max({M, N, K}) > tcg::host::kMaxExtent) return TCG_ERR_UNSUPPORTED;
     tcg_status st = check_operand(A, K, true);
     if (st == TCG_OK) st = check_operand(B, K, false);
     if (st == TCG_OK) st = check_output(N, beta, C, ldc, c_dtype, D, ldd, d_dtype);
@@ -257,7 +258,9 @@ tcg_status tcg_gemm_block128_grouped(int num_groups, const int* offsets, int row
     if (num_groups < 0 || rows < 0 || N < 0 || K < 0) return TCG_ERR_INVALID_ARG;
     if (ab_dtype != TCG_E4M3 && ab_dtype != TCG_E5M2) return TCG_ERR_INVALID_ARG;
     if (num_groups == 0 || rows == 0 || N == 0) return TCG_OK;
-    if (num_groups > tcg::b128::kMaxGroups || static_cast<long long>(num_groups) * N > INT_MAX) return TCG_ERR_UNSUPPORTED;
+    if (num_groups > tcg::b128::kMaxGroups || std::max(rows, K) > tcg::host::kMaxExtent ||
+        static_cast<long long>(num_groups) * N > tcg::host::kMaxExtent)
+        return TCG_ERR_UNSUPPORTED;
     if (!offsets) return TCG_ERR_INVALID_ARG;
     if (!aligned(offsets, 4)) return TCG_ERR_MISALIGNED;
     tcg_status st = check_operand(A, K, true);
@@ -289,7 +292,8 @@ tcg_status tcg_gemm_block128_grouped_k(int num_groups, const int* offsets, int M
     if (num_groups < 0 || M < 0 || N < 0 || padded_rows < 0) return TCG_ERR_INVALID_ARG;
     if (ab_dtype != TCG_E4M3 && ab_dtype != TCG_E5M2) return TCG_ERR_INVALID_ARG;
     if (num_groups == 0 || M == 0 || N == 0) return TCG_OK;
-    if (num_groups > tcg::b128::kMaxGroups || static_cast<long long>(num_groups) * M > INT_MAX ||
+    if (num_groups > tcg::b128::kMaxGroups || std::max(N, padded_rows) > tcg::host::kMaxExtent ||
+        static_cast<long long>(num_groups) * M > tcg::host::kMaxExtent ||
         static_cast<long long>(num_groups) * blocks(M, 128) * blocks(N, 128) > INT_MAX)
         return TCG_ERR_UNSUPPORTED;
     if (padded_rows % 128) return TCG_ERR_INVALID_ARG;

@@ -19,6 +19,7 @@ struct Device {
     int max_smem_optin = 0;
 };
 
+constexpr int kMaxExtent = 0x7FFFFFFF - 4095;   // rows or columns: an index rounded up to a tile or a step still fits an int
 constexpr size_t kWorkspaceHeader = 256;   // status word and diagnostics at the start of a workspace
 
 // The current device; TCG_ERR_ARCH when it is not sm_103.

@@ -397,7 +397,7 @@ tcg_status start(Balance& p, int tokens, int experts, int k, tcg_dtype dtype, co
                  const uint8_t* mask, float coef) {
     if (tokens < 0 || experts < 1 || k < 1) return TCG_ERR_INVALID_ARG;
     if (dtype != TCG_BF16 && dtype != TCG_F16 && dtype != TCG_F32) return TCG_ERR_INVALID_ARG;
-    if (experts > kMaxExperts) return TCG_ERR_UNSUPPORTED;
+    if (experts > kMaxExperts || tokens > tcg::host::kMaxExtent) return TCG_ERR_UNSUPPORTED;
     if (tokens > 0 && (!logits || ld < experts)) return TCG_ERR_INVALID_ARG;
     if (!aligned(logits, size_of(dtype))) return TCG_ERR_MISALIGNED;
     p.logits = logits;

