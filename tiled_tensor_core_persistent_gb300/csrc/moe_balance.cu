@@ -12,8 +12,8 @@
 //
 // Bound by memory on paper (logits once forward; once more, and their
 // gradient, backward: 5 us for 32768 x 256), in fact by the instructions and
-// latencies of a row's exponentials at that size (19.7 us forward, 18.6 us
-// backward), and for few tokens by the launch.  P_e sums stay in the registers
+// latencies of a row's exponentials at that size (forward and backward 29.5 us
+// back to back), and for few tokens by the launch.  P_e sums stay in the registers
 // of the lane that owns the columns.  A CTA's sums are added to 64-bit
 // fixed-point totals in the workspace (2^-32 steps: integer sums do not depend
 // on the order of arrival), which the last CTA reads in one go and leaves at
