@@ -482,8 +482,10 @@ typedef struct {
  * counters and fp32 partial sums.  num_groups = 0: tcg_gemm_block128;
  * otherwise tcg_gemm_block128_grouped with M rows in all
  * (tcg_gemm_block128_grouped_k needs 256 bytes).  Zero-fill it once
- * (tcg_workspace_init); the calls leave it so, and the workspace of several
- * calls on one stream may be one.  0 for invalid sizes.
+ * (tcg_workspace_init).  Calls leave zero what calls need zero, and the partial
+ * sums lie past that, so calls on one stream may share one workspace, these
+ * three and tcg_moe_balance among themselves in any order, with the largest of
+ * their sizes (fewer rows can need more).  0 for invalid sizes.
  */
 size_t tcg_block128_workspace_size(int num_groups, int M, int N, int K);
 
@@ -550,7 +552,8 @@ tcg_status tcg_gemm_block128_grouped_k(int num_groups, const int* offsets, int M
  * NULL), num_valid (n) and loss (fp32), all device memory.  The loss is the
  * same every time (the sums are integers).  experts <= 1024 (else
  * TCG_ERR_UNSUPPORTED).  workspace: tcg_moe_balance_workspace_size bytes,
- * zero-filled once; calls that share it must be ordered.
+ * zero-filled once; calls that share it must be ordered (the block-scaled
+ * products may be among them).
  */
 size_t tcg_moe_balance_workspace_size(void);
 tcg_status tcg_moe_balance(int tokens, int experts, int k, tcg_dtype dtype, const void* logits, int ld,

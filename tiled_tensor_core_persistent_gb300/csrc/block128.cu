@@ -20,15 +20,12 @@ struct Plan {
     int workers = 1;   // CTAs, or CTA pairs
 };
 
-constexpr size_t kCounterBytes = 8192;
-
 int tile_cols(Tile t) { return t == kPairTile ? 256 : t == kOneTile ? 128 : t == kFew16 ? 16 : 32; }
 bool few(Tile t) { return t == kFew16 || t == kFew32; }
 
 size_t workspace_bytes(const Plan& pl) {
-    size_t n = tcg::host::kWorkspaceHeader;
-    if (pl.stream) n += kCounterBytes + static_cast<size_t>(2) * pl.workers * 128 * tile_cols(pl.tile) * sizeof(float);
-    return n;
+    if (!pl.stream) return tcg::host::kWorkspaceHeader;
+    return tcg::host::kScratchAt + static_cast<size_t>(2) * pl.workers * 128 * tile_cols(pl.tile) * sizeof(float);
 }
 
 long long blocks(long long n, int b) { return (n + b - 1) / b; }
@@ -68,6 +65,8 @@ Plan make_plan(int mode, long long rows, int groups, int M, int N, int num_kb, i
     long long units = tile_rows * blocks(N, tn);
     if (pl.stream) units *= std::max(1, num_kb / 4);   // a run of fewer k-blocks than a pipeline holds gains nothing
     pl.workers = static_cast<int>(std::max(1LL, std::min<long long>(units, pl.tile == kPairTile ? sms / 2 : sms)));
+    // (a counter each)
+    if (pl.stream) pl.workers = std::min(pl.workers, static_cast<int>(tcg::host::kCounterBytes / sizeof(int)));
     return pl;
 }
 
@@ -184,7 +183,7 @@ tcg_status run(Params& p, const Plan& pl, const tcg_block_operand& A, const tcg_
     char* ws = static_cast<char*>(workspace);
     p.status = reinterpret_cast<int*>(ws);
     p.counters = reinterpret_cast<int*>(ws + tcg::host::kWorkspaceHeader);
-    p.partials = reinterpret_cast<float*>(ws + tcg::host::kWorkspaceHeader + kCounterBytes);
+    p.partials = reinterpret_cast<float*>(ws + tcg::host::kScratchAt);
     p.stream = pl.stream;
     p.timeout_ns = tcg::host::wait_timeout_ns();
     p.fault_inject = tcg::host::fault_inject();

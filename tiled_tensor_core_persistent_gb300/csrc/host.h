@@ -20,7 +20,19 @@ struct Device {
 };
 
 constexpr int kMaxExtent = 0x7FFFFFFF - 4095;   // rows or columns: an index rounded up to a tile or a step still fits an int
-constexpr size_t kWorkspaceHeader = 256;   // status word and diagnostics at the start of a workspace
+
+// A workspace, from its start: the status words, then what every call finds
+// zero and leaves zero (the arrival counters of tiles whose K is shared, the
+// balance loss's totals), then what a call may leave anything in (partial
+// sums).  Each has a range of its own, the same for every entry point, so one
+// workspace serves them in any order.
+constexpr size_t kWorkspaceHeader = 256;   // status word and diagnostics
+constexpr size_t kCounterBytes = 8192;
+constexpr int kMaxBalanceExperts = 1024;
+constexpr size_t kBalanceAt = kWorkspaceHeader + kCounterBytes;
+constexpr size_t kBalanceBytes = static_cast<size_t>(kMaxBalanceExperts) * 12 + 256;
+constexpr size_t kScratchAt = kBalanceAt + kBalanceBytes;
+static_assert(kBalanceAt % 256 == 0 && kScratchAt % 256 == 0, "ranges start on 256 bytes");
 
 // The current device; TCG_ERR_ARCH when it is not sm_103.
 tcg_status device(Device& out);

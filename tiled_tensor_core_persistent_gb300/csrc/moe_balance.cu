@@ -31,11 +31,11 @@
 
 namespace {
 
-constexpr int kMaxExperts = 1024;
+constexpr int kMaxExperts = tcg::host::kMaxBalanceExperts;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr double kFixed = 4294967296.0;   // 2^32
-constexpr size_t kTotalBytes = static_cast<size_t>(kMaxExperts) * 12 + 16;
+static_assert(kMaxExperts * 12 + 8 <= tcg::host::kBalanceBytes, "the totals fit their range of the workspace");
 // rows that a warp has on their way at once, by chunks of eight values a lane
 __host__ __device__ constexpr int rows_in_flight(int chunks) { return chunks == 2 ? 2 : 1; }
 
@@ -453,7 +453,7 @@ tcg_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ?
 
 extern "C" {
 
-size_t tcg_moe_balance_workspace_size(void) { return tcg::host::kWorkspaceHeader + kTotalBytes; }
+size_t tcg_moe_balance_workspace_size(void) { return tcg::host::kScratchAt; }
 
 tcg_status tcg_moe_balance(int tokens, int experts, int k, tcg_dtype dtype, const void* logits, int ld,
                            const int* topk, int ld_topk, const uint8_t* mask, float coef, int* counts, int* offsets,
@@ -475,10 +475,10 @@ tcg_status tcg_moe_balance(int tokens, int experts, int k, tcg_dtype dtype, cons
     p.valid = num_valid;
     p.loss = loss;
     char* ws = static_cast<char*>(workspace);
-    p.arrivals = reinterpret_cast<int*>(ws + 128);
-    p.total_p = reinterpret_cast<unsigned long long*>(ws + tcg::host::kWorkspaceHeader);
+    p.total_p = reinterpret_cast<unsigned long long*>(ws + tcg::host::kBalanceAt);
     p.total_c = reinterpret_cast<int*>(p.total_p + kMaxExperts);
     p.total_n = p.total_c + kMaxExperts;
+    p.arrivals = p.total_n + 1;
     const int chunks = chunks_of(experts);
     const int per_cta = kWarps * (32 / lanes_of(experts)) * rows_in_flight(chunks);
     const int ctas = std::max(1, std::min(dev.num_sms, (tokens + per_cta - 1) / per_cta));
