@@ -159,10 +159,13 @@ tcg_status tcg_arch_status(int major, int minor);
 
 /*
  * tcg_workspace_size -- bytes of device workspace tcg_gemm needs for this
- * problem on the current device: a 256-byte status/counter header plus, when
- * the planner splits K (skinny shapes), fp32 partial tiles and per-tile
- * arrival counters.  The workspace must be zero-filled once when allocated
- * (tcg_workspace_init); the library leaves it in that state after every call.
+ * problem on the current device: a status header, the ranges that every call
+ * finds zero and leaves zero (arrival counters among them; 21 KiB with the
+ * header) and, when the planner splits K (skinny shapes), fp32 partial tiles.
+ * The workspace must be zero-filled once when allocated (tcg_workspace_init).
+ * What calls need zero they leave zero, and partial tiles, packed copies and
+ * tables lie past that, so calls on one stream may share one workspace,
+ * whatever their sizes and entry points, with the largest of their sizes.
  * Returns 0 only for invalid sizes.
  */
 size_t tcg_workspace_size(int M, int N, int K, tcg_dtype ab_dtype);
@@ -282,10 +285,11 @@ int tcg_debug_schedule(int M, int N, int K, tcg_dtype ab_dtype, int num_sms, int
  * or latency-critical loops where cudaMalloc/cudaFree are not allowed.
  * The reference pages have no counterpart; this is a property of the library.
  *   Arguments: as tcg_gemm, without the workspace.  It allocates nothing.
- *   Scratch: a 32 MiB file-scope device array held by every GPU that loads
- *     the library until the process exits.  Problems whose workspace
- *     (tcg_workspace_size_for) exceeds 32 MiB return TCG_ERR_WORKSPACE with
- *     a message in tcg_last_error.
+ *   Scratch: a file-scope device array held by every GPU that loads the
+ *     library until the process exits, with 32 MiB for partial tiles and
+ *     packed copies.  Problems that need more (tcg_workspace_size_for less
+ *     tcg_workspace_size(1, 1, 1, ...)) return TCG_ERR_WORKSPACE with a
+ *     message in tcg_last_error.
  *   Set-up: the first call on each device (with that device current) looks
  *     up the array's device address; make that first call before any stream
  *     capture.
@@ -338,9 +342,9 @@ typedef struct {
 
 /*
  * tcg_grouped_workspace_size -- bytes of workspace tcg_gemm_grouped needs for
- * num_problems problems: the 256-byte status header plus a table of one
- * parameter block per problem (tensor maps, sizes, pointers) and the first
- * unit of each.  Zero-fill it once (tcg_workspace_init).  0 if num_problems < 0.
+ * num_problems problems: the status header and the ranges kept zero
+ * (tcg_workspace_size) plus a table of one parameter block per problem (tensor
+ * maps, sizes, pointers) and the first unit of each.  Zero-fill it once (tcg_workspace_init).  0 if num_problems < 0.
  */
 size_t tcg_grouped_workspace_size(int num_problems);
 
@@ -483,9 +487,9 @@ typedef struct {
  * otherwise tcg_gemm_block128_grouped with M rows in all
  * (tcg_gemm_block128_grouped_k needs 256 bytes).  Zero-fill it once
  * (tcg_workspace_init).  Calls leave zero what calls need zero, and the partial
- * sums lie past that, so calls on one stream may share one workspace, these
- * three and tcg_moe_balance among themselves in any order, with the largest of
- * their sizes (fewer rows can need more).  0 for invalid sizes.
+ * sums lie past that, so calls on one stream may share one workspace, in any
+ * order and with any other entry point, with the largest of their sizes (fewer
+ * rows can need more).  0 for invalid sizes.
  */
 size_t tcg_block128_workspace_size(int num_groups, int M, int N, int K);
 
@@ -552,8 +556,8 @@ tcg_status tcg_gemm_block128_grouped_k(int num_groups, const int* offsets, int M
  * NULL), num_valid (n) and loss (fp32), all device memory.  The loss is the
  * same every time (the sums are integers).  experts <= 1024 (else
  * TCG_ERR_UNSUPPORTED).  workspace: tcg_moe_balance_workspace_size bytes,
- * zero-filled once; calls that share it must be ordered (the block-scaled
- * products may be among them).
+ * zero-filled once; calls that share it, other entry points' too, must be
+ * ordered.
  */
 size_t tcg_moe_balance_workspace_size(void);
 tcg_status tcg_moe_balance(int tokens, int experts, int k, tcg_dtype dtype, const void* logits, int ld,

@@ -107,6 +107,55 @@ class Balance:
         assert abs(float(self.loss) - want) <= (E / 8 + 16 + T / 100 + E / 16 + 232) * 2.0 ** -24 * want
 
 
+class Dense:
+    """tcg_gemm in bf16: K split (few tiles), whole tiles, or operands that are packed first."""
+
+    def __init__(self, M, N, K, seed, lda=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.size, self.lda = (M, N, K), lda or K
+        A = torch.zeros(M, self.lda, dtype=torch.bfloat16, device="cuda")
+        A[:, :K] = torch.randint(-4, 5, (M, K), generator=g, device="cuda")
+        B = torch.randint(-4, 5, (N, K), generator=g, device="cuda").to(torch.bfloat16)
+        self.A, self.B = A, B
+        self.want = A[:, :K].double() @ B.double().t()
+        self.D = torch.empty(M, N, device="cuda")
+
+    def need(self):
+        M, N, K = self.size
+        return tcg.workspace_size_for(M, N, K, "bf16", self.A, self.lda, "row", self.B, K, "col")
+
+    def run(self, ws):
+        M, N, K = self.size
+        self.D.fill_(9.0)
+        tcg.gemm(M, N, K, 1.0, self.A, self.lda, "row", self.B, K, "col", 0.0, None, N, "f32", self.D, N, "f32", workspace=ws,
+                 workspace_bytes=ws.numel())
+
+    def check(self):
+        assert torch.equal(self.D.double(), self.want)
+
+
+class DenseGrouped:
+    """tcg_gemm_grouped: its table of problems lives in the workspace."""
+
+    def __init__(self, sizes, seed):
+        self.parts = [Dense(*s, seed + i) for i, s in enumerate(sizes)]
+
+    def need(self):
+        return tcg.grouped_workspace_size(len(self.parts))
+
+    def run(self, ws):
+        problems = []
+        for d in self.parts:
+            M, N, K = d.size
+            d.D.fill_(9.0)
+            problems.append(dict(M=M, N=N, K=K, A=d.A, lda=K, B=d.B, ldb=K, D=d.D, ldd=N))
+        tcg.gemm_grouped(problems, "row", "col", 0.0, "f32", "f32", workspace=ws, workspace_bytes=ws.numel())
+
+    def check(self):
+        for d in self.parts:
+            d.check()
+
+
 def share(calls):
     """Every ordered pair of the calls on one workspace that is zero-filled once."""
     ws = torch.zeros(max(c.need() for c in calls), dtype=torch.uint8, device="cuda")
@@ -122,3 +171,9 @@ def share(calls):
 def test_block_scaled_products_and_the_balance_loss_share_a_workspace():
     share([Block(16, 1500, 8192, 1), Block(120, 300, 9000, 3, 1), Grouped([3, 0, 1, 9, 2], 700, 4096, 5), Balance(4000, 100, 4, 7),
            Balance(20, 9, 2, 8), Block(2048, 2560, 512, 9)])
+
+
+def test_every_entry_point_shares_a_workspace():
+    share([Dense(16, 4096, 8192, 11), Dense(500, 300, 4096, 12), Dense(333, 290, 201, 13, lda=202), Dense(300, 2000, 2500, 14, lda=2501),
+           DenseGrouped([(100, 300, 128), (7, 260, 512), (64, 128, 256)], 15), Block(16, 1500, 8192, 1), Grouped([3, 0, 1, 9, 2], 700, 4096, 5),
+           Balance(4000, 100, 4, 7)])

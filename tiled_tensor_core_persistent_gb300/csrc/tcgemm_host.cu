@@ -39,7 +39,7 @@ int g_force_splits = 0;
 int g_force_cta2 = 0;
 constexpr long long kDefaultTimeoutNs = 2000000000LL;  // 2 s
 
-constexpr size_t kHeaderBytes = 256;  // status word + diagnostics
+constexpr size_t kHeaderBytes = tcg::host::kWorkspaceHeader;
 
 // Planner overrides for tuning experiments (environment, read once):
 // TCG_GROUP_M = raster group in M blocks, TCG_STAGES = pipeline depth cap.
@@ -596,10 +596,22 @@ size_t counter_bytes(const Plan& pl) {
     return (static_cast<size_t>(pl.num_m) * pl.num_n * pl.cluster * sizeof(int) + 255) / 256 * 256;
 }
 
+// Where a plan's counters lie: in the range that every entry point finds and
+// leaves zero, which holds those of any plan the heuristics choose (at most
+// one tile a CTA).  Forced splits of more tiles than that, a test knob, have
+// them in front of their partials and need a workspace of their own.
+size_t counters_at(const Plan& pl) {
+    return counter_bytes(pl) <= tcg::host::kCounterBytes ? tcg::host::kWorkspaceHeader : tcg::host::kScratchAt;
+}
+size_t partials_at(const Plan& pl) {
+    return tcg::host::kScratchAt + (counters_at(pl) == tcg::host::kScratchAt ? counter_bytes(pl) : 0);
+}
+
 // Workspace of one tcg_gemm call, in the order it is laid out: the status
-// header, then the split-K arrival counters and fp32 partials of its plan
-// (`base`), then the packed copies of A and B that the TMA cannot address as
-// stored (block-scaled operands are never packed: they must be aligned).
+// words and the ranges kept zero (host.h), then the split-K fp32 partials of
+// its plan (`base`), then the packed copies of A and B that the TMA cannot
+// address as stored (block-scaled operands are never packed: they must be
+// aligned).
 struct WorkspaceNeed {
     size_t base = 0, pack_a = 0, pack_b = 0;
     size_t total() const { return base + pack_a + pack_b; }
@@ -608,12 +620,13 @@ struct WorkspaceNeed {
 WorkspaceNeed workspace_need(const Plan& pl, int M, int N, int K, tcg_dtype ab, const void* A, int lda,
                              tcg_layout opA, const void* B, int ldb, tcg_layout opB) {
     WorkspaceNeed w;
-    w.base = kHeaderBytes + counter_bytes(pl) + partial_bytes(pl);
     if (K > 0 && !is_mx(ab)) {
         const int eb = elem_bytes(ab);
         w.pack_a = pack_bytes(M, K, opA, A, lda, eb);
         w.pack_b = pack_bytes(K, N, opB, B, ldb, eb);
     }
+    // (a call that neither splits nor packs uses the status words alone)
+    w.base = any_split(pl) || w.pack_a + w.pack_b > 0 ? partials_at(pl) + partial_bytes(pl) : kHeaderBytes;
     return w;
 }
 
@@ -805,7 +818,8 @@ size_t tcg_workspace_size(int M, int N, int K, tcg_dtype ab_dtype) {
     if (use_swap(M, N, ab_dtype, TCG_ROW))
         base = std::max(base, workspace_need(make_plan(N, M, K, ab_dtype, dev, -1, true, true), M, N, K, ab_dtype,
                                              nullptr, 0, TCG_ROW, nullptr, 0, TCG_COL).base);
-    return base;
+    // room in front of the packed copies that tcg_workspace_size_for adds
+    return std::max(base, tcg::host::kScratchAt);
 }
 
 size_t tcg_workspace_size_for(int M, int N, int K, tcg_dtype ab_dtype, const void* A, int lda, tcg_layout opA,
@@ -1020,10 +1034,10 @@ tcg_status tcg_gemm(int M, int N, int K, float alpha, const void* A, int lda, tc
     kp.stages = pl.stages;
     char* ws = static_cast<char*>(workspace);
     kp.status = reinterpret_cast<int*>(ws);
-    kp.tile_counters = any_split(pl) ? reinterpret_cast<int*>(ws + kHeaderBytes) : nullptr;
+    kp.tile_counters = any_split(pl) ? reinterpret_cast<int*>(ws + counters_at(pl)) : nullptr;
     kp.num_slots = static_cast<int>(partial_slots(pl));
     kp.num_counters = any_split(pl) ? pl.num_m * pl.num_n * pl.cluster : 0;
-    kp.partials = any_split(pl) ? reinterpret_cast<float*>(ws + kHeaderBytes + counter_bytes(pl)) : nullptr;
+    kp.partials = any_split(pl) ? reinterpret_cast<float*>(ws + partials_at(pl)) : nullptr;
     kp.timeout_ns = g_timeout_ns > 0 ? g_timeout_ns : kDefaultTimeoutNs;
     kp.fault_inject = g_fault_inject;
     kp.stats = g_env_stats ? reinterpret_cast<unsigned long long*>(ws + 64) : nullptr;
@@ -1142,7 +1156,7 @@ tcg_status tcg_device_status(void* workspace, void* stream_) {
 
 namespace {
 
-constexpr size_t kNoAllocScratchBytes = size_t(32) << 20;  // 32 MiB
+constexpr size_t kNoAllocScratchBytes = (size_t(32) << 20) + tcg::host::kScratchAt;  // 32 MiB of partials and copies
 
 // Device-side scratch.  In host code this name is only a stand-in for the
 // symbol, never a device address: the address is taken once per device with
@@ -1198,7 +1212,10 @@ extern "C" tcg_status tcg_gemm_noalloc(int M, int N, int K, float alpha, const v
     // The array keeps the previous call's contents: the status word and the
     // split-K arrival counters must start at zero.
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    e = cudaMemsetAsync(scratch, 0, kHeaderBytes + counter_bytes(pl), stream);
+    const bool in_line = counters_at(pl) == kHeaderBytes;   // one fill reaches both
+    e = cudaMemsetAsync(scratch, 0, kHeaderBytes + (in_line ? counter_bytes(pl) : 0), stream);
+    if (e == cudaSuccess && !in_line)
+        e = cudaMemsetAsync(static_cast<char*>(scratch) + counters_at(pl), 0, counter_bytes(pl), stream);
     if (e != cudaSuccess) return fail_launch("cudaMemsetAsync(scratch)", e);
     return tcg_gemm(M, N, K, alpha, A, lda, opA, B, ldb, opB, beta, C, ldc, c_dtype, D, ldd, d_dtype, epi, ab_dtype,
                     scales, scratch, kNoAllocScratchBytes, stream_);
@@ -1236,7 +1253,7 @@ tcg_status grouped_validate(int G, const tcg_problem* problems, tcg_layout opA, 
 
 extern "C" size_t tcg_grouped_workspace_size(int num_problems) {
     if (num_problems < 0) return 0;
-    return kHeaderBytes + grouped_table_bytes(num_problems);
+    return tcg::host::kScratchAt + grouped_table_bytes(num_problems);
 }
 
 extern "C" tcg_status tcg_grouped_plan(int num_problems, const tcg_problem* problems, tcg_dtype ab_dtype,
@@ -1269,7 +1286,7 @@ extern "C" tcg_status tcg_gemm_grouped(int num_problems, const tcg_problem* prob
     if ((st = arch_check(dev)) != TCG_OK) return st;
     const int n = static_cast<int>(live.size());
     const size_t table = grouped_table_bytes(n);
-    if (!workspace || !aligned16(workspace) || workspace_bytes < kHeaderBytes + table) return TCG_ERR_WORKSPACE;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < tcg::host::kScratchAt + table) return TCG_ERR_WORKSPACE;
     std::vector<int> tiles;
     const Plan pl = make_grouped_plan(live, ab_dtype, dev, &tiles);
     long long total = 0;
@@ -1360,13 +1377,13 @@ extern "C" tcg_status tcg_gemm_grouped(int num_problems, const tcg_problem* prob
     memcpy(host.data() + static_cast<size_t>(n) * sizeof(tcg::KernelParams), tile0.data(),
            static_cast<size_t>(n + 1) * sizeof(int));
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-    cudaError_t e = cudaMemcpyAsync(ws + kHeaderBytes, host.data(), table, cudaMemcpyHostToDevice, stream);
+    cudaError_t e = cudaMemcpyAsync(ws + tcg::host::kScratchAt, host.data(), table, cudaMemcpyHostToDevice, stream);
     if (e != cudaSuccess) return fail_launch("cudaMemcpyAsync(grouped table)", e);
 
     tcg::KernelParams kp = base;
     kp.num_units = kp.units_a = pl.units;
-    kp.group = reinterpret_cast<const tcg::KernelParams*>(ws + kHeaderBytes);
-    kp.group_tile0 = reinterpret_cast<const int*>(ws + kHeaderBytes + static_cast<size_t>(n) * sizeof(tcg::KernelParams));
+    kp.group = reinterpret_cast<const tcg::KernelParams*>(ws + tcg::host::kScratchAt);
+    kp.group_tile0 = reinterpret_cast<const int*>(ws + tcg::host::kScratchAt + static_cast<size_t>(n) * sizeof(tcg::KernelParams));
     kp.num_groups = n;
     kp.M = kp.N = kp.K = 1;   // launch-wide sizes are unused; the problems carry their own
     const char* what = "launch";
