@@ -209,8 +209,11 @@ tcg_status tcg_gemm(int M, int N, int K, float alpha,
 /*
  * tcg_device_status -- synchronises `stream`, reads the workspace status word
  * (TCG_OK, TCG_ERR_TIMEOUT, or in the debug build TCG_ERR_CHECK) written by
- * earlier tcg_gemm calls on this workspace, and clears it.  Returns
- * TCG_ERR_LAUNCH if the stream itself reports a CUDA error.
+ * earlier calls on this workspace, and clears it, with the arrival counters
+ * that a call which ended so may have left counting: the outputs of the calls
+ * since the last read are then not to be used, and the workspace is ready for
+ * the next call without another zero-fill.  Returns TCG_ERR_LAUNCH if the
+ * stream itself reports a CUDA error.
  *
  * Debug build: libtcgemm_debug.so (the same sources compiled with
  * TCG_DEBUG_CHECKS) checks the kernel's pipeline bookkeeping on the device:

@@ -177,3 +177,25 @@ def test_every_entry_point_shares_a_workspace():
     share([Dense(16, 4096, 8192, 11), Dense(500, 300, 4096, 12), Dense(333, 290, 201, 13, lda=202), Dense(300, 2000, 2500, 14, lda=2501),
            DenseGrouped([(100, 300, 128), (7, 260, 512), (64, 128, 256)], 15), Block(16, 1500, 8192, 1), Grouped([3, 0, 1, 9, 2], 700, 4096, 5),
            Balance(4000, 100, 4, 7)])
+
+
+@pytest.mark.parametrize("which", ["dense", "few rows", "one tile", "grouped"])
+def test_a_call_after_one_whose_waits_ran_out_is_exact(which):
+    """The test knob lets the first CTA's producer skip its first stage, so
+    some tiles' pieces arrive and others do not; reading the status makes the
+    workspace ready again without another zero-fill, its counters included
+    (the first 8448 bytes hold the status words and the counters)."""
+    make = dict(dense=lambda s: Dense(16, 4096, 8192, s), **{
+        "few rows": lambda s: Block(4, 900, 8192, s), "one tile": lambda s: Block(120, 300, 9000, s),
+        "grouped": lambda s: Grouped([3, 0, 1, 9, 2], 700, 4096, s)})[which]
+    calls = [make(s) for s in (1, 11, 21)]      # other operands: sums left over from one call are wrong for the next
+    ws = torch.zeros(calls[0].need(), dtype=torch.uint8, device="cuda")
+    tcg.debug_set(fault_inject=1, wait_timeout_ns=200_000_000)
+    calls[0].run(ws)
+    assert tcg.device_status(ws) == 7
+    tcg.debug_set()
+    assert not bool(ws[:256 + 8192].any())
+    for call in calls[1:] + calls:
+        call.run(ws)
+        assert tcg.device_status(ws) == 0
+        call.check()

@@ -126,6 +126,7 @@ __device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, const Param
             if (t0 == 0) t0 = now;
             if (static_cast<long long>(now - t0) > p.timeout_ns) {
                 *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
+                if (p.stream) p.status[3] = 1;   // shared tiles' counters may be left counting
                 if (atomicCAS(p.status, 0, kStatusTimeout) == 0) {
                     p.status[1] = where;
                     p.status[2] = static_cast<int>(blockIdx.x);

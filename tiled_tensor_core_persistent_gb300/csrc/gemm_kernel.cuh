@@ -127,7 +127,7 @@ struct KernelParams {
     int stages;
     float* partials;      // split-K partials: [slot * ranks + rank][BN][kBM] (row fastest), slot from partial_slot()
     int* tile_counters;   // split-K arrival counters [tile * ranks + rank]
-    int* status;          // [0] status, [1] where, [2] block
+    int* status;          // [0] status, [1] where, [2] block, [3] whether arrival counters may be left counting
     int num_slots;        // partial slots in the workspace (debug-build checks)
     int num_counters;     // tile arrival counters in the workspace (debug-build checks)
     long long timeout_ns;
@@ -179,6 +179,7 @@ struct alignas(16) SmemCtl {
 };
 
 __device__ __forceinline__ void record_timeout(const KernelParams& p, int where) {
+    if (p.tile_counters) p.status[3] = 1;
     if (atomicCAS(p.status, 0, kStatusTimeout) == 0) {
         p.status[1] = where;
         p.status[2] = static_cast<int>(blockIdx.x);
@@ -192,9 +193,12 @@ __device__ __forceinline__ void record_timeout(const KernelParams& p, int where)
 __device__ __forceinline__ bool dcheck(bool cond, const KernelParams& p, SmemCtl* ctl, int where) {
     if constexpr (kChecks) {
         if (!__all_sync(0xffffffffu, cond)) {
-            if ((threadIdx.x & 31) == 0 && atomicCAS(p.status, 0, kStatusCheck) == 0) {
-                p.status[1] = where;
-                p.status[2] = static_cast<int>(blockIdx.x);
+            if ((threadIdx.x & 31) == 0) {
+                if (p.tile_counters) p.status[3] = 1;
+                if (atomicCAS(p.status, 0, kStatusCheck) == 0) {
+                    p.status[1] = where;
+                    p.status[2] = static_cast<int>(blockIdx.x);
+                }
             }
             *reinterpret_cast<volatile int*>(&ctl->abort_flag) = 1;
             return false;

@@ -1133,7 +1133,11 @@ tcg_status tcg_device_status(void* workspace, void* stream_) {
         else
             snprintf(buf, sizeof buf, "device wait ran out (role/stage code %d, block %d)", words[1], words[2]);
         g_last_error = buf;
+        // Tiles whose last piece never came have left their arrival counters
+        // counting: those start at zero again with the status words.
         e = cudaMemset(workspace, 0, sizeof words);
+        if (e == cudaSuccess && words[3] != 0)
+            e = cudaMemset(static_cast<char*>(workspace) + tcg::host::kWorkspaceHeader, 0, tcg::host::kCounterBytes);
         if (e != cudaSuccess) return fail_launch("cudaMemset(status)", e);
         return static_cast<tcg_status>(words[0]);
     }
