@@ -3,7 +3,6 @@
 #include <algorithm>
 #include <climits>
 #include <cstring>
-#include <mutex>
 
 #include "block128_kernel.cuh"
 #include "host.h"
@@ -74,14 +73,14 @@ template <int TN, bool kPair, bool kSwap, bool kCol>
 tcg_status launch(Params& p, const Plan& pl, const tcg::host::Device& dev, cudaStream_t stream) {
     using S = tcg::b128::Shape<TN, kPair, kSwap, kCol>;
     auto* kernel = tcg::b128::block128_kernel<TN, kPair, kSwap, kCol>;
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [&] {
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    static tcg::host::OncePerDevice once;
+    const cudaError_t err = once([&] {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
         cudaFuncAttributes a;
-        if (err == cudaSuccess) err = cudaFuncGetAttributes(&a, kernel);
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
         // the register hand-over draws on what the block is launched with
-        if (err == cudaSuccess && S::kSplitRegs && a.numRegs < S::kLaunchRegs) err = cudaErrorInvalidConfiguration;
+        if (e == cudaSuccess && S::kSplitRegs && a.numRegs < S::kLaunchRegs) e = cudaErrorInvalidConfiguration;
+        return e;
     });
     if (err != cudaSuccess) return tcg::host::fail_launch("tcg_gemm_block128 kernel attributes", err);
     const int groups = p.mode == tcg::b128::kDense ? 0 : p.num_groups;

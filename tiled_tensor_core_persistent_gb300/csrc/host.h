@@ -8,6 +8,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/tcgemm.h"
 
@@ -33,6 +34,27 @@ constexpr size_t kBalanceAt = kWorkspaceHeader + kCounterBytes;
 constexpr size_t kBalanceBytes = static_cast<size_t>(kMaxBalanceExperts) * 12 + 256;
 constexpr size_t kScratchAt = kBalanceAt + kBalanceBytes;
 static_assert(kBalanceAt % 256 == 0 && kScratchAt % 256 == 0, "ranges start on 256 bytes");
+
+// What has to be set up once on each device, a kernel's attributes: f() runs in
+// the first call made with that device current, and its outcome is that
+// device's for good.
+constexpr int kMaxDevices = 64;
+class OncePerDevice {
+public:
+    template <typename F>
+    cudaError_t operator()(F f) {
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+        std::call_once(once_[dev], [&] { err_[dev] = f(); });
+        return err_[dev];
+    }
+
+private:
+    std::once_flag once_[kMaxDevices];
+    cudaError_t err_[kMaxDevices] = {};
+};
 
 // The current device; TCG_ERR_ARCH when it is not sm_103.
 tcg_status device(Device& out);

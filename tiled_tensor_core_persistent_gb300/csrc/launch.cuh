@@ -12,9 +12,9 @@
 #include <cuda_runtime.h>
 
 #include <cstring>
-#include <mutex>
 
 #include "gemm_kernel.cuh"
+#include "host.h"
 
 namespace tcg {
 
@@ -28,16 +28,15 @@ constexpr int kMaxDynamicSmem = 232448;   // 227 KiB per block
 
 template <int BN, bool kFp8, bool kCta2, int KA, int kBlk = 0, bool kGrouped = false, bool kTrans = false>
 cudaError_t set_smem_attr() {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(gemm_persistent_kernel<BN, kFp8, kCta2, KA, kBlk, kGrouped, kTrans>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
+    static host::OncePerDevice once;
+    return once([] {
+        cudaError_t err = cudaFuncSetAttribute(gemm_persistent_kernel<BN, kFp8, kCta2, KA, kBlk, kGrouped, kTrans>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
         if (err == cudaSuccess && kCta2)
             err = cudaFuncSetAttribute(gemm_persistent_kernel<BN, kFp8, kCta2, KA, kBlk, kGrouped, kTrans>,
                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
+        return err;
     });
-    return err;
 }
 
 // One launch; on failure *what names the call that failed.
