@@ -471,7 +471,10 @@ tcg_status tcg_quantize_tiles128(int batch, int rows, int cols, tcg_dtype x_dtyp
  *     scales[(r / scale_rows) * row_stride + kb * k_stride + g * group_stride]
  * with scale_rows = 1 (a scale per row) or 128 (per 128 rows), strides >= 0:
  * both orders of a scale matrix, and the transposed weights of an input
- * gradient, are addressed in place.
+ * gradient, are addressed in place.  r and kb count over the whole operand,
+ * but r over a group's own N rows in the B of tcg_gemm_block128_grouped;
+ * group_stride counts for both operands of the grouped forms (0 where the
+ * groups share one scale matrix).
  */
 typedef struct {
     const void* data;

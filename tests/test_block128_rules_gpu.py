@@ -1,0 +1,75 @@
+"""Rules of the block-scaled operators that only unusual arguments show."""
+import pytest
+import torch
+
+import tiled_tensor_core_persistent_gb300 as tcg
+
+from block128 import ceil_div, pitched, wide64, workspace
+from test_block128_gpu import int_operand, stacked
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from tiled_tensor_core_persistent_gb300 import _build
+    _build.build()
+    tcg.debug_set()
+
+
+@pytest.mark.parametrize("lens,N,K", [([2, 0, 3, 1], 200, 300), ([40, 90, 0, 33], 300, 512), ([300, 700, 256], 2100, 384)])
+def test_group_stride_of_the_rows_operand(lens, N, K):
+    """Every group has a scale matrix of its own for A (a group's rows at
+    their own row numbers in it); what it holds for the other groups' rows is NaN."""
+    G, rows, kb = len(lens), sum(lens), ceil_div(K, 128)
+    codes, scales = int_operand(rows, K, 1, 3)
+    at = [sum(lens[:g]) for g in range(G + 1)]
+    per_group = torch.full((G, kb, rows), float("nan"), device="cuda")
+    for g in range(G):
+        per_group[g, :, at[g]:at[g + 1]] = scales[:, at[g]:at[g + 1]]
+    data, ld = pitched(codes)
+    A = tcg.block_operand(data, ld, per_group, 1, 1, rows, kb * rows)
+    B, values, keep = stacked(G, N, K, 128, 9)
+    offsets = torch.tensor(at, dtype=torch.int32, device="cuda")
+    D = torch.empty(rows, N, device="cuda")
+    n = tcg.block128_workspace_size(G, rows, N, K)
+    ws = workspace(n)
+    tcg.gemm_block128_grouped(G, offsets, rows, N, K, A, B, D, N, "f32", workspace=ws, workspace_bytes=n)
+    assert tcg.device_status(ws) == 0
+    a64 = wide64(codes, scales, 1)
+    assert torch.equal(D.double(), torch.cat([a64[at[g]:at[g + 1]] @ values[g].t() for g in range(G)]))
+
+
+@pytest.mark.parametrize("which", ["A", "B"])
+def test_group_stride_of_weight_gradients(which):
+    lens, M, N = [100, 0, 300], 200, 130
+    G, at = len(lens), [0, 100, 100, 400]
+    padded = sum(ceil_div(n, 128) for n in lens) * 128
+    kb = padded // 128
+    ops = {"A": int_operand(M, padded, 1, 1), "B": int_operand(N, padded, 1, 2)}
+    want = [wide64(*ops[k], 1) for k in "AB"]
+    held, keep = {}, []
+    for name, (codes, scales) in ops.items():
+        r = codes.shape[0]
+        data, ld = pitched(codes)
+        if name == which:
+            factor = torch.tensor([1.0, 2.0, 4.0], device="cuda")[:, None, None]
+            scales = (scales[None] * factor).contiguous()
+            held[name] = tcg.block_operand(data, ld, scales, 1, 1, r, kb * r)
+        else:
+            held[name] = tcg.block_operand(data, ld, scales, 1, 1, r)
+        keep += [data, scales]
+    D = torch.empty(G, M, N, device="cuda")
+    offsets = torch.tensor(at, dtype=torch.int32, device="cuda")
+    ws = workspace(256)
+    tcg.gemm_block128_grouped_k(G, offsets, M, N, padded, held["A"], held["B"], 0.0, None, N, "f32", D, N, "f32", workspace=ws,
+                                workspace_bytes=256)
+    assert tcg.device_status(ws) == 0
+    place = 0
+    for g in range(G):
+        n = ceil_div(lens[g], 128) * 128
+        ref = (want[0][:, place:place + n] @ want[1][:, place:place + n].t()) * 2.0 ** g
+        assert torch.equal(D[g].double(), ref)
+        place += n

@@ -150,14 +150,13 @@ tcg_status check_output(int N, float beta, const void* C, int ldc, tcg_dtype c_d
     return TCG_OK;
 }
 
-tcg::b128::ScaleRef scale_ref(const tcg_block_operand& o, int rows) {
+tcg::b128::ScaleRef scale_ref(const tcg_block_operand& o) {
     tcg::b128::ScaleRef s;
     s.ptr = o.scales;
     s.rs = o.row_stride;
     s.ks = o.k_stride;
     s.gs = o.group_stride;
     s.shift = o.scale_rows == 128 ? 7 : 0;
-    s.rows = rows;
     return s;
 }
 
@@ -239,8 +238,8 @@ tcg_status tcg_gemm_block128(int M, int N, int K, tcg_dtype ab_dtype, tcg_block_
     p.M = M;
     p.N = N;
     p.num_kb = static_cast<int>(blocks(K, 128));
-    p.sa = scale_ref(A, M);
-    p.sb = scale_ref(B, N);
+    p.sa = scale_ref(A);
+    p.sb = scale_ref(B);
     p.ab_fmt = format_of(ab_dtype);
     p.bias = epi.bias;
     p.bias_f32 = epi.bias_dtype == TCG_F32;
@@ -275,8 +274,8 @@ tcg_status tcg_gemm_block128_grouped(int num_groups, const int* offsets, int row
     p.num_kb = static_cast<int>(blocks(K, 128));
     p.num_groups = num_groups;
     p.offsets = offsets;
-    p.sa = scale_ref(A, rows);
-    p.sb = scale_ref(B, N);
+    p.sa = scale_ref(A);
+    p.sb = scale_ref(B);
     p.ab_fmt = format_of(ab_dtype);
     set_output(p, 0.0f, nullptr, 0, TCG_F32, D, ldd, d_dtype);
     const Plan pl = make_plan(p.mode, rows, num_groups, rows, N, p.num_kb, dev.num_sms);
@@ -311,8 +310,8 @@ tcg_status tcg_gemm_block128_grouped_k(int num_groups, const int* offsets, int M
     p.num_kb = padded_rows / 128;
     p.num_groups = num_groups;
     p.offsets = offsets;
-    p.sa = scale_ref(A, M);
-    p.sb = scale_ref(B, N);
+    p.sa = scale_ref(A);
+    p.sb = scale_ref(B);
     p.ab_fmt = format_of(ab_dtype);
     set_output(p, beta, C, ldc, c_dtype, D, ldd, d_dtype);
     const Plan pl = make_plan(p.mode, 0, num_groups, M, N, p.num_kb, dev.num_sms);

@@ -54,7 +54,6 @@ struct ScaleRef {
     const float* ptr;
     long long rs, ks, gs;
     int shift;   // 0: one scale per row, 7: one per 128 rows
-    int rows;    // rows of one group (row indices are clamped below it)
 };
 
 struct Params {
@@ -456,10 +455,10 @@ __device__ __forceinline__ int slot_of(const Params& p, const Walk<true>& s, con
     return 2 * c + (begins ? 0 : 1);
 }
 
-// Where the scales of a row start (rows past the operand, or past B's group,
-// take the last one: nobody stores what they scale).
-__device__ __forceinline__ const float* scale_row(const ScaleRef& s, int row, int g) {
-    return s.ptr + static_cast<long long>(min(row, s.rows - 1) >> s.shift) * s.rs + g * s.gs;
+// Where the scales of a row of group g start (rows past the group's last one
+// take that one's: nobody stores what they scale).
+__device__ __forceinline__ const float* scale_row(const ScaleRef& s, int row, int last, int g) {
+    return s.ptr + static_cast<long long>(min(row, last) >> s.shift) * s.rs + g * s.gs;
 }
 
 // ------------------------------------------------------------------ epilogue
@@ -846,13 +845,14 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
         while (ok && walk.template next<S::kTileM, S::kTileNOut>(p, gr, w)) {
             const int l0 = kSwap ? w.n0 : w.m0 + static_cast<int>(rank) * 128;
             const int c0 = kSwap ? w.m0 : w.n0;
+            const int l_last = (kSwap ? p.N : w.m_end) - 1, c_last = (kSwap ? w.m_end : p.N) - 1;
             const float* lp[4];
             const float* cp[kColLoads];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) lp[i] = scale_row(sl, l0 + lane + 32 * i, kSwap ? w.g : 0) + w.kb0 * sl.ks;
+            for (int i = 0; i < 4; ++i) lp[i] = scale_row(sl, l0 + lane + 32 * i, l_last, w.g) + w.kb0 * sl.ks;
 #pragma unroll
             for (int i = 0; i < kColLoads; ++i)
-                cp[i] = scale_row(sc, c0 + (S::kCols ? lane + 32 * i : 128 * lane), kSwap ? 0 : w.g) + w.kb0 * sc.ks;
+                cp[i] = scale_row(sc, c0 + (S::kCols ? lane + 32 * i : 128 * lane), c_last, w.g) + w.kb0 * sc.ks;
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
                 if (!wait_warp(&ctl->scale_empty[slot], phase ^ 1u, p, ctl, 6)) { ok = false; break; }
                 const uint32_t dst = ptx::smem_u32(scale_words + slot * S::kSlotWords + lane);
