@@ -438,7 +438,9 @@ tcg_status tcg_quantize_rows128(int rows, int cols, tcg_dtype x_dtype, const voi
  * every place that holds no row (up to padded_rows) holds code 0.
  * padded_rows: a multiple of 128, at least the sum of the groups' lengths each
  * rounded up to 128 (rows / 128 * 128 + 128 * num_groups always suffices; rows
- * past it are dropped).  offsets NULL: one group of all rows.
+ * past it are dropped).  offsets NULL: one group of all rows.  Offsets without
+ * groups (num_groups = 0), or several groups without offsets:
+ * TCG_ERR_INVALID_ARG.
  *   q: cols x padded_rows, ldq >= padded_rows.
  *   scales: scale of column c, block b at scales[b * ld_scales + c],
  *     ld_scales >= cols.

@@ -1,0 +1,24 @@
+"""What the block-scaled operators and the balance loss refuse, on a machine
+without a GPU: combinations of arguments that would otherwise give a wrong
+answer."""
+import pytest
+
+import tiled_tensor_core_persistent_gb300 as tcg
+from tiled_tensor_core_persistent_gb300 import _build
+
+from test_block128_cpu import INVALID, P, code, cols, no_gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    _build.build()
+    return tcg.lib()
+
+
+def test_offsets_without_groups_are_refused():
+    """Offsets of no groups at all would leave every row out: only padding would be written."""
+    assert code(lambda: cols(offsets=P, num_groups=0)) == INVALID
+    assert code(lambda: cols(num_groups=2)) == INVALID
+    assert no_gpu(lambda: cols(offsets=P, num_groups=1))
+    assert no_gpu(lambda: cols(num_groups=1))
+    assert no_gpu(lambda: cols(num_groups=0))

@@ -516,7 +516,7 @@ tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const voi
     if (st != TCG_OK) return st;
     p.rows = rows;
     if (!q || ldq < padded_rows || ld_scales < cols) return TCG_ERR_INVALID_ARG;
-    if (num_groups > 1 && !offsets) return TCG_ERR_INVALID_ARG;
+    if (offsets ? num_groups == 0 : num_groups > 1) return TCG_ERR_INVALID_ARG;
     if (!offsets && padded_rows < rows) return TCG_ERR_INVALID_ARG;
     if (!aligned(offsets, 4)) return TCG_ERR_MISALIGNED;
     tcg::host::Device dev;
