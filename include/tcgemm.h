@@ -445,8 +445,9 @@ tcg_status tcg_quantize_rows128(int rows, int cols, tcg_dtype x_dtype, const voi
  *   scales: scale of column c, block b at scales[b * ld_scales + c],
  *     ld_scales >= cols.
  *   x, row_index, source_rows: as in tcg_quantize_rows128.
- * Offsets outside [0, rows] are clamped.  num_groups <= 1024, padded_rows <=
- * 65535 * 128 (else TCG_ERR_UNSUPPORTED).
+ * Offsets outside [0, rows] are clamped, and one below an earlier one counts
+ * as that one.  num_groups <= 1024, padded_rows <= 65535 * 128 (else
+ * TCG_ERR_UNSUPPORTED).
  */
 tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx,
                                 const int* row_index, int source_rows,
@@ -528,7 +529,8 @@ tcg_status tcg_gemm_block128(int M, int N, int K, tcg_dtype ab_dtype, tcg_block_
  * non-decreasing row numbers from 0 to at most rows (tcg_moe_balance writes
  * them); they are read by the kernel, so the host never waits for the
  * routing.  Rows of D outside every group are not written; offsets outside
- * [0, rows] are clamped.  num_groups <= 1024 (else TCG_ERR_UNSUPPORTED).
+ * [0, rows] are clamped, and one below an earlier one counts as that one (no
+ * two groups share a row).  num_groups <= 1024 (else TCG_ERR_UNSUPPORTED).
  */
 tcg_status tcg_gemm_block128_grouped(int num_groups, const int* offsets, int rows, int N, int K, tcg_dtype ab_dtype,
                                      tcg_block_operand A, tcg_block_operand B,

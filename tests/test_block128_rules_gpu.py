@@ -4,7 +4,7 @@ import torch
 
 import tiled_tensor_core_persistent_gb300 as tcg
 
-from block128 import ceil_div, pitched, wide64, workspace
+from block128 import ceil_div, operand, pitched, quantize_rows, wide64, workspace
 from test_block128_gpu import int_operand, stacked
 
 pytestmark = pytest.mark.gpu
@@ -72,4 +72,63 @@ def test_group_stride_of_weight_gradients(which):
         n = ceil_div(lens[g], 128) * 128
         ref = (want[0][:, place:place + n] @ want[1][:, place:place + n].t()) * 2.0 ** g
         assert torch.equal(D[g].double(), ref)
+        place += n
+
+
+# offsets that go back: what they stand for (an offset below an earlier one counts as that one)
+TABLES = [([0, 30, 10, 50], [0, 30, 30, 50]), ([5, 3, 60, 60, 2, 70], [5, 5, 60, 60, 60, 70]), ([80, 10, 20, 30], [80, 80, 80, 80])]
+
+
+@pytest.mark.parametrize("given,meant", TABLES)
+def test_offsets_that_go_back(given, meant):
+    G, rows, N, K = len(given) - 1, 80, 200, 256
+    a = int_operand(rows, K, 1, 1)
+    A, ka = operand(*a, 1)
+    B, values, kb = stacked(G, N, K, 128, 5)
+    offsets = torch.tensor(given, dtype=torch.int32, device="cuda")
+    n = tcg.block128_workspace_size(G, rows, N, K)
+    ws = workspace(n)
+    D = torch.full((rows, N), 777.0, device="cuda")
+    tcg.gemm_block128_grouped(G, offsets, rows, N, K, A, B, D, N, "f32", workspace=ws, workspace_bytes=n)
+    assert tcg.device_status(ws) == 0
+    want = torch.full((rows, N), 777.0, dtype=torch.float64, device="cuda")
+    a64 = wide64(*a, 1)
+    for g in range(G):
+        want[meant[g]:meant[g + 1]] = a64[meant[g]:meant[g + 1]] @ values[g].t()
+    assert torch.equal(D.double(), want)
+
+
+@pytest.mark.parametrize("given,meant", TABLES)
+def test_offsets_that_go_back_by_columns(given, meant):
+    """The column quantiser and the weight gradients read such a table the same way."""
+    G, rows, M, N = len(given) - 1, 80, 150, 70
+    padded = 128 * G
+    xa, xb = torch.randn(rows, M, device="cuda"), torch.randn(rows, N, device="cuda")
+    offsets = torch.tensor(given, dtype=torch.int32, device="cuda")
+    ops, keep, wide = [], [], []
+    for x in (xa, xb):
+        c = x.shape[1]
+        q, s = torch.empty(c, padded, dtype=torch.uint8, device="cuda"), torch.empty(G, c, device="cuda")
+        tcg.quantize_cols128(rows, c, x, c, "f32", q, padded, "e4m3", s, c, padded_rows=padded, num_groups=G, offsets=offsets)
+        y = torch.zeros(padded, c, device="cuda")
+        place = 0
+        for g in range(G):
+            n = meant[g + 1] - meant[g]
+            y[place:place + n] = x[meant[g]:meant[g + 1]]
+            place += ceil_div(n, 128) * 128
+        want_q, want_s = quantize_rows(y.t().contiguous())
+        assert torch.equal(s, want_s) and torch.equal(q, want_q.view(torch.uint8))
+        wide.append(wide64(want_q, want_s, 1))
+        ops.append(tcg.block_operand(q, padded, s, 1, 1, c))
+        keep += [q, s]
+    D = torch.empty(G, M, N, device="cuda")
+    ws = workspace(256)
+    tcg.gemm_block128_grouped_k(G, offsets, M, N, padded, ops[0], ops[1], 0.0, None, N, "f32", D, N, "f32", workspace=ws, workspace_bytes=256)
+    assert tcg.device_status(ws) == 0
+    place = 0
+    for g in range(G):
+        n = ceil_div(meant[g + 1] - meant[g], 128) * 128
+        a, b = wide[0][:, place:place + n], wide[1][:, place:place + n]
+        # 128 products and their scaling (132 units of the terms' magnitudes), one k-block
+        assert bool(((D[g].double() - a @ b.t()).abs() <= 136 * 2.0 ** -24 * (a.abs() @ b.abs().t())).all())
         place += n

@@ -36,6 +36,7 @@
 #pragma once
 
 #include "gemm_kernel.cuh"
+#include "groups.cuh"
 #include "host.h"
 
 namespace tcg {
@@ -301,18 +302,18 @@ struct Groups {
     const int* len;     // num_groups
 };
 
-// offsets are clamped into [0, rows], so a table that is not one (a negative
-// length, an offset past the operand) reads and writes nothing out of range.
+// (group_rows: whatever the offsets hold, the groups share the operand's rows
+// out, so every sum here is bounded by the operand's own tiles or k-blocks
+// and one more a group.)
 template <int kTileM>
 __device__ __forceinline__ void build_groups(const Params& p, int* start, int* row0, int* len, int lane) {
-    int base = 0;
+    const int cap = p.mode == kGroupedRows ? p.M : p.num_kb * kBlock;
+    int base = 0, last = 0;
     for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
         const int g = g0 + lane;
-        int n = 0, r = 0;
+        int n, r;
+        group_rows(p.offsets, p.num_groups, cap, g0, lane, last, r, n);
         if (g < p.num_groups) {
-            const int cap = p.mode == kGroupedRows ? p.M : p.num_kb * kBlock;
-            r = min(max(__ldg(p.offsets + g), 0), cap);
-            n = max(min(max(__ldg(p.offsets + g + 1), 0), cap) - r, 0);
             row0[g] = r;
             len[g] = n;
         }

@@ -25,6 +25,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "groups.cuh"
 #include "host.h"
 
 namespace {
@@ -260,16 +261,12 @@ __device__ __forceinline__ void find_block(const Quant& p, int b, int lane, int&
         n = min(128, p.rows - row);
         return;
     }
-    int base = 0;
+    int base = 0, last = 0;
     row = 0;
     n = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
-        const int g = g0 + lane;
-        int r = 0, len = 0;
-        if (g < p.groups) {
-            r = min(max(__ldg(p.offsets + g), 0), p.rows);
-            len = max(min(max(__ldg(p.offsets + g + 1), 0), p.rows) - r, 0);
-        }
+        int r, len;
+        tcg::group_rows(p.offsets, p.groups, p.rows, g0, lane, last, r, len);
         const int blocks = (len + 127) >> 7;
         int incl = blocks;
 #pragma unroll
