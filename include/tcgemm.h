@@ -160,7 +160,7 @@ tcg_status tcg_arch_status(int major, int minor);
 /*
  * tcg_workspace_size -- bytes of device workspace tcg_gemm needs for this
  * problem on the current device: a status header, the ranges that every call
- * finds zero and leaves zero (arrival counters among them; 21 KiB with the
+ * finds zero and leaves zero (arrival counters among them; 37 KiB with the
  * header) and, when the planner splits K (skinny shapes), fp32 partial tiles.
  * The workspace must be zero-filled once when allocated (tcg_workspace_init).
  * What calls need zero they leave zero, and partial tiles, packed copies and

@@ -31,7 +31,7 @@ constexpr size_t kWorkspaceHeader = 256;   // status word and diagnostics
 constexpr size_t kCounterBytes = 8192;
 constexpr int kMaxBalanceExperts = 1024;
 constexpr size_t kBalanceAt = kWorkspaceHeader + kCounterBytes;
-constexpr size_t kBalanceBytes = static_cast<size_t>(kMaxBalanceExperts) * 12 + 256;
+constexpr size_t kBalanceBytes = static_cast<size_t>(kMaxBalanceExperts) * 28 + 256;
 constexpr size_t kScratchAt = kBalanceAt + kBalanceBytes;
 static_assert(kBalanceAt % 256 == 0 && kScratchAt % 256 == 0, "ranges start on 256 bytes");
 

@@ -14,10 +14,11 @@
 // gradient, backward: 5 us for 32768 x 256), in fact by the instructions and
 // latencies of a row's exponentials at that size (forward and backward 29.5 us
 // back to back), and for few tokens by the launch.  P_e sums stay in the registers
-// of the lane that owns the columns.  A CTA's sums are added to 64-bit
-// fixed-point totals in the workspace (2^-32 steps: integer sums do not depend
-// on the order of arrival), which the last CTA reads in one go and leaves at
-// zero; sums of every CTA read back one after the other took 10 us more.
+// of the lane that owns the columns.  A CTA's sums are added to fixed-point
+// totals in the workspace, three 64-bit words an expert (integer sums do not
+// depend on the order of arrival, and 2^-136 steps lose nothing of an fp32 sum
+// above 2^-113), which the last CTA reads in one go and leaves at zero; sums of
+// every CTA read back one after the other took 10 us more.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,8 +35,10 @@ namespace {
 constexpr int kMaxExperts = tcg::host::kMaxBalanceExperts;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr double kFixed = 4294967296.0;   // 2^32
-static_assert(kMaxExperts * 12 + 8 <= tcg::host::kBalanceBytes, "the totals fit their range of the workspace");
+// Words of a total, in units of 2^-32, 2^-84 and 2^-136: the lower ones hold 52
+// bits of each CTA's sum, so that 2^11 CTAs' fit.
+constexpr int kWords = 3, kWordBits = 52;
+static_assert(kMaxExperts * (8 * kWords + 4) + 8 <= tcg::host::kBalanceBytes, "the totals fit their range of the workspace");
 // rows that a warp has on their way at once, by chunks of eight values a lane
 __host__ __device__ constexpr int rows_in_flight(int chunks) { return chunks == 2 ? 2 : 1; }
 
@@ -51,7 +54,7 @@ struct Balance {
     int* offsets;
     int* valid;
     float* loss;
-    unsigned long long* total_p;   // [experts], units of 2^-32
+    unsigned long long* total_p;   // [kWords][kMaxExperts]
     int* total_c;                  // [experts]
     int* total_n;
     int* arrivals;
@@ -177,6 +180,49 @@ __device__ __forceinline__ float exp_row(float (&x)[kC][8]) {
     return s == 0.0f ? 0.0f : 1.0f / s;
 }
 
+// Adds s >= 0 to a total, exactly down to the last word's unit: s is 24 bits
+// from bit b of the fixed-point number on, which reach into two words at most
+// (sums of 2^-8 and more, the ordinary ones, into the first alone).  A sum that
+// is not a number sets the first word's top bit, which totals of at most 2^31
+// tokens never reach.
+__device__ __forceinline__ void add_total(unsigned long long* total, float s) {
+    if (!(s <= 2147483648.0f)) {
+        atomicOr(total, 1ull << 63);
+        return;
+    }
+    const uint32_t bits = __float_as_uint(s) & 0x7FFFFFFFu, e = bits >> 23;
+    unsigned long long m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+    int b = static_cast<int>(e ? e : 1u) - 150 + (32 + (kWords - 1) * kWordBits);
+    if (b < 0) {
+        m = (m + (1ull << (-b - 1))) >> -b;
+        b = 0;
+    }
+    const int word = max(kWords - 1 - b / kWordBits, 0), off = b - (kWords - 1 - word) * kWordBits;
+    unsigned long long here = m << off, above = 0ull;
+    if (word > 0) {
+        above = m >> (kWordBits - off);
+        here &= (1ull << kWordBits) - 1;
+    }
+    if (here) atomicAdd(total + word * kMaxExperts, here);
+    if (above) atomicAdd(total + (word - 1) * kMaxExperts, above);
+}
+
+// The total as a float (its words' sum in 64 bits, rounded once), left at zero.
+__device__ __forceinline__ float take_total(unsigned long long* total) {
+    unsigned long long w[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __ldcg(total + i * kMaxExperts);
+    double v = 0.0;
+#pragma unroll
+    for (int i = kWords - 1; i >= 0; --i) {
+        if (w[i] == 0ull) continue;
+        constexpr double kUnit[kWords] = {0x1p-32, 0x1p-84, 0x1p-136};
+        v += static_cast<double>(w[i]) * kUnit[i];
+        total[i * kMaxExperts] = 0ull;
+    }
+    return w[0] >> 63 ? __int_as_float(0x7FC00000) : static_cast<float>(v);
+}
+
 template <typename T, int kL, int kC>
 __global__ void __launch_bounds__(kThreads) balance_kernel(const __grid_constant__ Balance p) {
     tcg::host::wait_for_kernel_ahead();
@@ -271,11 +317,7 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(const __grid_constant
     const bool alone = gridDim.x == 1;
     if (!alone) {
         for (int e = threadIdx.x; e < p.experts; e += kThreads) {
-            // (a sum that is not a number sets the top bit, which the totals, at most
-            // 2^31 tokens, never reach, and comes out as one)
-            const float s = sums[e];
-            if (s <= 2147483648.0f) atomicAdd(p.total_p + e, static_cast<unsigned long long>(static_cast<double>(s) * kFixed + 0.5));
-            else atomicOr(p.total_p + e, 1ull << 63);
+            add_total(p.total_p + e, sums[e]);
             if (hist[e]) atomicAdd(p.total_c + e, hist[e]);
         }
         if (threadIdx.x == 0 && n_valid) atomicAdd(p.total_n, n_valid);
@@ -289,10 +331,8 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(const __grid_constant
         if (!last) return;
         // The last CTA: the totals, left at zero for the next call.
         for (int e = threadIdx.x; e < p.experts; e += kThreads) {
-            const unsigned long long f = __ldcg(p.total_p + e);
-            sums[e] = f >> 63 ? __int_as_float(0x7FC00000) : static_cast<float>(static_cast<double>(f) * (1.0 / kFixed));
+            sums[e] = take_total(p.total_p + e);
             hist[e] = __ldcg(p.total_c + e);
-            p.total_p[e] = 0ull;
             p.total_c[e] = 0;
         }
         if (threadIdx.x == 0) {
@@ -476,7 +516,7 @@ tcg_status tcg_moe_balance(int tokens, int experts, int k, tcg_dtype dtype, cons
     p.loss = loss;
     char* ws = static_cast<char*>(workspace);
     p.total_p = reinterpret_cast<unsigned long long*>(ws + tcg::host::kBalanceAt);
-    p.total_c = reinterpret_cast<int*>(p.total_p + kMaxExperts);
+    p.total_c = reinterpret_cast<int*>(p.total_p + kWords * kMaxExperts);
     p.total_n = p.total_c + kMaxExperts;
     p.arrivals = p.total_n + 1;
     const int chunks = chunks_of(experts);
