@@ -578,7 +578,8 @@ tcg_status tcg_moe_balance(int tokens, int experts, int k, tcg_dtype dtype, cons
 /*
  * tcg_moe_balance_backward -- dlogits_te = g * coef / n * p_te * (f_e - sum_j
  * f_j p_tj) for g = *grad_loss (device), with counts and num_valid from the
- * forward call; 0 for masked tokens.  The assignments are constants.  Every
+ * forward call; 0 for masked tokens and tokens whose logits are all -inf, even
+ * where g is not finite.  The assignments are constants.  Every
  * row of dlogits (tokens x experts, ldd >= experts, d_dtype TCG_BF16, TCG_F16
  * or TCG_F32) is written; it may be the logits' own memory when the types and
  * leading dimensions agree.

@@ -8,7 +8,7 @@
 //   dlogits_te = g coef / n  p_te (f_e - sum_j f_j p_tj)
 //
 // The assignments are constants of the gradient.  A token whose logits are
-// all -inf has p = 0 (and gradient 0).  Statistics and sums are fp32.
+// all -inf has p = 0, and gradient 0 as masked ones have, whatever g is.  Statistics and sums are fp32.
 //
 // Bound by memory on paper (logits once forward; once more, and their
 // gradient, backward: 5 us for 32768 x 256), in fact by the instructions and
@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(256) balance_grad_kernel(const __grid_constant
 #pragma unroll
             for (int d = 1; d < kL; d <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
             dot *= inv;
-            const float gi = g * inv;
+            // (a row of nothing, masked or all -inf, has gradient 0 whatever g is)
+            const float gi = inv == 0.0f ? 0.0f : g * inv;
             if (t < p.tokens) {
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
