@@ -564,10 +564,10 @@ tcg_status tcg_gemm_block128_grouped_k(int num_groups, const int* offsets, int M
  * p = 0.  Writes counts (experts), offsets (experts + 1: where each expert's
  * rows start when the counted assignments are put in expert order; may be
  * NULL), num_valid (n) and loss (fp32), all device memory.  The loss is the
- * same every time (the sums are integers).  experts <= 1024 (else
- * TCG_ERR_UNSUPPORTED).  workspace: tcg_moe_balance_workspace_size bytes,
- * zero-filled once; calls that share it, other entry points' too, must be
- * ordered.
+ * same every time (the sums are integers).  experts <= 1024 and
+ * tokens * k < 2^31 (else TCG_ERR_UNSUPPORTED).  workspace:
+ * tcg_moe_balance_workspace_size bytes, zero-filled once; calls that share it,
+ * other entry points' too, must be ordered.
  */
 size_t tcg_moe_balance_workspace_size(void);
 tcg_status tcg_moe_balance(int tokens, int experts, int k, tcg_dtype dtype, const void* logits, int ld,

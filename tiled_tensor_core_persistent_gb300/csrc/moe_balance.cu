@@ -502,6 +502,8 @@ tcg_status tcg_moe_balance(int tokens, int experts, int k, tcg_dtype dtype, cons
     Balance p = {};
     tcg_status st = start(p, tokens, experts, k, dtype, logits, ld, mask, coef);
     if (st != TCG_OK) return st;
+    // (counts and offsets are ints)
+    if (static_cast<long long>(tokens) * k > INT_MAX) return TCG_ERR_UNSUPPORTED;
     if (!counts || !num_valid || !loss || (tokens > 0 && (!topk || ld_topk < k))) return TCG_ERR_INVALID_ARG;
     if (!aligned(topk, 4) || !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(num_valid, 4) || !aligned(loss, 4))
         return TCG_ERR_MISALIGNED;
