@@ -132,3 +132,58 @@ def test_offsets_that_go_back_by_columns(given, meant):
         # 128 products and their scaling (132 units of the terms' magnitudes), one k-block
         assert bool(((D[g].double() - a @ b.t()).abs() <= 136 * 2.0 ** -24 * (a.abs() @ b.abs().t())).all())
         place += n
+
+
+@pytest.mark.parametrize("scale_rows", [1, 128])
+@pytest.mark.parametrize("G,rows,N", [(1024, 1500, 40), (1000, 50000, 136), (800, 4000, 300)])
+def test_as_many_groups_as_the_tables_hold(G, rows, N, scale_rows):
+    """Few-row, single and pair tiles next to the tables of many groups: every
+    row of D, and the weight gradients, exact."""
+    K = 128
+    g = torch.Generator().manual_seed(G)
+    cuts = torch.sort(torch.randint(0, rows + 1, (G - 1,), generator=g)).values.tolist()
+    at = [0] + cuts + [rows]
+    a, (bc, bs) = int_operand(rows, K, 1, 1), int_operand(G * N, K, 1, 2)
+    A, ka = operand(*a, 1)
+    data, ld = pitched(bc)
+    if scale_rows == 1:
+        B = tcg.block_operand(data, ld, bs, 1, 1, G * N, N)
+        wide = wide64(bc, bs, 1)
+    else:
+        nb = ceil_div(N, 128)
+        tiles = torch.exp2(torch.randint(-1, 2, (G, nb), generator=g).float()).cuda()
+        B = tcg.block_operand(data, ld, tiles, 128, 1, 1, nb)
+        wide = wide64(bc, tiles.repeat_interleave(128, 1)[:, :N].reshape(1, G * N), 1)
+    offsets = torch.tensor(at, dtype=torch.int32, device="cuda")
+    n = tcg.block128_workspace_size(G, rows, N, K)
+    ws = workspace(n)
+    D = torch.full((rows, N), 777.0, device="cuda")
+    tcg.gemm_block128_grouped(G, offsets, rows, N, K, A, B, D, N, "f32", workspace=ws, workspace_bytes=n)
+    assert tcg.device_status(ws) == 0
+    owner = torch.searchsorted(offsets[1:].contiguous(), torch.arange(rows, device="cuda", dtype=torch.int32), right=True)
+    a64, wide = wide64(*a, 1), wide.view(G, N, K)
+    for r0 in range(0, rows, 2000):
+        r = slice(r0, min(rows, r0 + 2000))
+        assert torch.equal(D[r].double(), torch.einsum("rk,rnk->rn", a64[r], wide[owner[r]]))
+
+
+@pytest.mark.parametrize("G,M,N", [(1024, 130, 140), (300, 300, 520), (1024, 40, 20)])
+def test_weight_gradients_of_as_many_groups_as_the_tables_hold(G, M, N):
+    g = torch.Generator().manual_seed(G + M)
+    lens = torch.randint(0, 3, (G,), generator=g).tolist()
+    at = [sum(lens[:i]) for i in range(G + 1)]
+    padded = sum(ceil_div(n, 128) for n in lens) * 128
+    a, b = int_operand(M, padded, 1, 1), int_operand(N, padded, 1, 2)
+    A, ka = operand(*a, 1)
+    B, kb = operand(*b, 1)
+    offsets = torch.tensor(at, dtype=torch.int32, device="cuda")
+    D = torch.empty(G, M, N, device="cuda")
+    ws = workspace(256)
+    tcg.gemm_block128_grouped_k(G, offsets, M, N, padded, A, B, 0.0, None, N, "f32", D, N, "f32", workspace=ws, workspace_bytes=256)
+    assert tcg.device_status(ws) == 0
+    a64, b64 = wide64(*a, 1), wide64(*b, 1)
+    place = 0
+    for i in range(G):
+        n = ceil_div(lens[i], 128) * 128
+        assert torch.equal(D[i].double(), a64[:, place:place + n] @ b64[:, place:place + n].t())
+        place += n

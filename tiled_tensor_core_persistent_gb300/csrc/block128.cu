@@ -75,7 +75,7 @@ tcg_status launch(Params& p, const Plan& pl, const tcg::host::Device& dev, cudaS
     auto* kernel = tcg::b128::block128_kernel<TN, kPair, kSwap, kCol>;
     static tcg::host::OncePerDevice once;
     const cudaError_t err = once([&] {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tcg::b128::kSmemBytes);
         cudaFuncAttributes a;
         if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
         // the register hand-over draws on what the block is launched with
@@ -83,18 +83,14 @@ tcg_status launch(Params& p, const Plan& pl, const tcg::host::Device& dev, cudaS
         return e;
     });
     if (err != cudaSuccess) return tcg::host::fail_launch("tcg_gemm_block128 kernel attributes", err);
-    const int groups = p.mode == tcg::b128::kDense ? 0 : p.num_groups;
-    // Few rows: five stages of one k-block, so that two blocks fit on an SM and the
-    // next call's set up beside this one's (1 x 8192 x 8192 back to back: 24.6 us
-    // with the SM's memory full of stages, 22.3 with five, 19.6 with the early
-    // launch below).
-    p.stages = std::min(kSwap ? 5 : 8, (dev.max_smem_optin - S::smem_bytes(0, groups)) / S::kStageBytes);
+    const int tables = p.mode == tcg::b128::kDense ? 0 : p.mode == tcg::b128::kGroupedK ? 1 : 2;
+    p.stages = std::min(S::kMaxStages, (dev.max_smem_optin - S::smem_bytes(0, tables, p.num_groups)) / S::kStageBytes);
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((kPair ? 2 : 1) * pl.workers);
     cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::smem_bytes(p.stages, groups);
+    cfg.dynamicSmemBytes = S::smem_bytes(p.stages, tables, p.num_groups);
     cfg.stream = stream;
     // the blocks may be launched while the kernel ahead ends (they wait for it
     // before they read anything)

@@ -295,27 +295,28 @@ __device__ __forceinline__ Piece load_piece(const volatile Piece* s) {
 }
 
 // Group tables in shared memory, built once per CTA: first tile (grouped
-// rows) or first k-block (grouped K) of each group, and its rows.
+// rows) or first k-block (grouped K) of each group, and, for grouped rows, its
+// first row.  The groups lie one after the other, so each ends where the next
+// begins.
 struct Groups {
     const int* start;   // num_groups + 1
-    const int* row0;    // num_groups
-    const int* len;     // num_groups
+    const int* row;     // num_groups + 1 (grouped rows alone)
 };
 
 // (group_rows: whatever the offsets hold, the groups share the operand's rows
 // out, so every sum here is bounded by the operand's own tiles or k-blocks
 // and one more a group.)
 template <int kTileM>
-__device__ __forceinline__ void build_groups(const Params& p, int* start, int* row0, int* len, int lane) {
+__device__ __forceinline__ void build_groups(const Params& p, int* start, int* row, int lane) {
     const int cap = p.mode == kGroupedRows ? p.M : p.num_kb * kBlock;
     int base = 0, last = 0;
     for (int g0 = 0; g0 < p.num_groups; g0 += 32) {
         const int g = g0 + lane;
         int n, r;
         group_rows(p.offsets, p.num_groups, cap, g0, lane, last, r, n);
-        if (g < p.num_groups) {
-            row0[g] = r;
-            len[g] = n;
+        if (g < p.num_groups && p.mode == kGroupedRows) {
+            if (g == 0) row[0] = r;
+            row[g + 1] = r + n;
         }
         int c = p.mode == kGroupedRows ? (n + kTileM - 1) / kTileM * p.num_n : (n + kBlock - 1) / kBlock;
         int incl = c;
@@ -359,10 +360,9 @@ __device__ __forceinline__ void decode_tile(const Params& p, const Groups& gr, i
     if (p.mode == kGroupedRows) {
         w.g = find_group(gr, p.num_groups, t);
         local = t - gr.start[w.g];
-        row0 = gr.row0[w.g];
-        const int n = gr.len[w.g];
-        w.m_end = row0 + n;
-        nm = (n + kTileM - 1) / kTileM;
+        row0 = gr.row[w.g];
+        w.m_end = gr.row[w.g + 1];
+        nm = (w.m_end - row0 + kTileM - 1) / kTileM;
         brow = w.g * p.N;
     } else if (p.mode == kGroupedK) {
         const int per = p.num_m * p.num_n;
@@ -654,15 +654,35 @@ struct Shape {
     static constexpr bool kCols = kColScale || kSwap;
     static constexpr int kColWords = kCols ? kTileN : 4;
     static constexpr int kSlotWords = 128 + kColWords;
+    // Stages at most.  Few rows: five of one k-block, so that two blocks fit on
+    // an SM and the next call's set up beside this one's (1 x 8192 x 8192 back to
+    // back: 24.6 us with the SM's memory full of stages, 22.3 with five, 19.6 with
+    // the early launch).  Pairs: two, although three fit where there are few
+    // groups; the L1 that the third would take holds what the promote warps spill
+    // (8192^3 521 us with three, 514 with two; a scale per row of B 742 and 707;
+    // weight gradients of 4096 x 4096 over 16384 rows in 7 groups 618 and 587).
+    // Single tiles: three (256 x 8192 x 8192 35 us, 38 with two), two where the
+    // tables of 780 groups and more and a scale per row of B leave no room.
+    static constexpr int kMaxStages = kSwap ? 5 : kPair ? 2 : 3;
+    static constexpr int kMinStages = kSwap ? 5 : 2;   // fit whatever the groups (asserted below)
     static constexpr int kTileM = kSwap ? kTileN : (kPair ? 256 : 128);   // rows of D per tile
     static constexpr int kTileNOut = kSwap ? 128 : kTileN;                // columns of D per tile
     static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "TMEM columns are a power of two");
     static_assert(kAtomBytes % 1024 == 0, "atoms stay 1024-byte aligned");
-    static int smem_bytes(int stages, int groups) {
+    // tables: 0 (dense), 1 (grouped K) or 2 (grouped rows) of groups + 1 words
+    static constexpr int smem_bytes(int stages, int tables, int groups) {
         return 1024 + stages * kStageBytes + (kPromoteWarps * kWarpWords + kScaleSlots * kSlotWords) * 4 + static_cast<int>(sizeof(Ctl)) +
-               (groups > 0 ? (3 * groups + 1) * 4 : 0) + 64;
+               tables * (groups + 1) * 4;
     }
 };
+
+constexpr int kSmemBytes = 232448;   // 227 KiB, the most a block may have
+template <typename S>
+constexpr bool fits_any_groups() { return S::smem_bytes(S::kMinStages, 2, kMaxGroups) <= kSmemBytes; }
+static_assert(fits_any_groups<Shape<256, true, false, true>>() && fits_any_groups<Shape<256, true, false, false>>() &&
+                  fits_any_groups<Shape<128, false, false, true>>() && fits_any_groups<Shape<128, false, false, false>>() &&
+                  fits_any_groups<Shape<16, false, true, false>>() && fits_any_groups<Shape<32, false, true, false>>(),
+              "group tables take no stage below kMinStages");
 
 template <int kTileN, bool kPair, bool kSwap, bool kColScale>
 __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThreads, 1)
@@ -676,7 +696,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
     float* scale_words = reinterpret_cast<float*>(warp_words + S::kPromoteWarps * S::kWarpWords);
     Ctl* ctl = reinterpret_cast<Ctl*>(scale_words + kScaleSlots * S::kSlotWords);
     int* tables = reinterpret_cast<int*>(ctl + 1);
-    const Groups gr{tables, tables + p.num_groups + 1, tables + 2 * p.num_groups + 1};
+    const Groups gr{tables, tables + p.num_groups + 1};
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -717,7 +737,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
     // what the call before has written is read only from here on.
     host::wait_for_kernel_ahead();
     if (warp == 0 && p.mode != kDense)
-        build_groups<S::kTileM>(p, tables, tables + p.num_groups + 1, tables + 2 * p.num_groups + 1, lane);
+        build_groups<S::kTileM>(p, tables, tables + p.num_groups + 1, lane);
     ptx::tc_fence_before_sync();
     if constexpr (kPair) ptx::cluster_sync();   // the peer's barriers exist before anyone signals them
     __syncthreads();
