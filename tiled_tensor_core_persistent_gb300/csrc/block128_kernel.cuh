@@ -30,7 +30,9 @@
 // rows over 16 experts of 4096 x 4096: 45.7 us, 5.1 TB/s).
 //
 // Roles (one CTA or a CTA pair, persistent): warp 0 TMA producer, warp 1 MMA
-// issuer and TMEM owner, the others promote and store.  All waits are
+// issuer and TMEM owner, warp 2 copies the scales ahead, warp 3 idle (it fills
+// the control warps' group of four, which give up registers together), the
+// others promote and store.  All waits are
 // bounded; on expiry the status word gets TCG_ERR_TIMEOUT, the roles drain
 // their copies and MMAs, free the TMEM and return.
 #pragma once
@@ -173,7 +175,8 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const 
 }
 
 // 32 lanes x 16 or 32 consecutive TMEM columns.  The registers are valid
-// after tmem_wait, which takes them as operands so that no use moves ahead.
+// after tmem_wait; what uses them is volatile too (fold), so that none moves
+// ahead of it.
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -195,32 +198,17 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr)
         : "memory");
 }
-template <int N>
-__device__ __forceinline__ void tmem_wait(uint32_t (&)[N]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-#ifndef FOLD
-#define FOLD 3
-#endif
-#ifndef WAITS
-#define WAITS 1
-#endif
-#if FOLD == 3
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // (volatile, so that none moves ahead of the wait for its operand)
 __device__ __forceinline__ void fold(float& acc, uint32_t t, float s) {
     asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "r"(t), "f"(s));
 }
-#else
-__device__ __forceinline__ void fold2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s2) {
-    asm volatile("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s2));
-}
-#endif
 
 // The four K = 32 MMAs of one k-block into fresh accumulator columns, and the
 // arrival on `full` (of both CTAs of a pair) when they have ended.  One block
-// of instructions, operand descriptors as 32-bit halves: the issuing thread
-// spends 390 cycles here of the 512 that the MMAs of a pair tile take, and
-// everything else it does per k-block has to fit into the rest.
+// of instructions, operand descriptors as 32-bit halves: what the issuing
+// thread spends here (elect_one) and on everything else of a k-block has to
+// fit into the 512 cycles that the MMAs of a pair tile take.
 template <bool kPair>
 __device__ __forceinline__ void mma_kblock(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
                                            uint64_t* full) {
@@ -448,8 +436,9 @@ struct Walk<true> {
     }
 };
 
-// Partial slot of piece q of a shared tile: a worker's run holds the end of
-// at most one shared tile (slot 1) and the beginning of at most one (slot 0).
+// Partial slot of piece q of a shared tile.  A worker's run can share the tile
+// it starts in (slot 0: the run starts at or after the tile's first k-block)
+// and the one it ends in (slot 1: the run starts before the tile).
 __device__ __forceinline__ int slot_of(const Params& p, const Walk<true>& s, const Piece& w, int q) {
     const int c = w.first + q;
     const bool begins = c * s.total / s.workers >= static_cast<long long>(w.tile) * p.num_kb;
@@ -980,7 +969,7 @@ __global__ void __launch_bounds__(Shape<kTileN, kPair, kSwap, kColScale>::kThrea
                 if (more) read_scale(nslot);
 #pragma unroll
                 for (int j = 0; j < kChunks; ++j) {
-                    tmem_wait(r[j & 1]);
+                    tmem_wait();
                     if (j + 1 < kChunks) {
                         tmem_load(t0 + (j + 1) * kChunk, r[(j + 1) & 1]);
                     } else {

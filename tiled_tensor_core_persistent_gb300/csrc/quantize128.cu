@@ -45,13 +45,12 @@ struct Quant {
     long long ldqt;
     float* scales;
     long long lds;
-    float inv_top, top;
+    float inv_top;
     int pow2;
     int e5m2;
     int vec;               // x may be read, q written, in whole vectors
     const int* offsets;
     int groups;
-    int padded;
 };
 
 __device__ __forceinline__ float scale_of(const Quant& p, float amax) {
@@ -436,8 +435,7 @@ tcg_status start(Quant& p, int rows, int cols, tcg_dtype x_dtype, const void* x,
     p.index = index;
     p.source = source;
     p.scales = scales;
-    p.top = q_dtype == TCG_E5M2 ? 57344.0f : 448.0f;
-    p.inv_top = 1.0f / p.top;
+    p.inv_top = 1.0f / (q_dtype == TCG_E5M2 ? 57344.0f : 448.0f);
     p.pow2 = pow2 != 0;
     p.e5m2 = q_dtype == TCG_E5M2;
     p.vec = aligned(x, 16) && (static_cast<long long>(ldx) * x_bytes(x_dtype)) % 16 == 0;
@@ -523,7 +521,6 @@ tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const voi
     p.lds = ld_scales;
     p.offsets = offsets;
     p.groups = num_groups;
-    p.padded = padded_rows;
     const int row_blocks = padded_rows / 128;
     const dim3 grid((cols + 127) / 128, row_blocks);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
