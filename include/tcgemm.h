@@ -460,7 +460,8 @@ tcg_status tcg_quantize_cols128(int rows, int cols, tcg_dtype x_dtype, const voi
  * matrices of rows x cols, matrix b being rows [b * rows, (b + 1) * rows) of
  * x.  q (rows x cols each, stacked the same way, ldq >= cols) and qt (the
  * transposed codes, cols x rows each, ldqt >= rows): either may be NULL.
- * scales: batch x ceil(rows / 128) x ceil(cols / 128), contiguous.
+ * scales: batch x ceil(rows / 128) x ceil(cols / 128), contiguous.  batch and
+ * ceil(rows / 128) <= 65535 (else TCG_ERR_UNSUPPORTED).
  */
 tcg_status tcg_quantize_tiles128(int batch, int rows, int cols, tcg_dtype x_dtype, const void* x, int ldx,
                                  void* q, int ldq, void* qt, int ldqt, tcg_dtype q_dtype, float* scales,

@@ -25,7 +25,7 @@
 // tiles under twelve promote warps (613-640), 128 x 256 tiles on one CTA (557).
 // A per-column scale (both operands scaled per row, the weight gradients) adds
 // one multiply per element, and fp32 C and D their traffic: 4096 x 4096 over
-// 16384 rows of K in 8 groups, 878 us, 2.6 TB/s.  Few rows are bound by B's
+// 16384 rows of K in 16 groups, 876-901 us, 2.5-2.6 TB/s.  Few rows are bound by B's
 // bytes and a launch's start and end (1 x 8192 x 8192: 19.6 us, 3.4 TB/s; 32
 // rows over 16 experts of 4096 x 4096: 45.7 us, 5.1 TB/s).
 //
