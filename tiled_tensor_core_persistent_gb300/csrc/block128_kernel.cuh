@@ -17,7 +17,7 @@
 // issue cycles of each scheduler, next to the waits and the hand-overs).  Two
 // accumulators of 256 columns fill the TMEM, so the chain MMAs -> commit ->
 // fold -> hand-back closes over two k-blocks, and one takes about 950 cycles:
-// 8192^3 in 513-526 us, 2.09-2.14 PFLOP/s, 1.1 times the bf16 rate of the
+// 8192^3 in 506-526 us, 2.09-2.17 PFLOP/s, 1.1 times the bf16 rate of the
 // library on this GPU.  Measured at 8192^3 and slower: FMAs of two sums an
 // instruction (the pairs cost a move each), 128-column accumulators with an
 // issuer each or one issuer for both (513-565 us beside 498-520), the next
@@ -25,7 +25,7 @@
 // tiles under twelve promote warps (613-640), 128 x 256 tiles on one CTA (557).
 // A per-column scale (both operands scaled per row, the weight gradients) adds
 // one multiply per element, and fp32 C and D their traffic: 4096 x 4096 over
-// 16384 rows of K in 16 groups, 876-901 us, 2.5-2.6 TB/s.  Few rows are bound by B's
+// 16384 rows of K in 16 groups, 870-892 us, 2.6 TB/s.  Few rows are bound by B's
 // bytes and a launch's start and end (1 x 8192 x 8192: 19.6 us, 3.4 TB/s; 32
 // rows over 16 experts of 4096 x 4096: 45.7 us, 5.1 TB/s).
 //

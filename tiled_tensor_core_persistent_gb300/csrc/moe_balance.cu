@@ -12,7 +12,7 @@
 //
 // Bound by memory on paper (logits once forward; once more, and their
 // gradient, backward: 5 us for 32768 x 256), in fact by latencies at that size
-// (forward 16.8, backward 17.2, one after the other 29.8 us): both issue in
+// (forward 16.7, backward 17.0, one after the other 29.8 us): both issue in
 // 42-44 % of the cycles, the forward's largest stall is its barriers (eight
 // in the tree over the warps' column sums; then the totals, and one CTA that
 // finishes alone), the backward's the wait for a row's loads.  Few tokens are
