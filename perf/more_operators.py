@@ -13,9 +13,9 @@ it is trained on:
             in that of the tokens: where each expert's rows start, the token of
             every row (-1 past the last), and the row of every assignment (-1
             for those that were dropped or masked).
-  dispatch  row r of the experts' input is the row of x that the sorted order
-            names.  Training: with the gradient of x, each token's sum over its
-            rows.
+  dispatch  the row of x of every token goes to the rows of its assignments in
+            the experts' input; rows of no assignment stay as they are.
+            Training: with the gradient of x, each token's sum over its rows.
   combine   y_t = sum over j of w_tj x[row_of[t, j]].  Training: the gradients
             of the rows and of the weights.
   xent      lse_t = log sum_v exp(x_t . W_v), loss_t = lse_t - x_t . W_target,
@@ -274,7 +274,7 @@ def prepare(case, seed):
     n, cols, dt = t * k, c["cols"], TYPE[c["x"]]
     if op == "dispatch":
         s["x"] = randn(t, cols).to(dt)
-        s["out"] = torch.empty(n, cols, dtype=dt, device=dev)
+        s["out"] = torch.zeros(n, cols, dtype=dt, device=dev)    # (rows of no token stay as they are)
         if c["train"]:
             s["dout"] = (0.1 * randn(n, cols)).to(dt)
             s["dx"] = torch.empty(t, cols, dtype=dt, device=dev)
@@ -285,7 +285,7 @@ def prepare(case, seed):
     s["y"] = torch.empty(t, cols, dtype=dt, device=dev)
     if c["train"]:
         s["dy"] = (0.1 * randn(t, cols)).to(dt)
-        s["dx"] = torch.zeros(n, cols, dtype=dt, device=dev)     # (rows of no token stay as they are)
+        s["dx"] = torch.zeros(n, cols, dtype=dt, device=dev)
         s["dweights"] = torch.empty(t, k, device=dev)
     return s
 
@@ -363,7 +363,7 @@ def _run_own(s):
         return dict(offsets=s["offsets"], row_token=s["row_token"], row_of=s["row_of"])
     n, cols, x = t * k, c["cols"], c["x"]
     if op == "dispatch":
-        tcg.moe_dispatch(n, cols, s["x"], cols, x, t, s["row_token"], s["out"], cols, x, stream=stream)
+        tcg.moe_dispatch(t, k, cols, n, s["x"], cols, x, s["row_of"], k, s["out"], cols, x, stream=stream)
         out = dict(out=s["out"])
         if c["train"]:
             tcg.moe_combine(t, k, cols, n, s["dout"], cols, x, s["row_of"], k, None, k, s["dx"], cols, x, stream=stream)
@@ -372,7 +372,7 @@ def _run_own(s):
     tcg.moe_combine(t, k, cols, n, s["x"], cols, x, s["row_of"], k, s["weights"], k, s["y"], cols, x, stream=stream)
     out = dict(y=s["y"])
     if c["train"]:
-        tcg.moe_combine_backward(t, k, cols, n, s["x"], cols, x, s["row_of"], k, s["weights"], k, s["dy"], cols, x, s["dx"], cols, x,
+        tcg.moe_combine_backward(t, k, cols, n, s["x"], cols, x, s["row_of"], k, s["weights"], k, s["dy"], cols, x, s["dx"], cols,
                                  s["dweights"], k, stream=stream)
         out.update(dx=s["dx"], dweights=s["dweights"])
     return out
@@ -397,7 +397,7 @@ def work(case):
         return dict(bytes=t * (12 * k + 1) + 4 * (e + 1), flops=t * k)
     row, live = c["cols"] * SIZE[c["x"]], int(0.98 * (1.0 - c["masked"]) * t * k)
     if op == "dispatch":
-        once = (t + t * k) * row + 4 * t * k
+        once = (t + live) * row + 4 * t * k
         return dict(bytes=once + ((live + t) * row + 4 * t * k if c["train"] else 0), flops=live * c["cols"] if c["train"] else 0)
     once = (live + t) * row + 8 * t * k
     if not c["train"]:
