@@ -591,6 +591,151 @@ tcg_status tcg_moe_balance_backward(int tokens, int experts, int k, tcg_dtype dt
                                     void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The way of tokens to their experts and back.  A router chooses (tcg_moe_route),
+ * the assignments are put in expert order (tcg_moe_sort), the tokens' rows go to
+ * the experts' (tcg_moe_dispatch; tcg_quantize_rows128 with row_token where the
+ * products run in 8 bits), the grouped products take the offsets, and the
+ * results go back with their weights (tcg_moe_combine).  Types: TCG_BF16,
+ * TCG_F16 or TCG_F32; any alignments of the element and leading dimensions,
+ * whole words where rows start on 16 bytes.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * tcg_moe_route -- each token's k experts and their weights.  topk (tokens x k,
+ * ld_topk >= k): the experts of the k largest logits, in falling order, equal
+ * ones (both zeros are equal) by the lower expert.  weights (fp32, tokens x k):
+ *     w_j = exp(x_{e_j} - m) / sum over all experts e of exp(x_e - m),
+ * or, with renormalize != 0, over the chosen e_j alone (m: the largest logit).
+ * An expert whose logit is -inf is switched off: it is never chosen, and where
+ * fewer than k are left, the last places hold -1 with weight 0.  So do all of a
+ * token's with mask 0 (mask: one byte per token, NULL: all count), whatever its
+ * logits hold.  A NaN counts as the largest and makes the token's weights NaN.
+ * k <= experts (else TCG_ERR_INVALID_ARG), k <= 32 and experts <= 1024 (else
+ * TCG_ERR_UNSUPPORTED).
+ */
+tcg_status tcg_moe_route(int tokens, int experts, int k, tcg_dtype dtype, const void* logits, int ld,
+                         const uint8_t* mask, int renormalize, int* topk, int ld_topk,
+                         float* weights, int ld_weights, void* stream);
+
+/*
+ * tcg_moe_route_backward -- the logits' gradient from that of the weights, for
+ * the topk that tcg_moe_route wrote (the choice itself is a constant):
+ *     dlogits_e = p_e (sum_{j: e_j = e} g_j - sum_j g_j p_{e_j})   or, renormalized,
+ *     dlogits_{e_j} = w_j (g_j - sum_i g_i w_i), 0 for the others.
+ * Entries of topk outside [0, experts) take no part: their gradient is not read,
+ * and a token without any has gradient 0 whatever its logits hold.  An expert
+ * that a token names twice has both places' gradients.  accumulate != 0: added
+ * to dlogits (tcg_moe_balance_backward's, say), in fp32 with one rounding.
+ * Without it dlogits may be the logits' own memory when the types and leading
+ * dimensions agree.
+ */
+tcg_status tcg_moe_route_backward(int tokens, int experts, int k, tcg_dtype dtype, const void* logits, int ld,
+                                  const int* topk, int ld_topk, int renormalize,
+                                  const float* grad_weights, int ld_grad, int accumulate,
+                                  void* dlogits, int ldd, tcg_dtype d_dtype, void* stream);
+
+/*
+ * tcg_moe_sort -- the assignments (token t, place j) in the order of their
+ * experts and, inside an expert, of (t, j).  Entries of topk outside [0,
+ * experts), and all of a token's with mask 0, are dropped.
+ *   offsets (experts + 1, may be NULL): where each expert's rows start, as
+ *     tcg_moe_balance writes them for the same topk and mask.
+ *   row_token (tokens * k): the token of each row, -1 in the rows past the last
+ *     (tcg_quantize_rows128 makes zeros of those).
+ *   row_of (tokens x k, ld_row_of >= k): the row of each assignment, -1 where it
+ *     was dropped.
+ * experts <= 1024 and tokens * k <= 2^31 - 2^20 - 4096 (else
+ * TCG_ERR_UNSUPPORTED).  The order is the same every time.  workspace:
+ * tcg_moe_sort_workspace_size bytes, shared as in tcg_moe_balance.
+ */
+size_t tcg_moe_sort_workspace_size(int tokens, int experts, int k);
+tcg_status tcg_moe_sort(int tokens, int experts, int k, const int* topk, int ld_topk, const uint8_t* mask,
+                        int* offsets, int* row_token, int* row_of, int ld_row_of,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tcg_moe_dispatch -- row row_of[t, j] of out is row t of x (tokens x cols), for
+ * every assignment.  Entries of row_of outside [0, rows) are skipped; rows of
+ * out that none names are left as they were, and one that several name holds
+ * one of them.  Its gradient is tcg_moe_combine without weights.  cols <=
+ * 65535 * 4096 here and below.  Outputs must not overlap inputs.
+ */
+tcg_status tcg_moe_dispatch(int tokens, int k, int cols, int rows, const void* x, int ldx, tcg_dtype x_dtype,
+                            const int* row_of, int ld_row_of, void* out, int ldo, tcg_dtype out_dtype, void* stream);
+
+/*
+ * tcg_moe_combine -- y_t = sum over j of weights[t, j] * x[row_of[t, j]], summed
+ * in fp32 in the order of j and rounded once.  x: rows x cols; entries of
+ * row_of outside [0, rows) are skipped, whatever their weight; a token without
+ * any has y_t = 0.  weights (fp32, ld_weights >= k): NULL counts as 1.
+ */
+tcg_status tcg_moe_combine(int tokens, int k, int cols, int rows, const void* x, int ldx, tcg_dtype x_dtype,
+                           const int* row_of, int ld_row_of, const float* weights, int ld_weights,
+                           void* y, int ldy, tcg_dtype y_dtype, void* stream);
+
+/*
+ * tcg_moe_combine_backward -- both gradients of tcg_moe_combine, in one pass
+ * over dy and x: dx[row_of[t, j]] = weights[t, j] * dy_t (rows that no
+ * assignment names are left as they were) and dweights[t, j] = sum over the
+ * columns of dy_t * x[row_of[t, j]], 0 for skipped entries.  dx has x's type.
+ * dweights may be NULL, and x with it.
+ */
+tcg_status tcg_moe_combine_backward(int tokens, int k, int cols, int rows, const void* x, int ldx, tcg_dtype x_dtype,
+                                    const int* row_of, int ld_row_of, const float* weights, int ld_weights,
+                                    const void* dy, int lddy, tcg_dtype dy_dtype, void* dx, int lddx,
+                                    float* dweights, int ld_dweights, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Softmax cross entropy of a linear layer over a vocabulary: the product with
+ * the loss as its epilogue.  The logits X @ W^T (tokens x vocab) are never
+ * kept: tiles of them end in their rows' maximum and sum, and the gradient
+ * computes them again, a piece of the vocabulary at a time.
+ *   X: tokens x hidden, W: vocab x hidden, row-major, both dtype (TCG_BF16 or
+ *     TCG_F16), 16-byte aligned with leading dimensions that are multiples of 8
+ *     (else TCG_ERR_UNSUPPORTED).  vocab, hidden >= 1.
+ *   target: the word of each token; one outside [0, vocab) does not count.
+ *   workspace: tcg_linear_xent_workspace_size bytes (backward != 0: of the
+ *     gradient, which suffices for the loss as well), zero-filled once and
+ *     shared as in tcg_moe_balance.
+ * ---------------------------------------------------------------------------
+ */
+size_t tcg_linear_xent_workspace_size(int tokens, int vocab, int hidden, int backward);
+
+/*
+ * tcg_linear_xent -- lse_t = log sum_v exp(x_t . W_v) (every token's), loss_t =
+ * lse_t - x_t . W_target (0 where the token does not count; loss may be NULL),
+ * num_valid = n, the tokens that count, and mean = their losses' sum / n (0 when
+ * n = 0); fp32, device memory.  A logit that is NaN or +inf makes its token's
+ * lse and loss NaN.  The results are the same every time.
+ */
+tcg_status tcg_linear_xent(int tokens, int vocab, int hidden, tcg_dtype dtype, const void* X, int ldx,
+                           const void* W, int ldw, const int* target, float* lse, float* loss, float* mean, int* num_valid,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * tcg_linear_xent_backward -- the gradients of X and W, for lse and num_valid of
+ * the forward call:
+ *     dz_tv = r_t (exp(z_tv - lse_t) - [v = target_t]),  r_t = *grad_mean / n + grad_loss_t
+ *     dX = dz W,   dW = dz^T X + dw_beta * dW
+ * grad_mean (one value) and grad_loss (per token), device memory: the
+ * gradients of mean and loss, NULL where there is none.  Tokens that do not
+ * count have dz = 0 (their rows of X take part with that, so they have to be
+ * finite).  dX (tokens x hidden) and dW (vocab x hidden): TCG_BF16, TCG_F16 or
+ * TCG_F32; either may be NULL.  dz is rounded once to dtype, which bounds the
+ * gradients' precision whatever their type; sums are fp32.  Outputs must not
+ * overlap inputs.
+ */
+tcg_status tcg_linear_xent_backward(int tokens, int vocab, int hidden, tcg_dtype dtype, const void* X, int ldx,
+                                    const void* W, int ldw, const int* target, const float* lse, const int* num_valid,
+                                    const float* grad_mean, const float* grad_loss,
+                                    void* dX, int lddx, tcg_dtype dx_dtype,
+                                    float dw_beta, void* dW, int lddw, tcg_dtype dw_dtype,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * tcg_debug_tma_swizzle128 -- TEST-ONLY: one TMA load of a rows x 128-byte
  * tile (row-major, 128-byte rows, device memory at src) into 1024-byte-aligned
  * shared memory with 128-byte swizzling, copied back unchanged to dst (rows x

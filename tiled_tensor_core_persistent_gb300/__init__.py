@@ -39,7 +39,9 @@ EXPORTED = ["tcg_can_implement", "tcg_workspace_size", "tcg_workspace_size_for",
             "tcg_debug_tma_swizzle128", "tcg_arch_status", "tcg_quantize_rows128", "tcg_quantize_cols128",
             "tcg_quantize_tiles128", "tcg_block128_workspace_size", "tcg_gemm_block128", "tcg_gemm_block128_grouped",
             "tcg_gemm_block128_grouped_k", "tcg_moe_balance_workspace_size", "tcg_moe_balance",
-            "tcg_moe_balance_backward"]
+            "tcg_moe_balance_backward", "tcg_moe_route", "tcg_moe_route_backward", "tcg_moe_sort_workspace_size", "tcg_moe_sort",
+            "tcg_moe_dispatch", "tcg_moe_combine", "tcg_moe_combine_backward", "tcg_linear_xent_workspace_size",
+            "tcg_linear_xent", "tcg_linear_xent_backward"]
 
 
 class TcgError(RuntimeError):
@@ -153,6 +155,28 @@ def lib() -> ctypes.CDLL:
         L.tcg_moe_balance.restype = i32
         L.tcg_moe_balance_backward.argtypes = [i32, i32, i32, i32, P, i32, P, f32, P, P, P, P, i32, i32, P]
         L.tcg_moe_balance_backward.restype = i32
+        L.tcg_moe_route.argtypes = [i32, i32, i32, i32, P, i32, P, i32, P, i32, P, i32, P]
+        L.tcg_moe_route.restype = i32
+        L.tcg_moe_route_backward.argtypes = [i32, i32, i32, i32, P, i32, P, i32, i32, P, i32, i32, P, i32, i32, P]
+        L.tcg_moe_route_backward.restype = i32
+        L.tcg_moe_sort_workspace_size.argtypes = [i32, i32, i32]
+        L.tcg_moe_sort_workspace_size.restype = sz
+        L.tcg_moe_sort.argtypes = [i32, i32, i32, P, i32, P, P, P, P, i32, P, sz, P]
+        L.tcg_moe_sort.restype = i32
+        L.tcg_moe_dispatch.argtypes = [i32, i32, i32, i32, P, i32, i32, P, i32, P, i32, i32, P]
+        L.tcg_moe_dispatch.restype = i32
+        L.tcg_moe_combine.argtypes = [i32, i32, i32, i32, P, i32, i32, P, i32, P, i32, P, i32, i32, P]
+        L.tcg_moe_combine.restype = i32
+        L.tcg_moe_combine_backward.argtypes = [i32, i32, i32, i32, P, i32, i32, P, i32, P, i32, P, i32, i32, P, i32, P,
+                                               i32, P]
+        L.tcg_moe_combine_backward.restype = i32
+        L.tcg_linear_xent_workspace_size.argtypes = [i32, i32, i32, i32]
+        L.tcg_linear_xent_workspace_size.restype = sz
+        L.tcg_linear_xent.argtypes = [i32, i32, i32, i32, P, i32, P, i32, P, P, P, P, P, P, sz, P]
+        L.tcg_linear_xent.restype = i32
+        L.tcg_linear_xent_backward.argtypes = [i32, i32, i32, i32, P, i32, P, i32, P, P, P, P, P, P, i32, i32, f32, P, i32,
+                                               i32, P, sz, P]
+        L.tcg_linear_xent_backward.restype = i32
         L.tcg_debug_tma_swizzle128.argtypes = [P, i32, P, P, P]
         L.tcg_debug_tma_swizzle128.restype = i32
         _lib = L
@@ -415,6 +439,95 @@ def moe_balance_backward(tokens, experts, k, logits, ld, dtype, mask, coef, coun
                                         _enum(d_dtype, DTYPES), _stream(stream))
     if st != 0:
         raise TcgError(st, "tcg_moe_balance_backward", last_error())
+
+
+# ---------------------------------------- tokens to their experts and back
+
+def moe_route(tokens, experts, k, logits, ld, dtype, mask, renormalize, topk, ld_topk, weights, ld_weights, *,
+              stream=None) -> None:
+    """Queue each token's k experts and their weights (tcg_moe_route)."""
+    st = lib().tcg_moe_route(tokens, experts, k, _enum(dtype, DTYPES), _addr(logits), ld, _addr(mask), int(renormalize),
+                             _addr(topk), ld_topk, _addr(weights), ld_weights, _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_moe_route", last_error())
+
+
+def moe_route_backward(tokens, experts, k, logits, ld, dtype, topk, ld_topk, renormalize, grad_weights, ld_grad,
+                       accumulate, dlogits, ldd, d_dtype, *, stream=None) -> None:
+    """Queue the logits' gradient from that of the chosen experts' weights (tcg_moe_route_backward)."""
+    st = lib().tcg_moe_route_backward(tokens, experts, k, _enum(dtype, DTYPES), _addr(logits), ld, _addr(topk), ld_topk,
+                                      int(renormalize), _addr(grad_weights), ld_grad, int(accumulate), _addr(dlogits),
+                                      ldd, _enum(d_dtype, DTYPES), _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_moe_route_backward", last_error())
+
+
+def moe_sort_workspace_size(tokens, experts, k) -> int:
+    return int(lib().tcg_moe_sort_workspace_size(tokens, experts, k))
+
+
+def moe_sort(tokens, experts, k, topk, ld_topk, mask, offsets, row_token, row_of, ld_row_of, *, workspace=None,
+             workspace_bytes=0, stream=None) -> None:
+    """Queue the assignments' order by expert: offsets, the rows' tokens, the assignments' rows (tcg_moe_sort)."""
+    st = lib().tcg_moe_sort(tokens, experts, k, _addr(topk), ld_topk, _addr(mask), _addr(offsets), _addr(row_token),
+                            _addr(row_of), ld_row_of, _addr(workspace), workspace_bytes, _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_moe_sort", last_error())
+
+
+def moe_dispatch(tokens, k, cols, rows, x, ldx, x_dtype, row_of, ld_row_of, out, ldo, out_dtype, *, stream=None) -> None:
+    """Queue every token's row to the rows of its assignments (tcg_moe_dispatch)."""
+    st = lib().tcg_moe_dispatch(tokens, k, cols, rows, _addr(x), ldx, _enum(x_dtype, DTYPES), _addr(row_of), ld_row_of,
+                                _addr(out), ldo, _enum(out_dtype, DTYPES), _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_moe_dispatch", last_error())
+
+
+def moe_combine(tokens, k, cols, rows, x, ldx, x_dtype, row_of, ld_row_of, weights, ld_weights, y, ldy, y_dtype, *,
+                stream=None) -> None:
+    """Queue each token's weighted sum over its assignments' rows (tcg_moe_combine)."""
+    st = lib().tcg_moe_combine(tokens, k, cols, rows, _addr(x), ldx, _enum(x_dtype, DTYPES), _addr(row_of), ld_row_of,
+                               _addr(weights), ld_weights, _addr(y), ldy, _enum(y_dtype, DTYPES), _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_moe_combine", last_error())
+
+
+def moe_combine_backward(tokens, k, cols, rows, x, ldx, x_dtype, row_of, ld_row_of, weights, ld_weights, dy, lddy, dy_dtype,
+                         dx, lddx, dweights, ld_dweights, *, stream=None) -> None:
+    """Queue the gradients of the rows (of x's type) and of the weights (tcg_moe_combine_backward)."""
+    st = lib().tcg_moe_combine_backward(tokens, k, cols, rows, _addr(x), ldx, _enum(x_dtype, DTYPES), _addr(row_of),
+                                        ld_row_of, _addr(weights), ld_weights, _addr(dy), lddy, _enum(dy_dtype, DTYPES),
+                                        _addr(dx), lddx, _addr(dweights), ld_dweights, _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_moe_combine_backward", last_error())
+
+
+# ------------------------------ softmax cross entropy over a vocabulary
+
+def linear_xent_workspace_size(tokens, vocab, hidden, backward=True) -> int:
+    return int(lib().tcg_linear_xent_workspace_size(tokens, vocab, hidden, int(backward)))
+
+
+def linear_xent(tokens, vocab, hidden, dtype, X, ldx, W, ldw, target, lse, loss, mean, num_valid, *, workspace=None,
+                workspace_bytes=0, stream=None) -> None:
+    """Queue the cross entropy of softmax(X @ W^T), without its logits in memory (tcg_linear_xent)."""
+    st = lib().tcg_linear_xent(tokens, vocab, hidden, _enum(dtype, DTYPES), _addr(X), ldx, _addr(W), ldw, _addr(target),
+                               _addr(lse), _addr(loss), _addr(mean), _addr(num_valid), _addr(workspace), workspace_bytes,
+                               _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_linear_xent", last_error())
+
+
+def linear_xent_backward(tokens, vocab, hidden, dtype, X, ldx, W, ldw, target, lse, num_valid, grad_mean, grad_loss, dX,
+                         lddx, dx_dtype, dw_beta, dW, lddw, dw_dtype, *, workspace=None, workspace_bytes=0,
+                         stream=None) -> None:
+    """Queue the gradients of X and W, a piece of the vocabulary at a time (tcg_linear_xent_backward)."""
+    st = lib().tcg_linear_xent_backward(tokens, vocab, hidden, _enum(dtype, DTYPES), _addr(X), ldx, _addr(W), ldw,
+                                        _addr(target), _addr(lse), _addr(num_valid), _addr(grad_mean), _addr(grad_loss),
+                                        _addr(dX), lddx, _enum(dx_dtype, DTYPES), dw_beta, _addr(dW), lddw,
+                                        _enum(dw_dtype, DTYPES), _addr(workspace), workspace_bytes, _stream(stream))
+    if st != 0:
+        raise TcgError(st, "tcg_linear_xent_backward", last_error())
 
 
 def debug_tma_swizzle128(src, rows, dst, status, stream=None) -> None:

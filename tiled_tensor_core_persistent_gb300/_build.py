@@ -29,7 +29,7 @@ def so_path(debug: bool | None = None) -> str:
     return DEBUG_SO_PATH if (debug_requested() if debug is None else debug) else SO_PATH
 GENCODE = "arch=compute_103a,code=sm_103a"
 UNITS = ("tcgemm_host", "launch_block_scaled", "launch_grouped", "launch_narrow", "launch_swapped", "block128",
-         "quantize128", "moe_balance", "debug_tma")
+         "quantize128", "moe_balance", "moe_route", "moe_rows", "linear_xent", "debug_tma")
 
 
 def _nvcc() -> str:

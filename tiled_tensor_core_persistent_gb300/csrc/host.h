@@ -68,13 +68,14 @@ tcg_status map_bytes(CUtensorMap* map, const void* base, uint64_t inner, uint64_
 // Launch with leave to start while the kernel ahead ends; the kernel calls
 // wait_for_kernel_ahead() before it reads or writes anything.
 template <typename P>
-cudaError_t launch_early(void (*kernel)(P), dim3 grid, unsigned threads, cudaStream_t stream, const P& p) {
+cudaError_t launch_early(void (*kernel)(P), dim3 grid, unsigned threads, cudaStream_t stream, const P& p, size_t smem = 0) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

@@ -1,0 +1,480 @@
+// linear_xent.cu -- softmax cross entropy of a linear layer over a vocabulary:
+// checks, the pieces of the vocabulary, launches.  The tiles: xent_kernel.cuh.
+//
+//   z = X W^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_{t, y_t}
+//   mean = sum of loss_t / n over the n tokens whose target names a word
+//   dz_tv = r_t (exp(z_tv - lse_t) - [v = y_t]),  r_t = grad_mean / n + grad_loss_t
+//   dX = dz W,  dW = dz^T X
+//
+// Forward, the tiles leave (M, s) of every row and column tile, which one small
+// kernel joins.  Backward, the logits of a piece of the vocabulary are computed
+// again and leave dz of that piece in the workspace, in the operands' type; two
+// products of this library take it to dX (summed over the pieces in fp32) and
+// dW.  One rounding of dz to 16 bits stands between the logits and the
+// gradients, of the same size as that of a 16-bit gradient: the other products
+// would need fp32 operands.  fp16 has no room for small gradients, so there dz
+// is scaled by a power of two that brings the largest |r_t| to 2^14, and the
+// products scale back.
+#include <algorithm>
+#include <climits>
+#include <cstring>
+
+#include "xent_kernel.cuh"
+
+namespace {
+
+using tcg::xent::Params;
+
+// What dz of a piece may take of the workspace.
+constexpr size_t kPieceBytes = size_t(256) << 20;
+constexpr int kMinTileN = 128;
+constexpr int kFinishRows = 32, kFinishSlices = 16, kFinishThreads = kFinishRows * kFinishSlices;
+constexpr float kHalfTop = 16384.0f;   // fp16: the largest |r_t| becomes this or up to half of it
+
+// ------------------------------------------------------- joining the tiles
+
+struct Finish {
+    const float2* part;
+    int num_n, tokens, vocab;
+    const float* picked;
+    const int* target;
+    float* lse;
+    float* loss;          // may be nullptr
+    float* mean;
+    int* valid;
+    double* sums;         // [CTA]
+    int* counts;          // [CTA]
+    int* arrivals;
+};
+
+// 16 threads a row, each some of the column tiles; sums in a fixed order.
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Finish p) {
+    tcg::host::wait_for_kernel_ahead();
+    __shared__ float2 slot[kFinishSlices][kFinishRows];
+    __shared__ int last;
+    const int r = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const long long row = static_cast<long long>(blockIdx.x) * kFinishRows + r;
+    const bool in = row < p.tokens;
+    auto join = [](float2 a, float2 b) {
+        const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.0f : m;
+        return make_float2(m, a.y * exp2f(a.x - base) + b.y * exp2f(b.x - base));
+    };
+    float2 v = make_float2(-INFINITY, 0.0f);
+    if (in) {
+#pragma unroll 4
+        for (int n = slice; n < p.num_n; n += kFinishSlices) v = join(v, p.part[static_cast<size_t>(n) * p.tokens + row]);
+    }
+    slot[slice][r] = v;
+    __syncthreads();
+    double sum = 0.0;
+    int count = 0;
+    if (slice == 0) {
+        if (in) {
+#pragma unroll
+            for (int i = 1; i < kFinishSlices; ++i) v = join(v, slot[i][r]);
+            // (logits were multiplied by kLog2e as it is held, so that is what divides here)
+            const double lse = (static_cast<double>(v.x) + static_cast<double>(log2f(v.y))) / static_cast<double>(tcg::xent::kLog2e);
+            p.lse[row] = static_cast<float>(lse);
+            const int y = p.target[row];
+            const bool counts = y >= 0 && y < p.vocab;
+            const float loss = counts ? static_cast<float>(lse - static_cast<double>(p.picked[row])) : 0.0f;
+            if (p.loss) p.loss[row] = loss;
+            sum = static_cast<double>(loss);
+            count = counts;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            count += __shfl_xor_sync(0xffffffffu, count, d);
+        }
+    }
+    if (gridDim.x > 1) {
+        if (threadIdx.x == 0) {
+            p.sums[blockIdx.x] = sum;
+            p.counts[blockIdx.x] = count;
+            __threadfence();
+            last = tcg::ptx::atomic_add_acq_rel_gpu(p.arrivals, 1) == static_cast<int>(gridDim.x) - 1;
+        }
+        __syncthreads();
+        if (!last) return;
+        // the last CTA: every CTA's sum, in the same order whichever is last
+        if (threadIdx.x >= 32) return;
+        sum = 0.0;
+        count = 0;
+        for (int i = r; i < static_cast<int>(gridDim.x); i += 32) {
+            sum += __ldcg(p.sums + i);
+            count += __ldcg(p.counts + i);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            count += __shfl_xor_sync(0xffffffffu, count, d);
+        }
+        if (threadIdx.x == 0) *p.arrivals = 0;
+    }
+    if (threadIdx.x == 0) {
+        *p.mean = count > 0 ? static_cast<float>(sum / count) : 0.0f;
+        *p.valid = count;
+    }
+}
+
+// -------------------------------------------------------- r_t, and scales
+
+struct Scales {
+    int tokens, vocab, fill;
+    const int* target;
+    const int* valid;
+    const float* grad_mean;   // may be nullptr
+    const float* grad_loss;   // may be nullptr
+    int half;                 // fp16: bring the largest |r_t| to 2^14
+    float* r;                 // [tokens]
+    float* back;              // [fill]: what the products multiply by (fp16)
+};
+
+__device__ __forceinline__ float weight_of(const Scales& p, int t, float each) {
+    const int y = p.target[t];
+    if (y < 0 || y >= p.vocab) return 0.0f;
+    return each + (p.grad_loss ? p.grad_loss[t] : 0.0f);
+}
+
+__global__ void __launch_bounds__(1024) scales_kernel(const __grid_constant__ Scales p) {
+    tcg::host::wait_for_kernel_ahead();
+    __shared__ float most[32];
+    const int n = *p.valid;
+    const float each = p.grad_mean && n > 0 ? *p.grad_mean / static_cast<float>(n) : 0.0f;
+    float up = 1.0f;
+    if (p.half) {
+        float m = 0.0f;   // (fmaxf passes over NaN: one such token leaves the others' scale alone)
+        for (int t = threadIdx.x; t < p.tokens; t += 1024) m = fmaxf(m, fabsf(weight_of(p, t, each)));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+        __syncthreads();
+        m = most[threadIdx.x & 31];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        // the power of two at or below m, kept where its reciprocal and 2^14 times it are ordinary numbers
+        const int e = m > 0.0f && m < INFINITY ? min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100), 100) : 0;
+        up = 0.5f * kHalfTop * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const float back = 2.0f / kHalfTop * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        for (int i = threadIdx.x; i < p.fill; i += 1024) p.back[i] = back;
+    }
+    for (int t = threadIdx.x; t < p.tokens; t += 1024) p.r[t] = weight_of(p, t, each) * up;
+}
+
+// ------------------------------------------------- fp32 sums to fp16 outputs
+
+struct Half {
+    const float* src;
+    long long lds;
+    __half* dst;
+    long long ldd;
+    int rows, cols;
+    float beta;
+};
+__global__ void __launch_bounds__(256) half_kernel(const __grid_constant__ Half p) {
+    tcg::host::wait_for_kernel_ahead();
+    const int c = static_cast<int>(blockIdx.y * 256 + threadIdx.x);
+    if (c >= p.cols) return;
+    for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
+        float v = p.src[r * p.lds + c];
+        __half* d = p.dst + r * p.ldd + c;
+        if (p.beta != 0.0f) v = fmaf(p.beta, __half2float(*d), v);
+        *d = __float2half_rn(v);
+    }
+}
+
+// ----------------------------------------------------------------- plans
+
+long long blocks(long long n, long long b) { return (n + b - 1) / b; }
+size_t padded(size_t n) { return (n + 255) / 256 * 256; }
+
+struct Plan {
+    bool pair = false;
+    int tile_n = 256, num_m = 1, num_n = 1, workers = 1;
+};
+
+// The width whose waves of tiles take the least: a tile's time goes with its
+// columns, plus what a tile costs by itself (about sixteen columns' worth).
+Plan make_plan(int tokens, long long cols, int sms) {
+    Plan pl;
+    pl.pair = tokens > tcg::xent::kBM;
+    pl.num_m = static_cast<int>(blocks(tokens, pl.pair ? 256 : 128));
+    const int workers = std::max(1, pl.pair ? sms / 2 : sms);
+    long long best = LLONG_MAX;
+    for (int w = tcg::xent::kMaxN; w >= kMinTileN; w -= 32) {
+        const long long tiles = pl.num_m * blocks(cols, w), cost = blocks(tiles, workers) * (w + 16);
+        if (cost < best) {
+            best = cost;
+            pl.tile_n = w;
+        }
+    }
+    pl.num_n = static_cast<int>(blocks(cols, pl.tile_n));
+    pl.workers = static_cast<int>(std::min<long long>(static_cast<long long>(pl.num_m) * pl.num_n, workers));
+    return pl;
+}
+
+// Words a piece of the vocabulary has (the last one may have fewer).
+int piece_words(int tokens, int vocab) {
+    const long long fit = std::max<long long>(256, static_cast<long long>(kPieceBytes / 2) / std::max(1, tokens) / 256 * 256);
+    const long long pieces = blocks(vocab, fit);
+    return static_cast<int>(std::min<long long>(vocab, blocks(blocks(vocab, pieces), 256) * 256));
+}
+
+// Where things lie in the workspace.  Forward: behind the ranges that are kept
+// zero.  Backward: behind what the products need.
+struct Layout {
+    size_t part = 0, picked = 0, sums = 0, counts = 0;                      // forward
+    size_t r = 0, back = 0, dz = 0, dx = 0, dw = 0;                         // backward
+    size_t bytes = 0;
+    size_t take(size_t n) {
+        const size_t at = bytes;
+        bytes += padded(n);
+        return at;
+    }
+};
+
+Layout forward_layout(int tokens, int vocab) {
+    Layout l;
+    l.bytes = tcg::host::kScratchAt;
+    l.part = l.take(static_cast<size_t>(blocks(vocab, kMinTileN)) * tokens * sizeof(float2));
+    l.picked = l.take(static_cast<size_t>(tokens) * sizeof(float));
+    l.sums = l.take(static_cast<size_t>(blocks(tokens, kFinishRows)) * sizeof(double));
+    l.counts = l.take(static_cast<size_t>(blocks(tokens, kFinishRows)) * sizeof(int));
+    return l;
+}
+
+int padded_hidden(int hidden) { return static_cast<int>(blocks(hidden, 8) * 8); }
+
+Layout backward_layout(int tokens, int vocab, int hidden) {
+    Layout l;
+    const int words = piece_words(tokens, vocab), rest = vocab - (vocab - 1) / words * words;
+    size_t need = tcg::host::kScratchAt;
+    for (const int w : {words, rest}) {
+        need = std::max(need, tcg_workspace_size(tokens, hidden, w, TCG_BF16));
+        need = std::max(need, tcg_workspace_size(w, hidden, tokens, TCG_BF16));
+    }
+    l.bytes = padded(need);
+    const size_t ld = padded_hidden(hidden);
+    l.r = l.take(static_cast<size_t>(tokens) * sizeof(float));
+    l.back = l.take(static_cast<size_t>(std::max(tokens, words)) * sizeof(float));
+    l.dz = l.take(static_cast<size_t>(tokens) * blocks(words, 32) * 32 * 2);
+    l.dx = l.take(static_cast<size_t>(tokens) * ld * sizeof(float));
+    l.dw = l.take(static_cast<size_t>(words) * ld * sizeof(float));
+    return l;
+}
+
+// ---------------------------------------------------------------- launches
+
+template <typename T, bool kPair, bool kGrad>
+tcg_status launch(const Params& p, const Plan& pl, cudaStream_t stream) {
+    auto* kernel = tcg::xent::xent_kernel<T, kPair, kGrad>;
+    constexpr int kSmem = tcg::xent::Shape<kPair>::kSmemBytes;
+    static tcg::host::OncePerDevice once;
+    cudaError_t e = once([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+    if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent kernel attributes", e);
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3((kPair ? 2 : 1) * pl.workers);
+    cfg.blockDim = dim3(tcg::xent::kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kPair ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, p);
+    return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch("tcg_linear_xent", e);
+}
+
+// The tiles of words [first, first + cols) on X's rows.
+template <bool kGrad>
+tcg_status launch_tiles(Params& p, tcg_dtype dtype, const void* X, int ldx, const void* W, int ldw, int tokens, int hidden,
+                        int first, int cols, const tcg::host::Device& dev, cudaStream_t stream) {
+    const Plan pl = make_plan(tokens, cols, dev.num_sms);
+    const int atoms = pl.pair ? tcg::xent::Shape<true>::kAtoms : tcg::xent::Shape<false>::kAtoms;
+    p.tokens = tokens;
+    p.cols = cols;
+    p.first = first;
+    p.num_m = pl.num_m;
+    p.num_n = pl.num_n;
+    p.num_kb = static_cast<int>(blocks(2LL * hidden, tcg::xent::kRowBytes * atoms));
+    p.tile_n = pl.tile_n;
+    p.raster_m = 16;
+    p.fmt = dtype == TCG_F16 ? 0u : 1u;
+    p.timeout_ns = tcg::host::wait_timeout_ns();
+    p.fault_inject = tcg::host::fault_inject();
+    const char* w = static_cast<const char*>(W) + static_cast<size_t>(first) * ldw * 2;
+    tcg_status st = tcg::host::map_bytes(&p.tmX, X, 2ull * hidden, tokens, 2ull * ldx, tcg::xent::kRowBytes, tcg::xent::kBM);
+    if (st == TCG_OK)
+        st = tcg::host::map_bytes(&p.tmW, w, 2ull * hidden, cols, 2ull * ldw, tcg::xent::kRowBytes, pl.pair ? pl.tile_n / 2 : pl.tile_n);
+    if (st != TCG_OK) return st;
+    if (dtype == TCG_F16)
+        return pl.pair ? launch<__half, true, kGrad>(p, pl, stream) : launch<__half, false, kGrad>(p, pl, stream);
+    return pl.pair ? launch<__nv_bfloat16, true, kGrad>(p, pl, stream) : launch<__nv_bfloat16, false, kGrad>(p, pl, stream);
+}
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+int size_of(tcg_dtype t) { return t == TCG_F32 ? 4 : 2; }
+
+tcg_status check(int tokens, int vocab, int hidden, tcg_dtype dtype, const void* X, int ldx, const void* W, int ldw,
+                 const int* target) {
+    if (tokens < 0 || vocab < 1 || hidden < 1) return TCG_ERR_INVALID_ARG;
+    if (dtype != TCG_BF16 && dtype != TCG_F16) return TCG_ERR_INVALID_ARG;
+    // (extents in bytes, and the number of tiles, are ints)
+    if (tokens > tcg::host::kMaxExtent / 2 || vocab > tcg::host::kMaxExtent / 2 || hidden > tcg::host::kMaxExtent / 4 ||
+        blocks(tokens, 128) * blocks(vocab, kMinTileN) > tcg::host::kMaxExtent / 2)
+        return TCG_ERR_UNSUPPORTED;
+    if (!W || ldw < hidden || (tokens > 0 && (!X || ldx < hidden || !target))) return TCG_ERR_INVALID_ARG;
+    if (!aligned(X, 2) || !aligned(W, 2) || !aligned(target, 4)) return TCG_ERR_MISALIGNED;
+    // what the TMA can address
+    if (!aligned(W, 16) || ldw % 8 || (tokens > 0 && (!aligned(X, 16) || ldx % 8))) return TCG_ERR_UNSUPPORTED;
+    return TCG_OK;
+}
+
+tcg_status check_gradient(const void* d, int ld, int hidden, tcg_dtype t) {
+    if (!d) return TCG_OK;
+    if (t != TCG_BF16 && t != TCG_F16 && t != TCG_F32) return TCG_ERR_INVALID_ARG;
+    if (ld < hidden) return TCG_ERR_INVALID_ARG;
+    return aligned(d, size_of(t)) ? TCG_OK : TCG_ERR_MISALIGNED;
+}
+
+tcg_status to_half(const float* src, int lds, void* dst, long long ldd, int rows, int cols, float beta, cudaStream_t stream) {
+    if (rows == 0) return TCG_OK;
+    Half p = {src, lds, static_cast<__half*>(dst), ldd, rows, cols, beta};
+    const dim3 grid(std::min(rows, 4096), static_cast<unsigned>(blocks(cols, 256)));
+    const cudaError_t e = tcg::host::launch_early(half_kernel, grid, 256, stream, p);
+    return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch("tcg_linear_xent_backward", e);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tcg_linear_xent_workspace_size(int tokens, int vocab, int hidden, int backward) {
+    if (tokens < 0 || vocab < 1 || hidden < 1) return 0;
+    const size_t forward = forward_layout(tokens, vocab).bytes;
+    return backward ? std::max(forward, backward_layout(tokens, vocab, hidden).bytes) : forward;
+}
+
+tcg_status tcg_linear_xent(int tokens, int vocab, int hidden, tcg_dtype dtype, const void* X, int ldx, const void* W, int ldw,
+                           const int* target, float* lse, float* loss, float* mean, int* num_valid, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    tcg_status st = check(tokens, vocab, hidden, dtype, X, ldx, W, ldw, target);
+    if (st != TCG_OK) return st;
+    if (!mean || !num_valid || (tokens > 0 && !lse)) return TCG_ERR_INVALID_ARG;
+    if (!aligned(lse, 4) || !aligned(loss, 4) || !aligned(mean, 4) || !aligned(num_valid, 4)) return TCG_ERR_MISALIGNED;
+    tcg::host::Device dev;
+    if ((st = tcg::host::device(dev)) != TCG_OK) return st;
+    const Layout l = forward_layout(tokens, vocab);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < l.bytes)
+        return tcg::host::fail(TCG_ERR_WORKSPACE, "workspace NULL, not 16-byte aligned or smaller than tcg_linear_xent_workspace_size");
+    char* ws = static_cast<char*>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Params p;
+    memset(&p, 0, sizeof p);
+    p.target = target;
+    p.part = reinterpret_cast<float2*>(ws + l.part);
+    p.picked = reinterpret_cast<float*>(ws + l.picked);
+    p.status = reinterpret_cast<int*>(ws);
+    if (tokens > 0 && (st = launch_tiles<false>(p, dtype, X, ldx, W, ldw, tokens, hidden, 0, vocab, dev, s)) != TCG_OK) return st;
+    Finish f = {};
+    f.part = p.part;
+    f.num_n = p.num_n;
+    f.tokens = tokens;
+    f.vocab = vocab;
+    f.picked = p.picked;
+    f.target = target;
+    f.lse = lse;
+    f.loss = loss;
+    f.mean = mean;
+    f.valid = num_valid;
+    f.sums = reinterpret_cast<double*>(ws + l.sums);
+    f.counts = reinterpret_cast<int*>(ws + l.counts);
+    f.arrivals = reinterpret_cast<int*>(ws + tcg::host::kWorkspaceHeader);
+    const dim3 grid(static_cast<unsigned>(std::max(1LL, blocks(tokens, kFinishRows))));
+    const cudaError_t e = tcg::host::launch_early(finish_kernel, grid, kFinishThreads, s, f);
+    return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch("tcg_linear_xent", e);
+}
+
+tcg_status tcg_linear_xent_backward(int tokens, int vocab, int hidden, tcg_dtype dtype, const void* X, int ldx, const void* W,
+                                    int ldw, const int* target, const float* lse, const int* num_valid, const float* grad_mean,
+                                    const float* grad_loss, void* dX, int lddx, tcg_dtype dx_dtype, float dw_beta, void* dW,
+                                    int lddw, tcg_dtype dw_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    tcg_status st = check(tokens, vocab, hidden, dtype, X, ldx, W, ldw, target);
+    if (st == TCG_OK) st = check_gradient(dX, lddx, hidden, dx_dtype);
+    if (st == TCG_OK) st = check_gradient(dW, lddw, hidden, dw_dtype);
+    if (st != TCG_OK) return st;
+    if (!num_valid || (tokens > 0 && !lse)) return TCG_ERR_INVALID_ARG;
+    if (!aligned(lse, 4) || !aligned(num_valid, 4) || !aligned(grad_mean, 4) || !aligned(grad_loss, 4)) return TCG_ERR_MISALIGNED;
+    tcg::host::Device dev;
+    if ((st = tcg::host::device(dev)) != TCG_OK) return st;
+    const Layout l = backward_layout(tokens, vocab, hidden);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < l.bytes)
+        return tcg::host::fail(TCG_ERR_WORKSPACE, "workspace NULL, not 16-byte aligned or smaller than tcg_linear_xent_workspace_size");
+    if (!dX && !dW) return TCG_OK;
+    char* ws = static_cast<char*>(workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int words = piece_words(tokens, vocab), ld = padded_hidden(hidden);
+    const int pitch = static_cast<int>(blocks(words, 32) * 32);
+    const bool half = dtype == TCG_F16;
+    float* r = reinterpret_cast<float*>(ws + l.r);
+    float* back = reinterpret_cast<float*>(ws + l.back);
+    void* dz = ws + l.dz;
+    float* dx32 = reinterpret_cast<float*>(ws + l.dx);
+    float* dw32 = reinterpret_cast<float*>(ws + l.dw);
+    if (tokens > 0) {
+        Scales sc = {tokens, vocab, std::max(tokens, words), target, num_valid, grad_mean, grad_loss, half, r, back};
+        const cudaError_t e = tcg::host::launch_early(scales_kernel, dim3(1), 1024, s, sc);
+        if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent_backward", e);
+    }
+    const tcg_epilogue none = {nullptr, TCG_BF16, TCG_ACT_NONE};
+    tcg_scales scales;
+    memset(&scales, 0, sizeof scales);
+    scales.scale_a = scales.scale_b = 1.0f;
+    scales.row_scale = half ? back : nullptr;
+    for (int v0 = 0; v0 < vocab; v0 += words) {
+        const int n = std::min(words, vocab - v0);
+        const bool last = v0 + n == vocab;
+        const char* w = static_cast<const char*>(W) + static_cast<size_t>(v0) * ldw * 2;
+        if (tokens > 0) {
+            Params p;
+            memset(&p, 0, sizeof p);
+            p.target = target;
+            p.lse = lse;
+            p.scale = r;
+            p.d = dz;
+            p.ldd = pitch;
+            p.status = reinterpret_cast<int*>(ws);
+            if ((st = launch_tiles<true>(p, dtype, X, ldx, W, ldw, tokens, hidden, v0, n, dev, s)) != TCG_OK) return st;
+        }
+        if (dX && tokens > 0) {
+            // fp32 sums of the pieces so far, in dX itself where it is fp32
+            const bool own = dx_dtype == TCG_F32;
+            float* sum = own ? static_cast<float*>(dX) : dx32;
+            const int lds = own ? lddx : ld;
+            const bool out = !own && last && dx_dtype == TCG_BF16;
+            st = tcg_gemm(tokens, hidden, n, 1.0f, dz, pitch, TCG_ROW, w, ldw, TCG_ROW, v0 > 0 ? 1.0f : 0.0f, sum, lds, TCG_F32,
+                          out ? dX : sum, out ? lddx : lds, out ? TCG_BF16 : TCG_F32, none, dtype, scales, ws, l.r, s);
+            if (st == TCG_OK && last && dx_dtype == TCG_F16) st = to_half(sum, lds, dX, lddx, tokens, hidden, 0.0f, s);
+            if (st != TCG_OK) return st;
+        }
+        if (dW) {
+            const bool direct = dw_dtype != TCG_F16;
+            char* d = static_cast<char*>(dW) + static_cast<size_t>(v0) * lddw * size_of(dw_dtype);
+            st = tcg_gemm(n, hidden, tokens, 1.0f, dz, pitch, TCG_COL, X, ldx, TCG_ROW, direct ? dw_beta : 0.0f, d, lddw, direct ? dw_dtype : TCG_F32,
+                          direct ? static_cast<void*>(d) : dw32, direct ? lddw : ld, direct ? dw_dtype : TCG_F32, none, dtype, scales, ws,
+                          l.r, s);
+            if (st == TCG_OK && !direct) st = to_half(dw32, ld, d, lddw, n, hidden, dw_beta, s);
+            if (st != TCG_OK) return st;
+        }
+    }
+    return TCG_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,591 @@
+// moe_rows.cu -- the way of tokens to their experts and back.
+//
+//   sort      the assignments (t, j) in the order of (expert, t, j): where each
+//             expert's rows start, the token of a row, the row of an assignment
+//   dispatch  x[row_of[t, j]] = y[t]
+//   combine   y[t] = sum_j w_tj x[row_of[t, j]]
+//   gradient  dx[row_of[t, j]] = w_tj dy[t],  dw_tj = sum_c dy[t, c] x[row_of[t, j], c]
+//
+// The sort counts: CTAs own runs of neighbouring assignments and their warps
+// runs of those, so a row is the expert's start, plus the expert's assignments
+// in the CTAs and warps before, plus its place among equal ones of the warp.
+// Two launches (counts per CTA; places), one where a single CTA holds all; the
+// second starts while the first runs and counts its own run meanwhile.
+//
+// The other three go by tokens, so that a token's row is read or written once
+// however many experts it has, and each expert's row once.  Bound by memory.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "host.h"
+#include "values.cuh"
+
+namespace {
+
+using namespace tcg;
+
+constexpr int kMaxExperts = 1024;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+// ------------------------------------------------------------------- sort
+
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+// Assignments a CTA takes at least.
+constexpr int kSortRun = 2048;
+// As many as this are one CTA's, in one launch.
+constexpr int kSortAlone = 4096;
+
+struct Sort {
+    const int* topk;
+    long long ld_topk;
+    const uint8_t* mask;
+    int total, k, experts;       // total: tokens * k
+    int* offsets;
+    int* row_token;
+    int* row_of;
+    long long ld_row_of;
+    int* counts;                 // [CTA][expert], nullptr where one CTA holds all
+};
+
+__device__ __forceinline__ int run_start(int total, int part, int parts) {
+    return static_cast<int>(static_cast<long long>(total) * part / parts);
+}
+
+// The expert of assignment a, -1 where it has none.
+__device__ __forceinline__ int expert_of(const Sort& p, int a, int& t, int& j) {
+    t = static_cast<int>(static_cast<unsigned>(a) / static_cast<unsigned>(p.k));
+    j = a - t * p.k;
+    if (p.mask && !__ldcg(p.mask + t)) return -1;
+    const int e = __ldcg(p.topk + t * p.ld_topk + j);
+    return e >= 0 && e < p.experts ? e : -1;
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_constant__ Sort p) {
+    __shared__ int hist[kMaxExperts];
+    // (the second launch may read the assignments from here on: they were there before this one)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int e = threadIdx.x; e < p.experts; e += kSortThreads) hist[e] = 0;
+    __syncthreads();
+    const int a1 = run_start(p.total, blockIdx.x + 1, gridDim.x);
+    for (int a = run_start(p.total, blockIdx.x, gridDim.x) + static_cast<int>(threadIdx.x); a < a1; a += kSortThreads) {
+        int t, j;
+        const int e = expert_of(p, a, t, j);
+        if (e >= 0) atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.experts; e += kSortThreads) p.counts[static_cast<size_t>(blockIdx.x) * p.experts + e] = hist[e];
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_constant__ Sort p) {
+    extern __shared__ int smem[];
+    int* total = smem;                       // [experts]: all assignments, then the expert's first row
+    int* before = smem + p.experts;          // [experts]: those of the CTAs before
+    int* place = smem + 2 * p.experts;       // [warp][experts]: counts, then the warp's next row
+    __shared__ int rows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool alone = p.counts == nullptr;
+    if (alone) asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = threadIdx.x; i < (kSortWarps + 2) * p.experts; i += kSortThreads) smem[i] = 0;
+    __syncthreads();
+    const int c0 = run_start(p.total, blockIdx.x, gridDim.x), c1 = run_start(p.total, blockIdx.x + 1, gridDim.x);
+    const int a0 = c0 + run_start(c1 - c0, warp, kSortWarps), a1 = c0 + run_start(c1 - c0, warp + 1, kSortWarps);
+    int* mine = place + warp * p.experts;
+    for (int a = a0 + lane; a < a1; a += 32) {
+        int t, j;
+        const int e = expert_of(p, a, t, j);
+        if (e >= 0) atomicAdd(&mine[e], 1);
+    }
+    if (!alone) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        // parts threads an expert add up the CTAs' counts
+        const int per = min(kSortThreads, (p.experts + 31) / 32 * 32), parts = kSortThreads / per;
+        const int part = threadIdx.x / per;
+        if (part < parts) {
+            for (int e = threadIdx.x - part * per; e < p.experts; e += per) {
+                int all = 0, ahead = 0;
+#pragma unroll 8
+                for (int b = part; b < static_cast<int>(gridDim.x); b += parts) {
+                    const int n = p.counts[static_cast<size_t>(b) * p.experts + e];
+                    all += n;
+                    ahead += b < static_cast<int>(blockIdx.x) ? n : 0;
+                }
+                atomicAdd(&total[e], all);
+                atomicAdd(&before[e], ahead);
+            }
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __syncthreads();
+    if (alone) {
+        for (int e = threadIdx.x; e < p.experts; e += kSortThreads) {
+            int n = 0;
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) n += place[w * p.experts + e];
+            total[e] = n;
+        }
+        __syncthreads();
+    }
+    if (warp == 0) {
+        // each lane a run of experts
+        const int per = (p.experts + 31) / 32, e0 = min(lane * per, p.experts), e1 = min(e0 + per, p.experts);
+        int n = 0;
+        for (int e = e0; e < e1; ++e) n += total[e];
+        int start = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(kAll, start, d);
+            if (lane >= d) start += o;
+        }
+        if (lane == 31) rows = start;
+        start -= n;
+        for (int e = e0; e < e1; ++e) {
+            const int m = total[e];
+            total[e] = start;
+            start += m;
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.experts; e += kSortThreads) {
+        int next = total[e] + before[e];
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int n = place[w * p.experts + e];
+            place[w * p.experts + e] = next;
+            next += n;
+        }
+        if (p.offsets && blockIdx.x == 0) p.offsets[e] = total[e];
+    }
+    if (p.offsets && blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.experts] = rows;
+    __syncthreads();
+    for (int b = a0; b < a1; b += 32) {
+        const int a = b + lane;
+        int t = 0, j = 0;
+        const int e = a < a1 ? expert_of(p, a, t, j) : -1;
+        const uint32_t same = __match_any_sync(kAll, e);
+        int row = -1;
+        if (e >= 0) row = mine[e] + __popc(same & ((1u << lane) - 1u));
+        __syncwarp();
+        if (e >= 0 && (same >> lane) == 1u) mine[e] = row + 1;   // the last of its equals
+        __syncwarp();
+        if (row >= 0) p.row_token[row] = t;
+        if (a < a1) p.row_of[t * p.ld_row_of + j] = row;
+    }
+    for (int r = rows + static_cast<int>(blockIdx.x * kSortThreads + threadIdx.x); r < p.total; r += static_cast<int>(gridDim.x) * kSortThreads)
+        p.row_token[r] = -1;
+}
+
+// --------------------------------------------- rows to their experts and back
+
+constexpr int kMoveThreads = 256;
+constexpr int kSteps = 2;          // eight columns each that a thread has on its way
+constexpr int kMaxCols = 65535 * kMoveThreads * 8 * kSteps;   // a grid's second extent
+
+struct Rows {
+    const void* y;      // tokens' side: read by dispatch and the gradient, written by combine
+    long long ldy;
+    const void* x;      // experts' side
+    long long ldx;
+    void* out;          // what is written
+    long long ldo;
+    int tokens, k, cols, rows;
+    const int* row_of;
+    long long ld_row_of;
+    const float* weights;
+    long long ld_weights;
+    float* dweights;
+    long long ld_dweights;
+    int vec_in, vec_out, vec_y;   // eight values of x, out and y may be moved as whole words
+    int lanes;          // threads a token
+};
+
+// Where this thread works: its token and its first eight columns.
+struct Place {
+    long long t;
+    int c0, step;
+};
+__device__ __forceinline__ Place place_of(const Rows& p) {
+    Place w;
+    const int slot = threadIdx.x / p.lanes;
+    w.t = static_cast<long long>(blockIdx.x) * (kMoveThreads / p.lanes) + slot;
+    w.c0 = (static_cast<int>(blockIdx.y) * p.lanes * kSteps + static_cast<int>(threadIdx.x) - slot * p.lanes) * 8;
+    w.step = p.lanes * 8;
+    return w;
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> fetch(const T* row, int c, int cols, int vec) {
+    return vec && c + 8 <= cols ? load_raw8<T, true>(row + c) : load_some8<T>(row + c, cols - c);
+}
+template <typename T>
+__device__ __forceinline__ void put(T* row, int c, int cols, int vec, const Raw8<T>& v) {
+    if (vec && c + 8 <= cols) store_raw8<T>(row + c, v);
+    else store_some8<T>(row + c, v, cols - c);
+}
+
+// The row of an assignment, -1 where it has none.
+__device__ __forceinline__ int row_at(const Rows& p, long long t, int j) {
+    const int r = p.row_of[t * p.ld_row_of + j];
+    return r >= 0 && r < p.rows ? r : -1;
+}
+
+template <typename TY, typename TX>
+__global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const __grid_constant__ Rows p) {
+    tcg::host::wait_for_kernel_ahead();
+    const Place w = place_of(p);
+    if (w.t >= p.tokens) return;
+    const TY* src = static_cast<const TY*>(p.y) + w.t * p.ldy;
+    Raw8<TX> v[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int c = w.c0 + s * w.step;
+        if (c >= p.cols) break;
+        const Raw8<TY> r = fetch<TY>(src, c, p.cols, p.vec_y);
+        if constexpr (std::is_same<TX, TY>::value) {
+            v[s] = r;
+        } else {
+            float f[8];
+            values_of<TY>(r, f);
+            v[s] = raw_of<TX>(f);
+        }
+    }
+    for (int j = 0; j < p.k; ++j) {
+        const int r = row_at(p, w.t, j);
+        if (r < 0) continue;
+        TX* dst = static_cast<TX*>(p.out) + r * p.ldo;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int c = w.c0 + s * w.step;
+            if (c < p.cols) put<TX>(dst, c, p.cols, p.vec_out, v[s]);
+        }
+    }
+}
+
+// kJ assignments' rows are on their way at once; sums in the order of j.
+template <typename TX, typename TY, int kJ>
+__global__ void __launch_bounds__(kMoveThreads) combine_kernel(const __grid_constant__ Rows p) {
+    tcg::host::wait_for_kernel_ahead();
+    const Place w = place_of(p);
+    if (w.t >= p.tokens) return;
+    float acc[kSteps][8];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[s][i] = 0.0f;
+    for (int j0 = 0; j0 < p.k; j0 += kJ) {
+        Raw8<TX> v[kJ][kSteps];
+        int row[kJ];
+        float wt[kJ];
+#pragma unroll
+        for (int q = 0; q < kJ; ++q) {
+            row[q] = j0 + q < p.k ? row_at(p, w.t, j0 + q) : -1;
+            wt[q] = row[q] < 0 ? 0.0f : (p.weights ? p.weights[w.t * p.ld_weights + j0 + q] : 1.0f);
+        }
+#pragma unroll
+        for (int q = 0; q < kJ; ++q)
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int c = w.c0 + s * w.step;
+                if (row[q] >= 0 && c < p.cols) v[q][s] = fetch<TX>(static_cast<const TX*>(p.x) + row[q] * p.ldx, c, p.cols, p.vec_in);
+            }
+#pragma unroll
+        for (int q = 0; q < kJ; ++q)
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                if (row[q] < 0 || w.c0 + s * w.step >= p.cols) continue;
+                float f[8];
+                values_of<TX>(v[q][s], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[s][i] = fmaf(wt[q], f[i], acc[s][i]);
+            }
+    }
+    TY* dst = static_cast<TY*>(p.out) + w.t * p.ldo;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int c = w.c0 + s * w.step;
+        if (c < p.cols) put<TY>(dst, c, p.cols, p.vec_out, raw_of<TY>(acc[s]));
+    }
+}
+
+// p.lanes threads a token (a power of two from 32 on), over all its columns;
+// kJ assignments at a time, whose weights' gradients are summed in a fixed order.
+template <typename TX, typename TY, int kJ>
+__global__ void __launch_bounds__(kMoveThreads) combine_grad_kernel(const __grid_constant__ Rows p) {
+    tcg::host::wait_for_kernel_ahead();
+    __shared__ float part[kJ][kMoveThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int slot = threadIdx.x / p.lanes, per_cta = kMoveThreads / p.lanes, warps = p.lanes / 32;
+    const long long t = static_cast<long long>(blockIdx.x) * per_cta + slot;
+    const bool in = t < p.tokens;
+    const int first = (static_cast<int>(threadIdx.x) - slot * p.lanes) * 8, step = p.lanes * 8;
+    const TY* dy = static_cast<const TY*>(p.y) + (in ? t : 0) * p.ldy;
+    for (int j0 = 0; j0 < p.k; j0 += kJ) {
+        int row[kJ];
+        float wt[kJ], dot[kJ];
+#pragma unroll
+        for (int q = 0; q < kJ; ++q) {
+            row[q] = in && j0 + q < p.k ? row_at(p, t, j0 + q) : -1;
+            wt[q] = row[q] < 0 ? 0.0f : (p.weights ? p.weights[t * p.ld_weights + j0 + q] : 1.0f);
+            dot[q] = 0.0f;
+        }
+        if (in) {
+            for (int c = first; c < p.cols; c += step) {
+                Raw8<TX> v[kJ];
+                const Raw8<TY> g = fetch<TY>(dy, c, p.cols, p.vec_y);
+#pragma unroll
+                for (int q = 0; q < kJ; ++q)
+                    if (row[q] >= 0 && p.dweights) v[q] = fetch<TX>(static_cast<const TX*>(p.x) + row[q] * p.ldx, c, p.cols, p.vec_in);
+                float d[8];
+                values_of<TY>(g, d);
+#pragma unroll
+                for (int q = 0; q < kJ; ++q) {
+                    if (row[q] < 0) continue;
+                    float f[8];
+                    if (p.dweights) {
+                        values_of<TX>(v[q], f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dot[q] = fmaf(f[i], d[i], dot[q]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = wt[q] * d[i];
+                    put<TX>(static_cast<TX*>(p.out) + row[q] * p.ldo, c, p.cols, p.vec_out, raw_of<TX>(f));
+                }
+            }
+        }
+        if (!p.dweights) continue;
+#pragma unroll
+        for (int q = 0; q < kJ; ++q) {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) dot[q] += __shfl_xor_sync(kAll, dot[q], d);
+            if (lane == 0) part[q][warp] = dot[q];
+        }
+        __syncthreads();
+        if (in && first == 0) {
+#pragma unroll
+            for (int q = 0; q < kJ; ++q) {
+                if (j0 + q >= p.k) continue;
+                float sum = 0.0f;
+                for (int i = 0; i < warps; ++i) sum += part[q][warp + i];
+                p.dweights[t * p.ld_dweights + j0 + q] = row[q] < 0 ? 0.0f : sum;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+int size_of(tcg_dtype t) { return t == TCG_F32 ? 4 : 2; }
+bool known(tcg_dtype t) { return t == TCG_BF16 || t == TCG_F16 || t == TCG_F32; }
+bool whole_words(const void* p, int ld, tcg_dtype t) { return aligned(p, 16) && static_cast<long long>(ld) * size_of(t) % 16 == 0; }
+
+tcg_status start(Rows& p, int tokens, int k, int cols, int rows, const int* row_of, int ld_row_of) {
+    if (tokens < 0 || k < 1 || cols < 0 || rows < 0) return TCG_ERR_INVALID_ARG;
+    if (std::max(tokens, rows) > tcg::host::kMaxExtent || cols > kMaxCols) return TCG_ERR_UNSUPPORTED;
+    if (tokens == 0) return TCG_OK;
+    if (!row_of || ld_row_of < k) return TCG_ERR_INVALID_ARG;
+    if (!aligned(row_of, 4)) return TCG_ERR_MISALIGNED;
+    p.tokens = tokens;
+    p.k = k;
+    p.cols = cols;
+    p.rows = rows;
+    p.row_of = row_of;
+    p.ld_row_of = ld_row_of;
+    return TCG_OK;
+}
+
+// A matrix of `cols` columns that has to be there (where it has rows).
+tcg_status check_matrix(const void* m, int ld, int cols, tcg_dtype t, bool needed = true) {
+    if (!known(t)) return TCG_ERR_INVALID_ARG;
+    if (needed && (!m || ld < cols)) return TCG_ERR_INVALID_ARG;
+    return aligned(m, size_of(t)) ? TCG_OK : TCG_ERR_MISALIGNED;
+}
+
+template <typename F>
+void with_type(tcg_dtype t, F f) {
+    if (t == TCG_BF16) f(__nv_bfloat16{});
+    else if (t == TCG_F16) f(__half{});
+    else f(float{});
+}
+
+// Threads a token: as many as its columns occupy at `steps` of eight each.
+int lanes_for(int cols, int steps) {
+    const int want = (cols + 8 * steps - 1) / (8 * steps);
+    int lanes = 32;
+    while (lanes < want && lanes < kMoveThreads) lanes *= 2;
+    return lanes;
+}
+dim3 move_grid(const Rows& p) {
+    const int per_cta = kMoveThreads / p.lanes, span = p.lanes * 8 * kSteps;
+    return dim3(static_cast<unsigned>((static_cast<long long>(p.tokens) + per_cta - 1) / per_cta),
+                static_cast<unsigned>((static_cast<long long>(p.cols) + span - 1) / span));
+}
+
+tcg_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch(what, e); }
+
+int sort_ctas(long long total, int sms) {
+    return total <= kSortAlone ? 1 : static_cast<int>(std::min<long long>(sms, (total + kSortRun - 1) / kSortRun));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tcg_moe_sort_workspace_size(int tokens, int experts, int k) {
+    if (tokens < 0 || experts < 1 || k < 1 || experts > kMaxExperts) return 0;
+    tcg::host::Device dev;
+    if (tcg::host::device(dev) != TCG_OK) dev.num_sms = 1024;
+    const int ctas = sort_ctas(static_cast<long long>(tokens) * k, dev.num_sms);
+    return tcg::host::kScratchAt + (ctas > 1 ? static_cast<size_t>(ctas) * experts * sizeof(int) : 0);
+}
+
+tcg_status tcg_moe_sort(int tokens, int experts, int k, const int* topk, int ld_topk, const uint8_t* mask, int* offsets,
+                        int* row_token, int* row_of, int ld_row_of, void* workspace, size_t workspace_bytes, void* stream) {
+    if (tokens < 0 || experts < 1 || k < 1) return TCG_ERR_INVALID_ARG;
+    // (rows are ints, and a run's end plus a step still is one)
+    if (experts > kMaxExperts || static_cast<long long>(tokens) * k > tcg::host::kMaxExtent - (1 << 20)) return TCG_ERR_UNSUPPORTED;
+    if (tokens > 0 && (!topk || ld_topk < k || !row_token || !row_of || ld_row_of < k)) return TCG_ERR_INVALID_ARG;
+    if (!aligned(topk, 4) || !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(row_of, 4)) return TCG_ERR_MISALIGNED;
+    tcg::host::Device dev;
+    tcg_status st = tcg::host::device(dev);
+    if (st != TCG_OK) return st;
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < tcg_moe_sort_workspace_size(tokens, experts, k))
+        return tcg::host::fail(TCG_ERR_WORKSPACE, "workspace NULL, not 16-byte aligned or smaller than tcg_moe_sort_workspace_size");
+    static tcg::host::OncePerDevice once;
+    cudaError_t err = once([] {
+        return cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (kSortWarps + 2) * kMaxExperts * static_cast<int>(sizeof(int)));
+    });
+    if (err != cudaSuccess) return launched(err, "tcg_moe_sort kernel attributes");
+    Sort p = {};
+    p.topk = topk;
+    p.ld_topk = ld_topk;
+    p.mask = mask;
+    p.total = tokens * k;
+    p.k = k;
+    p.experts = experts;
+    p.offsets = offsets;
+    p.row_token = row_token;
+    p.row_of = row_of;
+    p.ld_row_of = ld_row_of;
+    const int ctas = sort_ctas(p.total, dev.num_sms);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (ctas > 1) {
+        p.counts = reinterpret_cast<int*>(static_cast<char*>(workspace) + tcg::host::kScratchAt);
+        err = tcg::host::launch_early(sort_count_kernel, dim3(ctas), kSortThreads, s, p);
+        if (err != cudaSuccess) return launched(err, "tcg_moe_sort");
+    }
+    return launched(tcg::host::launch_early(sort_place_kernel, dim3(ctas), kSortThreads, s, p,
+                                            (kSortWarps + 2) * static_cast<size_t>(experts) * sizeof(int)), "tcg_moe_sort");
+}
+
+tcg_status tcg_moe_dispatch(int tokens, int k, int cols, int rows, const void* x, int ldx, tcg_dtype x_dtype, const int* row_of,
+                            int ld_row_of, void* out, int ldo, tcg_dtype out_dtype, void* stream) {
+    Rows p = {};
+    tcg_status st = start(p, tokens, k, cols, rows, row_of, ld_row_of);
+    if (st == TCG_OK) st = check_matrix(x, ldx, cols, x_dtype, tokens > 0);
+    if (st == TCG_OK) st = check_matrix(out, ldo, cols, out_dtype, rows > 0 && tokens > 0);
+    if (st != TCG_OK || tokens == 0 || cols == 0 || rows == 0) return st;
+    tcg::host::Device dev;
+    if ((st = tcg::host::device(dev)) != TCG_OK) return st;
+    p.y = x;
+    p.ldy = ldx;
+    p.out = out;
+    p.ldo = ldo;
+    p.vec_y = whole_words(x, ldx, x_dtype);
+    p.vec_out = whole_words(out, ldo, out_dtype);
+    p.lanes = lanes_for(cols, kSteps);
+    cudaError_t err = cudaSuccess;
+    with_type(x_dtype, [&](auto y) {
+        with_type(out_dtype, [&](auto o) {
+            err = tcg::host::launch_early(dispatch_kernel<decltype(y), decltype(o)>, move_grid(p), kMoveThreads,
+                                          static_cast<cudaStream_t>(stream), p);
+        });
+    });
+    return launched(err, "tcg_moe_dispatch");
+}
+
+tcg_status tcg_moe_combine(int tokens, int k, int cols, int rows, const void* x, int ldx, tcg_dtype x_dtype, const int* row_of,
+                           int ld_row_of, const float* weights, int ld_weights, void* y, int ldy, tcg_dtype y_dtype,
+                           void* stream) {
+    Rows p = {};
+    tcg_status st = start(p, tokens, k, cols, rows, row_of, ld_row_of);
+    if (st == TCG_OK) st = check_matrix(x, ldx, cols, x_dtype, rows > 0 && tokens > 0);
+    if (st == TCG_OK) st = check_matrix(y, ldy, cols, y_dtype, tokens > 0);
+    if (st != TCG_OK || tokens == 0 || cols == 0) return st;
+    if (weights && ld_weights < k) return TCG_ERR_INVALID_ARG;
+    if (!aligned(weights, 4)) return TCG_ERR_MISALIGNED;
+    tcg::host::Device dev;
+    if ((st = tcg::host::device(dev)) != TCG_OK) return st;
+    p.x = x;
+    p.ldx = ldx;
+    p.weights = weights;
+    p.ld_weights = ld_weights;
+    p.out = y;
+    p.ldo = ldy;
+    p.vec_in = whole_words(x, ldx, x_dtype);
+    p.vec_out = whole_words(y, ldy, y_dtype);
+    p.lanes = lanes_for(cols, kSteps);
+    cudaError_t err = cudaSuccess;
+    with_type(x_dtype, [&](auto a) {
+        with_type(y_dtype, [&](auto b) {
+            const auto run = [&](auto* kernel) {
+                err = tcg::host::launch_early(kernel, move_grid(p), kMoveThreads, static_cast<cudaStream_t>(stream), p);
+            };
+            if (k == 1) run(combine_kernel<decltype(a), decltype(b), 1>);
+            else if (k == 2) run(combine_kernel<decltype(a), decltype(b), 2>);
+            else run(combine_kernel<decltype(a), decltype(b), 4>);
+        });
+    });
+    return launched(err, "tcg_moe_combine");
+}
+
+tcg_status tcg_moe_combine_backward(int tokens, int k, int cols, int rows, const void* x, int ldx, tcg_dtype x_dtype,
+                                    const int* row_of, int ld_row_of, const float* weights, int ld_weights, const void* dy,
+                                    int lddy, tcg_dtype dy_dtype, void* dx, int lddx, float* dweights, int ld_dweights,
+                                    void* stream) {
+    Rows p = {};
+    tcg_status st = start(p, tokens, k, cols, rows, row_of, ld_row_of);
+    if (tokens > 0 && st == TCG_OK && dweights && ld_dweights < k) return TCG_ERR_INVALID_ARG;
+    if (st == TCG_OK) st = check_matrix(x, ldx, cols, x_dtype, rows > 0 && tokens > 0 && dweights);
+    if (st == TCG_OK) st = check_matrix(dy, lddy, cols, dy_dtype, tokens > 0);
+    if (st == TCG_OK) st = check_matrix(dx, lddx, cols, x_dtype, rows > 0 && tokens > 0);
+    if (st != TCG_OK || tokens == 0) return st;
+    if (weights && ld_weights < k) return TCG_ERR_INVALID_ARG;
+    if (!aligned(weights, 4) || !aligned(dweights, 4)) return TCG_ERR_MISALIGNED;
+    tcg::host::Device dev;
+    if ((st = tcg::host::device(dev)) != TCG_OK) return st;
+    p.tokens = tokens;
+    p.k = k;
+    p.x = x;
+    p.ldx = ldx;
+    p.y = dy;
+    p.ldy = lddy;
+    p.weights = weights;
+    p.ld_weights = ld_weights;
+    p.out = dx;
+    p.ldo = lddx;
+    p.dweights = dweights;
+    p.ld_dweights = ld_dweights;
+    p.vec_in = whole_words(x, ldx, x_dtype);
+    p.vec_y = whole_words(dy, lddy, dy_dtype);
+    p.vec_out = whole_words(dx, lddx, x_dtype);
+    p.lanes = lanes_for(cols, 4);
+    const int per_cta = kMoveThreads / p.lanes;
+    const dim3 grid(static_cast<unsigned>((static_cast<long long>(tokens) + per_cta - 1) / per_cta));
+    cudaError_t err = cudaSuccess;
+    with_type(x_dtype, [&](auto a) {
+        with_type(dy_dtype, [&](auto b) {
+            const auto run = [&](auto* kernel) {
+                err = tcg::host::launch_early(kernel, grid, kMoveThreads, static_cast<cudaStream_t>(stream), p);
+            };
+            if (k == 1) run(combine_grad_kernel<decltype(a), decltype(b), 1>);
+            else if (k == 2) run(combine_grad_kernel<decltype(a), decltype(b), 2>);
+            else run(combine_grad_kernel<decltype(a), decltype(b), 4>);
+        });
+    });
+    return launched(err, "tcg_moe_combine_backward");
+}
+
+}  // extern "C"
