@@ -32,14 +32,16 @@ using tcg::xent::Params;
 // What dz of a piece may take of the workspace.
 constexpr size_t kPieceBytes = size_t(256) << 20;
 constexpr int kMinTileN = 128;
-constexpr int kFinishRows = 32, kFinishSlices = 16, kFinishThreads = kFinishRows * kFinishSlices;
+constexpr int kPartK = 1024;           // k of the statistics' products that the tensor cores sum in one go, about
+constexpr int kFinishRows = 32, kFinishSlices = 32, kFinishThreads = kFinishRows * kFinishSlices;
+constexpr int kFinishBatch = 8;
 constexpr float kHalfTop = 16384.0f;   // fp16: what the largest |r_t| becomes
 
 // ------------------------------------------------------- joining the tiles
 
 struct Finish {
     const float2* part;
-    int num_n, tokens, vocab;
+    int num_n, tokens, vocab;   // num_n: half column tiles
     const float* picked;
     const int* target;
     float* lse;
@@ -51,7 +53,8 @@ struct Finish {
     int* arrivals;
 };
 
-// 16 threads a row, each some of the column tiles; sums in a fixed order.
+// 32 threads a row, each some of the column tiles, eight of them on their way at
+// once; sums in a fixed order.
 __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Finish p) {
     tcg::host::wait_for_kernel_ahead();
     __shared__ float2 slot[kFinishSlices][kFinishRows];
@@ -64,9 +67,21 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
         return make_float2(m, a.y * exp2f(a.x - base) + b.y * exp2f(b.x - base));
     };
     float2 v = make_float2(-INFINITY, 0.0f);
-    if (in) {
-#pragma unroll 4
-        for (int n = slice; n < p.num_n; n += kFinishSlices) v = join(v, p.part[static_cast<size_t>(n) * p.tokens + row]);
+    for (int n0 = slice; in && n0 < p.num_n; n0 += kFinishSlices * kFinishBatch) {
+        float2 w[kFinishBatch];
+        float m = v.x;
+#pragma unroll
+        for (int i = 0; i < kFinishBatch; ++i) {
+            const int n = n0 + i * kFinishSlices;
+            w[i] = n < p.num_n ? p.part[static_cast<size_t>(n) * p.tokens + row] : make_float2(-INFINITY, 0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < kFinishBatch; ++i) m = fmaxf(m, w[i].x);
+        const float base = m == -INFINITY ? 0.0f : m;
+        float s = v.y * exp2f(v.x - base);
+#pragma unroll
+        for (int i = 0; i < kFinishBatch; ++i) s += w[i].y * exp2f(w[i].x - base);
+        v = make_float2(m, s);
     }
     slot[slice][r] = v;
     __syncthreads();
@@ -189,19 +204,21 @@ size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Plan {
     bool pair = false;
+    int parts = 1;     // accumulations that share a tile's K
     int tile_n = 256, num_m = 1, num_n = 1, workers = 1;
 };
 
 // The width whose waves of tiles take the least: a tile's time goes with its
 // columns, plus what a tile costs by itself (about sixteen columns' worth).
-Plan make_plan(int tokens, long long cols, int sms) {
+Plan make_plan(int tokens, long long cols, int hidden, bool grad, int sms) {
     Plan pl;
     pl.pair = tokens > tcg::xent::kBM;
+    pl.parts = grad ? 1 : std::max(1, (hidden + kPartK / 2) / kPartK);
     pl.num_m = static_cast<int>(blocks(tokens, pl.pair ? 256 : 128));
     const int workers = std::max(1, pl.pair ? sms / 2 : sms);
     long long best = LLONG_MAX;
     for (int w = tcg::xent::kMaxN; w >= kMinTileN; w -= 32) {
-        const long long tiles = pl.num_m * blocks(cols, w), cost = blocks(tiles, workers) * (w + 16);
+        const long long cost = blocks(pl.num_m * blocks(cols, w), workers) * (w + 16);
         if (cost < best) {
             best = cost;
             pl.tile_n = w;
@@ -235,7 +252,7 @@ struct Layout {
 Layout forward_layout(int tokens, int vocab) {
     Layout l;
     l.bytes = tcg::host::kScratchAt;
-    l.part = l.take(static_cast<size_t>(blocks(vocab, kMinTileN)) * tokens * sizeof(float2));
+    l.part = l.take(2 * static_cast<size_t>(blocks(vocab, kMinTileN)) * tokens * sizeof(float2));
     l.picked = l.take(static_cast<size_t>(tokens) * sizeof(float));
     l.sums = l.take(static_cast<size_t>(blocks(tokens, kFinishRows)) * sizeof(double));
     l.counts = l.take(static_cast<size_t>(blocks(tokens, kFinishRows)) * sizeof(int));
@@ -269,7 +286,14 @@ tcg_status launch(const Params& p, const Plan& pl, cudaStream_t stream) {
     auto* kernel = tcg::xent::xent_kernel<T, kPair, kGrad>;
     constexpr int kSmem = tcg::xent::Shape<kPair>::kSmemBytes;
     static tcg::host::OncePerDevice once;
-    cudaError_t e = once([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+    cudaError_t e = once([&] {
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaFuncAttributes a;
+        if (err == cudaSuccess) err = cudaFuncGetAttributes(&a, kernel);
+        // the register hand-over draws on what the block is launched with
+        if (err == cudaSuccess && a.numRegs < tcg::xent::kLaunchRegs) err = cudaErrorInvalidConfiguration;
+        return err;
+    });
     if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent kernel attributes", e);
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
@@ -290,11 +314,16 @@ tcg_status launch(const Params& p, const Plan& pl, cudaStream_t stream) {
     return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch("tcg_linear_xent", e);
 }
 
+template <typename T, bool kGrad>
+tcg_status launch_plan(const Params& p, const Plan& pl, cudaStream_t stream) {
+    return pl.pair ? launch<T, true, kGrad>(p, pl, stream) : launch<T, false, kGrad>(p, pl, stream);
+}
+
 // The tiles of words [first, first + cols) on X's rows.
 template <bool kGrad>
 tcg_status launch_tiles(Params& p, tcg_dtype dtype, const void* X, int ldx, const void* W, int ldw, int tokens, int hidden,
                         int first, int cols, const tcg::host::Device& dev, cudaStream_t stream) {
-    const Plan pl = make_plan(tokens, cols, dev.num_sms);
+    const Plan pl = make_plan(tokens, cols, hidden, kGrad, dev.num_sms);
     const int atoms = pl.pair ? tcg::xent::Shape<true>::kAtoms : tcg::xent::Shape<false>::kAtoms;
     p.tokens = tokens;
     p.cols = cols;
@@ -302,6 +331,7 @@ tcg_status launch_tiles(Params& p, tcg_dtype dtype, const void* X, int ldx, cons
     p.num_m = pl.num_m;
     p.num_n = pl.num_n;
     p.num_kb = static_cast<int>(blocks(2LL * hidden, tcg::xent::kRowBytes * atoms));
+    p.parts = std::min(pl.parts, p.num_kb);
     p.tile_n = pl.tile_n;
     p.raster_m = 16;
     p.fmt = dtype == TCG_F16 ? 0u : 1u;
@@ -312,9 +342,7 @@ tcg_status launch_tiles(Params& p, tcg_dtype dtype, const void* X, int ldx, cons
     if (st == TCG_OK)
         st = tcg::host::map_bytes(&p.tmW, w, 2ull * hidden, cols, 2ull * ldw, tcg::xent::kRowBytes, pl.pair ? pl.tile_n / 2 : pl.tile_n);
     if (st != TCG_OK) return st;
-    if (dtype == TCG_F16)
-        return pl.pair ? launch<__half, true, kGrad>(p, pl, stream) : launch<__half, false, kGrad>(p, pl, stream);
-    return pl.pair ? launch<__nv_bfloat16, true, kGrad>(p, pl, stream) : launch<__nv_bfloat16, false, kGrad>(p, pl, stream);
+    return dtype == TCG_F16 ? launch_plan<__half, kGrad>(p, pl, stream) : launch_plan<__nv_bfloat16, kGrad>(p, pl, stream);
 }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -383,7 +411,7 @@ tcg_status tcg_linear_xent(int tokens, int vocab, int hidden, tcg_dtype dtype, c
     if (tokens > 0 && (st = launch_tiles<false>(p, dtype, X, ldx, W, ldw, tokens, hidden, 0, vocab, dev, s)) != TCG_OK) return st;
     Finish f = {};
     f.part = p.part;
-    f.num_n = p.num_n;
+    f.num_n = 2 * p.num_n;
     f.tokens = tokens;
     f.vocab = vocab;
     f.picked = p.picked;

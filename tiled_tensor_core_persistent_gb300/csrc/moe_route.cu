@@ -8,11 +8,16 @@
 //   chosen: dx_{e_j} = w_j (g_j - sum_i g_i w_i)
 //
 // A warp holds a row, kN neighbouring experts a lane.  Logits become integers
-// that sort alike, and each round takes the warp's largest in one reduction;
-// then the lane that held it alone looks for its next.  16-bit logits share a
-// 32-bit key with the expert's number, so keys differ and "removed" is "not
-// below the last one taken"; fp32 keys need the lowest lane and place of equal
-// ones.  Statistics are fp32.
+// that sort alike; a lane sorts its own in runs of eight and leaves them in
+// shared memory, and each round takes the warp's largest head in one reduction,
+// after which the lane that had it reads its next.  16-bit logits share a
+// 32-bit key with the expert's number, so keys differ; an fp32 key is 64 bits,
+// and of equal logits the lowest lane has the lower expert.  Weights, their
+// gradients and the chosen logits are worked on k lanes a row, for as many rows
+// as fit a warp.  Statistics are fp32.
+//
+// Bound by the instructions issued, next by memory (32768 x 256 of bf16: 2.5 us
+// for the logits each way).
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -27,7 +32,9 @@ using tcg::to_float;
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxK = 32;       // a lane each
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+// CTAs an SM is to hold, forward and backward
+constexpr int resident(int n, bool grad) { return n > 8 ? 4 : grad ? 8 : 10; }
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 struct Route {
@@ -35,6 +42,7 @@ struct Route {
     long long ld;
     const uint8_t* mask;
     int tokens, experts, k;
+    int width;        // lanes of k places: a power of two
     int chosen_only;
     int* topk;
     long long ld_topk;
@@ -88,125 +96,203 @@ __device__ __forceinline__ void load_row(const Route& p, long long t, int lane, 
     }
 }
 
-// Integers that sort as the values do: -inf is 0, both zeros are one, NaN is
-// the largest.  16-bit values share the word with the expert's number turned
-// over, so that of equal ones the lower expert is the larger key.
-__device__ __forceinline__ uint32_t key_of(float v, int) {
-    if (v != v) return 0xFFFFFFFFu;
-    if (v == -INFINITY) return 0u;
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-template <uint32_t kInf>
-__device__ __forceinline__ uint32_t key16(uint32_t b, int e) {
-    if (b == (0x8000u | kInf)) return 0u;
-    if (b == 0x8000u) b = 0u;
-    const uint32_t o = (b & 0x7FFFu) > kInf ? 0xFFFFu : (b & 0x8000u ? b ^ 0xFFFFu : b | 0x8000u);
-    return (o << 16) | static_cast<uint32_t>(0xFFFF - e);
-}
-__device__ __forceinline__ uint32_t key_of(__nv_bfloat16 v, int e) { return key16<0x7F80u>(__bfloat16_as_ushort(v), e); }
-__device__ __forceinline__ uint32_t key_of(__half v, int e) { return key16<0x7C00u>(__half_as_ushort(v), e); }
-
-// The value a key stands for.
+// Integers that sort as the values do.  NaN is the largest, both zeros are one,
+// and what stands for -inf is below kFloor.  A key ends in the expert's number
+// turned over, so that of equal values the lower expert has the larger key.
 template <typename T>
-__device__ __forceinline__ float value_of(uint32_t key) {
-    if constexpr (sizeof(T) == 4) {
-        if (key == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
-        return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
-    } else {
-        const uint32_t o = key >> 16;
-        if (o == 0xFFFFu) return __uint_as_float(0x7FC00000u);
-        const uint32_t b = o & 0x8000u ? o & 0x7FFFu : o ^ 0xFFFFu;
-        if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
-        else return __uint_as_float(b << 16);
+struct Keys {   // 16-bit values
+    using Key = uint32_t;
+    static constexpr uint32_t kFloor = std::is_same<T, __half>::value ? 0x04000000u : 0x00800000u;
+
+    // two experts, the first in the word's low half
+    static __device__ __forceinline__ void make2(T lo, T hi, uint32_t turned, Key& k0, Key& k1) {
+        // (adding zero makes -0 into +0, and every NaN into the positive one)
+        uint32_t w;
+        if constexpr (std::is_same<T, __half>::value) {
+            const __half2 v = __hadd2(__halves2half2(lo, hi), __float2half2_rn(0.0f));
+            w = *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+            const __nv_bfloat162 v = __hadd2(__halves2bfloat162(lo, hi), __float2bfloat162_rn(0.0f));
+            w = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        k0 = make(w << 16, turned);
+        k1 = make(w, turned - 1u);
+    }
+    static __device__ __forceinline__ Key make(uint32_t x, uint32_t turned) {
+        const uint32_t o = x ^ (static_cast<uint32_t>(static_cast<int>(x) >> 31) | 0x80000000u);
+        return __byte_perm(o, turned, 0x3254);   // o's upper half over the number
+    }
+    static __device__ __forceinline__ uint32_t rank(Key k) { return k; }
+    static __device__ __forceinline__ float value(uint32_t rank) {
+        const uint32_t x = (rank & 0x80000000u ? rank ^ 0x80000000u : ~rank) & 0xFFFF0000u;
+        if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<unsigned short>(x >> 16)));
+        else return __uint_as_float(x);
+    }
+};
+template <>
+struct Keys<float> {
+    using Key = unsigned long long;
+    static constexpr uint32_t kFloor = 0x00800000u;
+
+    static __device__ __forceinline__ Key make(float v, uint32_t turned) {
+        const uint32_t x = __float_as_uint(v + 0.0f);
+        const uint32_t o = v != v ? 0xFFFFFFFFu : x ^ (static_cast<uint32_t>(static_cast<int>(x) >> 31) | 0x80000000u);
+        return static_cast<Key>(o) << 32 | turned;
+    }
+    static __device__ __forceinline__ void make2(float lo, float hi, uint32_t turned, Key& k0, Key& k1) {
+        k0 = make(lo, turned);
+        k1 = make(hi, turned - 1u);
+    }
+    static __device__ __forceinline__ uint32_t rank(Key k) { return static_cast<uint32_t>(k >> 32); }
+    static __device__ __forceinline__ float value(uint32_t rank) {
+        return __uint_as_float(rank & 0x80000000u ? rank ^ 0x80000000u : ~rank);
+    }
+};
+
+// Falling order, for one, two, four or eight keys (odd-even merges).
+template <int kL, typename K>
+__device__ __forceinline__ void sort_run(K (&k)[kL]) {
+    auto order = [&](int i, int j) {
+        const K a = k[i], b = k[j];
+        k[i] = max(a, b);
+        k[j] = min(a, b);
+    };
+    if constexpr (kL >= 2) {
+#pragma unroll
+        for (int i = 0; i < kL; i += 2) order(i, i + 1);
+    }
+    if constexpr (kL >= 4) {
+#pragma unroll
+        for (int i = 0; i < kL; i += 4) {
+            order(i, i + 2);
+            order(i + 1, i + 3);
+            order(i + 1, i + 2);
+        }
+    }
+    if constexpr (kL >= 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) order(i, i + 4);
+        order(2, 4);
+        order(3, 5);
+        order(1, 2);
+        order(3, 4);
+        order(5, 6);
     }
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+// Sums and maxima over neighbouring lanes, width of them (a power of two).
+__device__ __forceinline__ float lanes_sum(float v, int width = 32) {
+    for (int d = width >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+__device__ __forceinline__ float lanes_max(float v, int width = 32) {
+    for (int d = width >> 1; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
     return v;
+}
+
+// This warp's tokens: a run of neighbours.
+struct Run {
+    long long t0, t1;
+};
+__device__ __forceinline__ Run run_of(const Route& p) {
+    const long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5), n = static_cast<long long>(gridDim.x) * kWarps;
+    return {p.tokens * w / n, p.tokens * (w + 1) / n};
+}
+
+// The largest logit of a row, kN a lane (0 where all are -inf).
+template <typename T, int kN>
+__device__ __forceinline__ float row_max(const T (&x)[kN]) {
+    float m = to_float(x[0]);
+#pragma unroll
+    for (int i = 1; i < kN; ++i) m = fmaxf(m, to_float(x[i]));
+    m = lanes_max(m);
+    return m == -INFINITY ? 0.0f : m;
 }
 
 template <typename T, int kN>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const __grid_constant__ Route p) {
+__global__ void __launch_bounds__(32 * kWarps, resident(kN, false)) route_kernel(const __grid_constant__ Route p) {
     tcg::host::wait_for_kernel_ahead();
+    using K = Keys<T>;
+    using Key = typename K::Key;
+    constexpr int kL = kN < 8 ? kN : 8, kRuns = kN / kL;
+    // each run ends in a key that is below any
+    __shared__ Key sorted[kWarps][32 * kRuns * (kL + 1)];
     const int lane = threadIdx.x & 31;
-    const long long t = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (t >= p.tokens) return;
-    int* topk = p.topk + t * p.ld_topk;
-    float* weights = p.weights + t * p.ld_weights;
-    if (p.mask && !p.mask[t]) {
-        if (lane < p.k) {
-            topk[lane] = -1;
-            weights[lane] = 0.0f;
-        }
-        return;
-    }
-    alignas(16) T x[kN];
-    load_row<T, kN>(p, t, lane, x);
-    uint32_t key[kN], mine = 0u;
+    Key* mine = sorted[threadIdx.x >> 5] + lane * kRuns * (kL + 1);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        key[i] = key_of(x[i], lane * kN + i);
-        mine = max(mine, key[i]);
-    }
-    int my_e = -1;
-    uint32_t my_key = 0u, top = 0u;
-    for (int j = 0; j < p.k; ++j) {
-        const uint32_t best = __reduce_max_sync(kAll, mine);
-        if (best == 0u) break;
-        if (j == 0) top = best;
-        int e;
-        if constexpr (sizeof(T) == 2) {
-            e = 0xFFFF - static_cast<int>(best & 0xFFFFu);
-            if (mine == best) {
-                mine = 0u;
+    for (int g = 0; g < kRuns; ++g) mine[g * (kL + 1) + kL] = Key(0);
+    const int slot = lane / p.width, place = lane - slot * p.width, fit = 32 / p.width;
+    const Run tokens = run_of(p);
+    for (long long tb = tokens.t0; tb < tokens.t1; tb += fit) {
+        const int rows = static_cast<int>(min(static_cast<long long>(fit), tokens.t1 - tb));
+        // lane (slot, place): the place's choice of row tb + slot
+        Key my_key = 0;
+        float my_sum = 0.0f;
+        for (int r = 0; r < rows; ++r) {
+            const long long t = tb + r;
+            if (p.mask && !p.mask[t]) continue;
+            alignas(16) T x[kN];
+            load_row<T, kN>(p, t, lane, x);
+            Key head[kRuns];
+            const Key* next[kRuns];
 #pragma unroll
-                for (int i = 0; i < kN; ++i) mine = max(mine, key[i] < best ? key[i] : 0u);
-            }
-        } else {
-            const int holder = __ffs(__ballot_sync(kAll, mine == best)) - 1;
-            int at = 0;
-            if (lane == holder) {
-                bool found = false;
-                mine = 0u;
+            for (int g = 0; g < kRuns; ++g) {
+                Key run[kL];
+                const uint32_t turned = 0xFFFFu - static_cast<uint32_t>(lane * kN + g * kL);
+                if constexpr (kL == 1) {
+                    Key other;
+                    K::make2(x[0], x[0], turned, run[0], other);
+                } else {
 #pragma unroll
-                for (int i = 0; i < kN; ++i) {
-                    if (!found && key[i] == best) {
-                        found = true;
-                        at = i;
-                        key[i] = 0u;
-                    }
-                    mine = max(mine, key[i]);
+                    for (int i = 0; i < kL; i += 2) K::make2(x[g * kL + i], x[g * kL + i + 1], turned - i, run[i], run[i + 1]);
                 }
-                at += lane * kN;
-            }
-            e = __shfl_sync(kAll, at, holder);
-        }
-        if (lane == j) {
-            my_e = e;
-            my_key = best;
-        }
-    }
-    // (a token without experts has top = 0, and no lane a choice)
-    const float m = value_of<T>(top);
-    const float z = my_e >= 0 ? expf(value_of<T>(my_key) - m) : 0.0f;
-    float s = z;
-    if (!p.chosen_only) {
-        s = 0.0f;
+                sort_run<kL>(run);
+                // (only this lane reads them)
 #pragma unroll
-        for (int i = 0; i < kN; ++i) s += expf(to_float(x[i]) - m);
-    }
-    s = warp_sum(s);
-    if (lane < p.k) {
-        topk[lane] = my_e;
-        weights[lane] = my_e >= 0 ? z / s : 0.0f;
+                for (int i = 1; i < kL; ++i) mine[g * (kL + 1) + i] = run[i];
+                head[g] = run[0];
+                next[g] = mine + g * (kL + 1) + 1;
+            }
+            const int last = r * p.width + p.k;
+            for (int to = r * p.width; to < last; ++to) {
+                Key most = head[0];
+#pragma unroll
+                for (int g = 1; g < kRuns; ++g) most = max(most, head[g]);
+                const uint32_t best = __reduce_max_sync(kAll, K::rank(most));
+                if (best < K::kFloor) break;
+                if constexpr (sizeof(T) == 4) {
+                    // of lanes with equal logits the lowest has the lowest expert
+                    const int holder = __ffs(__ballot_sync(kAll, K::rank(most) == best)) - 1;
+                    const Key taken = __shfl_sync(kAll, most, holder);
+                    if (lane == to) my_key = taken;
+#pragma unroll
+                    for (int g = 0; g < kRuns; ++g)
+                        if (head[g] == taken) head[g] = *next[g]++;
+                } else {
+                    if (lane == to) my_key = best;
+#pragma unroll
+                    for (int g = 0; g < kRuns; ++g)
+                        if (head[g] == best) head[g] = *next[g]++;
+                }
+            }
+            if (!p.chosen_only) {
+                const float m = K::value(K::rank(__shfl_sync(kAll, my_key, r * p.width)));
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kN; ++i) s += expf(to_float(x[i]) - m);
+                s = lanes_sum(s);
+                if (slot == r) my_sum = s;
+            }
+        }
+        // (a row's first choice has its largest logit; rows without one have no choice at all)
+        const int my_e = my_key == 0 ? -1 : 0xFFFF - static_cast<int>(my_key & 0xFFFFu);
+        const float v = K::value(K::rank(my_key)), m = __shfl_sync(kAll, v, slot * p.width);
+        const float z = my_e >= 0 ? expf(v - m) : 0.0f;
+        const float s = lanes_sum(z, p.width);
+        if (slot < rows && place < p.k) {
+            p.topk[(tb + slot) * p.ld_topk + place] = my_e;
+            p.weights[(tb + slot) * p.ld_weights + place] = my_e >= 0 ? z / (p.chosen_only ? s : my_sum) : 0.0f;
+        }
     }
 }
 
@@ -240,63 +326,81 @@ __device__ __forceinline__ void store_lane(const Route& p, long long t, int lane
 }
 
 template <typename T, int kN>
-__global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const __grid_constant__ Route p) {
+__global__ void __launch_bounds__(32 * kWarps, resident(kN, true)) route_grad_kernel(const __grid_constant__ Route p) {
     tcg::host::wait_for_kernel_ahead();
+    // Per warp a row of what the chosen experts get, zeros elsewhere and between rows.
+    __shared__ alignas(16) float given[kWarps][32 * kN];
     const int lane = threadIdx.x & 31;
-    const long long t = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (t >= p.tokens) return;
-    int e = lane < p.k ? p.topk[t * p.ld_topk + lane] : -1;
-    if (e >= p.experts) e = -1;
-    float g = e >= 0 ? p.grad[t * p.ld_grad + lane] : 0.0f;
-    uint32_t live = __ballot_sync(kAll, e >= 0);
-    float d[kN];
+    float* row = given[threadIdx.x >> 5];
+    float* mine = row + lane * kN;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) d[i] = 0.0f;
-    if (live == 0u && p.accumulate) return;   // a token of nobody adds nothing, whatever its logits hold
-    if (live != 0u) {
+    for (int i = 0; i < kN; ++i) mine[i] = 0.0f;
+    __syncwarp();
+    const int slot = lane / p.width, place = lane - slot * p.width, fit = 32 / p.width;
+    const uint32_t of_slot = (p.width == 32 ? kAll : (1u << p.width) - 1u) << (slot * p.width);
+    const Run tokens = run_of(p);
+    for (long long tb = tokens.t0; tb < tokens.t1; tb += fit) {
+        const int rows = static_cast<int>(min(static_cast<long long>(fit), tokens.t1 - tb));
+        // lane (slot, place): the place's expert in row tb + slot, and what it gets
+        const long long my_t = tb + slot;
+        int e = slot < rows && place < p.k ? p.topk[my_t * p.ld_topk + place] : -1;
+        if (e >= p.experts) e = -1;
+        float g = e >= 0 ? p.grad[my_t * p.ld_grad + place] : 0.0f;
         if (p.chosen_only) {
-            const float x = e >= 0 ? to_float(static_cast<const T*>(p.logits)[t * p.ld + e]) : -INFINITY;
-            float m = warp_max(x);
+            const float x = e >= 0 ? to_float(static_cast<const T*>(p.logits)[my_t * p.ld + e]) : -INFINITY;
+            float m = lanes_max(x, p.width);
             if (m == -INFINITY) m = 0.0f;
             const float z = expf(x - m);
-            const float s = warp_sum(z);
+            const float s = lanes_sum(z, p.width);
             const float w = s == 0.0f ? 0.0f : z / s;
-            g = w * (g - warp_sum(e >= 0 ? w * g : 0.0f));
+            g = w * (g - lanes_sum(e >= 0 ? w * g : 0.0f, p.width));
         }
-        // what the lane's experts get of the chosen ones, in their order
-        while (live) {
-            const int j = __ffs(live) - 1;
-            live &= live - 1;
-            const int at = __shfl_sync(kAll, e, j) - lane * kN;
-            const float gj = __shfl_sync(kAll, g, j);
-#pragma unroll
-            for (int i = 0; i < kN; ++i) d[i] += i == at ? gj : 0.0f;
-        }
-        if (!p.chosen_only) {
-            alignas(16) T x[kN];
-            load_row<T, kN>(p, t, lane, x);
-            float m = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kN; ++i) m = fmaxf(m, to_float(x[i]));
-            m = warp_max(m);
-            if (m == -INFINITY) m = 0.0f;
-            float z[kN], s = 0.0f, inner = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                z[i] = expf(to_float(x[i]) - m);
-                s += z[i];
-                inner += z[i] * d[i];
+        const uint32_t live = __ballot_sync(kAll, e >= 0);
+        // an expert named twice gets both, in their order, through the first
+        const uint32_t same = __match_any_sync(kAll, e >= 0 ? slot << 16 | e : -1 - lane);
+        const bool first = e >= 0 && (same & ((1u << lane) - 1u)) == 0u;
+        if (__any_sync(kAll, e >= 0 && !first)) {
+            float sum = 0.0f;
+            for (int j = 0; j < 32; ++j) {
+                const float gj = __shfl_sync(kAll, g, j);
+                if (same >> j & 1u) sum += gj;
             }
-            s = warp_sum(s);
-            const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-            inner = warp_sum(inner) * inv;
+            g = sum;
+        }
+        for (int r = 0; r < rows; ++r) {
+            const bool any = (__shfl_sync(kAll, live & of_slot, r * p.width)) != 0u;
+            if (!any && p.accumulate) continue;   // a token of nobody adds nothing, whatever its logits hold
+            const bool here = first && slot == r;
+            if (here) row[e] = g;
+            __syncwarp();
+            float d[kN];
 #pragma unroll
-            for (int i = 0; i < kN; ++i) d[i] = z[i] * inv * (d[i] - inner);
+            for (int i = 0; i < kN; ++i) d[i] = mine[i];
+            __syncwarp();
+            if (here) row[e] = 0.0f;
+            __syncwarp();
+            if (any && !p.chosen_only) {
+                alignas(16) T x[kN];
+                load_row<T, kN>(p, tb + r, lane, x);
+                const float m = row_max<T, kN>(x);
+                float z[kN], s = 0.0f, inner = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    z[i] = expf(to_float(x[i]) - m);
+                    s += z[i];
+                    inner += z[i] * d[i];
+                }
+                s = lanes_sum(s);
+                const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+                inner = lanes_sum(inner) * inv;
+#pragma unroll
+                for (int i = 0; i < kN; ++i) d[i] = z[i] * inv * (d[i] - inner);
+            }
+            if (p.d_dtype == TCG_F32) store_lane<float, kN>(p, tb + r, lane, d);
+            else if (p.d_dtype == TCG_F16) store_lane<__half, kN>(p, tb + r, lane, d);
+            else store_lane<__nv_bfloat16, kN>(p, tb + r, lane, d);
         }
     }
-    if (p.d_dtype == TCG_F32) store_lane<float, kN>(p, t, lane, d);
-    else if (p.d_dtype == TCG_F16) store_lane<__half, kN>(p, t, lane, d);
-    else store_lane<__nv_bfloat16, kN>(p, t, lane, d);
 }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -342,6 +446,7 @@ tcg_status start(Route& p, int tokens, int experts, int k, tcg_dtype dtype, cons
     p.experts = experts;
     p.k = k;
     p.chosen_only = chosen_only != 0;
+    for (p.width = 1; p.width < k;) p.width *= 2;
     p.topk = const_cast<int*>(topk);
     p.ld_topk = ld_topk;
     const long long word = std::min(16, lane_experts(experts) * size_of(dtype));
@@ -350,7 +455,11 @@ tcg_status start(Route& p, int tokens, int experts, int k, tcg_dtype dtype, cons
 }
 
 tcg_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch(what, e); }
-dim3 grid_of(int tokens) { return dim3((static_cast<unsigned>(tokens) + kWarps - 1) / kWarps); }
+// A warp a token, up to what the SMs hold at once.
+dim3 grid_of(const Route& p, int sms, bool grad) {
+    const long long ctas = (static_cast<long long>(p.tokens) + kWarps - 1) / kWarps;
+    return dim3(static_cast<unsigned>(std::min<long long>(ctas, static_cast<long long>(sms) * resident(lane_experts(p.experts), grad))));
+}
 
 }  // namespace
 
@@ -370,7 +479,7 @@ tcg_status tcg_moe_route(int tokens, int experts, int k, tcg_dtype dtype, const 
     p.ld_weights = ld_weights;
     cudaError_t err = cudaSuccess;
     with_types(dtype, experts, [&](auto x, auto n) {
-        err = tcg::host::launch_early(route_kernel<decltype(x), decltype(n)::value>, grid_of(tokens), 32 * kWarps,
+        err = tcg::host::launch_early(route_kernel<decltype(x), decltype(n)::value>, grid_of(p, dev.num_sms, false), 32 * kWarps,
                                       static_cast<cudaStream_t>(stream), p);
     });
     return launched(err, "tcg_moe_route");
@@ -395,7 +504,7 @@ tcg_status tcg_moe_route_backward(int tokens, int experts, int k, tcg_dtype dtyp
     p.d_dtype = d_dtype;
     cudaError_t err = cudaSuccess;
     with_types(dtype, experts, [&](auto x, auto n) {
-        err = tcg::host::launch_early(route_grad_kernel<decltype(x), decltype(n)::value>, grid_of(tokens), 32 * kWarps,
+        err = tcg::host::launch_early(route_grad_kernel<decltype(x), decltype(n)::value>, grid_of(p, dev.num_sms, true), 32 * kWarps,
                                       static_cast<cudaStream_t>(stream), p);
     });
     return launched(err, "tcg_moe_route_backward");

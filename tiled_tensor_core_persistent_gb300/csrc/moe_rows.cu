@@ -36,12 +36,16 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortRun = 2048;
 // As many as this are one CTA's, in one launch.
 constexpr int kSortAlone = 4096;
+// Assignments whose loads a thread has on their way at once.
+constexpr int kSortBatch = 4;
 
 struct Sort {
     const int* topk;
     long long ld_topk;
     const uint8_t* mask;
     int total, k, experts;       // total: tokens * k
+    uint32_t div_mul;            // a / k = (a + high half of a * div_mul) >> div_shift for 0 <= a < 2^31
+    int div_shift;
     int* offsets;
     int* row_token;
     int* row_of;
@@ -53,13 +57,25 @@ __device__ __forceinline__ int run_start(int total, int part, int parts) {
     return static_cast<int>(static_cast<long long>(total) * part / parts);
 }
 
-// The expert of assignment a, -1 where it has none.
-__device__ __forceinline__ int expert_of(const Sort& p, int a, int& t, int& j) {
-    t = static_cast<int>(static_cast<unsigned>(a) / static_cast<unsigned>(p.k));
-    j = a - t * p.k;
-    if (p.mask && !__ldcg(p.mask + t)) return -1;
-    const int e = __ldcg(p.topk + t * p.ld_topk + j);
-    return e >= 0 && e < p.experts ? e : -1;
+struct Assignment {
+    int t, j, e;   // e: -1 where it has no expert
+};
+// Assignments a, a + step, ...: those below end (the others have no expert).
+// Both loads of all of them are on their way before one is used.
+template <int kStep>
+__device__ __forceinline__ void load_batch(const Sort& p, int a, int end, Assignment (&v)[kSortBatch]) {
+    uint8_t counts[kSortBatch];
+#pragma unroll
+    for (int i = 0; i < kSortBatch; ++i) {
+        const int at = min(a + i * kStep, p.total - 1);
+        v[i].t = static_cast<int>((static_cast<uint32_t>(at) + __umulhi(static_cast<uint32_t>(at), p.div_mul)) >> p.div_shift);
+        v[i].j = at - v[i].t * p.k;
+        counts[i] = p.mask ? __ldcg(p.mask + v[i].t) : 1;
+        v[i].e = __ldcg(p.topk + v[i].t * p.ld_topk + v[i].j);
+    }
+#pragma unroll
+    for (int i = 0; i < kSortBatch; ++i)
+        if (!counts[i] || v[i].e < 0 || v[i].e >= p.experts || a + i * kStep >= end) v[i].e = -1;
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_constant__ Sort p) {
@@ -70,10 +86,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_c
     for (int e = threadIdx.x; e < p.experts; e += kSortThreads) hist[e] = 0;
     __syncthreads();
     const int a1 = run_start(p.total, blockIdx.x + 1, gridDim.x);
-    for (int a = run_start(p.total, blockIdx.x, gridDim.x) + static_cast<int>(threadIdx.x); a < a1; a += kSortThreads) {
-        int t, j;
-        const int e = expert_of(p, a, t, j);
-        if (e >= 0) atomicAdd(&hist[e], 1);
+    for (int a = run_start(p.total, blockIdx.x, gridDim.x) + static_cast<int>(threadIdx.x); a < a1; a += kSortBatch * kSortThreads) {
+        Assignment v[kSortBatch];
+        load_batch<kSortThreads>(p, a, a1, v);
+#pragma unroll
+        for (int i = 0; i < kSortBatch; ++i)
+            if (v[i].e >= 0) atomicAdd(&hist[v[i].e], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < p.experts; e += kSortThreads) p.counts[static_cast<size_t>(blockIdx.x) * p.experts + e] = hist[e];
@@ -93,10 +111,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
     const int c0 = run_start(p.total, blockIdx.x, gridDim.x), c1 = run_start(p.total, blockIdx.x + 1, gridDim.x);
     const int a0 = c0 + run_start(c1 - c0, warp, kSortWarps), a1 = c0 + run_start(c1 - c0, warp + 1, kSortWarps);
     int* mine = place + warp * p.experts;
-    for (int a = a0 + lane; a < a1; a += 32) {
-        int t, j;
-        const int e = expert_of(p, a, t, j);
-        if (e >= 0) atomicAdd(&mine[e], 1);
+    for (int a = a0 + lane; a < a1; a += kSortBatch * 32) {
+        Assignment v[kSortBatch];
+        load_batch<32>(p, a, a1, v);
+#pragma unroll
+        for (int i = 0; i < kSortBatch; ++i)
+            if (v[i].e >= 0) atomicAdd(&mine[v[i].e], 1);
     }
     if (!alone) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -106,7 +126,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
         if (part < parts) {
             for (int e = threadIdx.x - part * per; e < p.experts; e += per) {
                 int all = 0, ahead = 0;
-#pragma unroll 8
+#pragma unroll 16
                 for (int b = part; b < static_cast<int>(gridDim.x); b += parts) {
                     const int n = p.counts[static_cast<size_t>(b) * p.experts + e];
                     all += n;
@@ -160,18 +180,21 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
     }
     if (p.offsets && blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.experts] = rows;
     __syncthreads();
-    for (int b = a0; b < a1; b += 32) {
-        const int a = b + lane;
-        int t = 0, j = 0;
-        const int e = a < a1 ? expert_of(p, a, t, j) : -1;
-        const uint32_t same = __match_any_sync(kAll, e);
-        int row = -1;
-        if (e >= 0) row = mine[e] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (e >= 0 && (same >> lane) == 1u) mine[e] = row + 1;   // the last of its equals
-        __syncwarp();
-        if (row >= 0) p.row_token[row] = t;
-        if (a < a1) p.row_of[t * p.ld_row_of + j] = row;
+    for (int b = a0; b < a1; b += kSortBatch * 32) {
+        Assignment v[kSortBatch];
+        load_batch<32>(p, b + lane, a1, v);
+#pragma unroll
+        for (int i = 0; i < kSortBatch; ++i) {
+            const int e = v[i].e;
+            const uint32_t same = __match_any_sync(kAll, e);
+            int row = -1;
+            if (e >= 0) row = mine[e] + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (e >= 0 && (same >> lane) == 1u) mine[e] = row + 1;   // the last of its equals
+            __syncwarp();
+            if (row >= 0) p.row_token[row] = v[i].t;
+            if (b + i * 32 + lane < a1) p.row_of[v[i].t * p.ld_row_of + v[i].j] = row;
+        }
     }
     for (int r = rows + static_cast<int>(blockIdx.x * kSortThreads + threadIdx.x); r < p.total; r += static_cast<int>(gridDim.x) * kSortThreads)
         p.row_token[r] = -1;
@@ -465,6 +488,8 @@ tcg_status tcg_moe_sort(int tokens, int experts, int k, const int* topk, int ld_
     p.total = tokens * k;
     p.k = k;
     p.experts = experts;
+    while ((1ll << p.div_shift) < k) ++p.div_shift;
+    p.div_mul = static_cast<uint32_t>((((1ull << p.div_shift) - k) << 32) / k + 1);
     p.offsets = offsets;
     p.row_token = row_token;
     p.row_of = row_of;

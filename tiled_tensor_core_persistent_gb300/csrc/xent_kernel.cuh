@@ -12,12 +12,19 @@
 // Tiles of 256 rows (a pair of CTAs; 128, one CTA, where there are no more rows
 // than that) and up to 256 columns; the width is the one whose waves fit
 // (the launcher's rule).  Roles: warp 0 TMA producer, warp 1 MMA issuer and TMEM
-// owner, warps 2-5 read the accumulator, a row a thread, one of two so that a
-// tile's exponentials run beside the next tile's products.  A tile of 128 rows
-// of a CTA is 8 H cycles of the tensor cores (H = hidden) and 2048 of its
-// exponentials, so H >= 512 hides them.  All waits are bounded; on expiry the
-// status word gets TCG_ERR_TIMEOUT, the roles drain their copies and MMAs, free
-// the TMEM and return.
+// owner, warps 2 and 3 idle (they fill the control warps' group of four, which
+// give up registers together), warps 4-11 take the accumulators into registers, half of a row a thread,
+// and work on them while the next products go to the other accumulator.  A tile
+// of 128 rows of a CTA and 256 columns is 8 H cycles of the tensor cores (H =
+// hidden) and 2048 of its exponentials, so H >= 512 hides them.
+//
+// The tensor cores' fp32 sums are cut, not rounded, after every 16 k, so a long
+// sum is a little too near zero: with H = 4096 lse came out 1.2e-6 of itself
+// off, 30 times what fp32 arithmetic gives.  The statistics' sums are therefore
+// taken in parts of K that are added, rounded, in the registers.
+//
+// All waits are bounded; on expiry the status word gets TCG_ERR_TIMEOUT, the
+// roles drain their copies and MMAs, free the TMEM and return.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -33,22 +40,31 @@ namespace tcg {
 namespace xent {
 
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr int kThreads = 192;
+constexpr int kControlWarps = 4, kRowWarps = 8;
+constexpr int kThreads = 32 * (kControlWarps + kRowWarps);
+// Registers a thread: at the launch, and once they are handed over.
+constexpr int kLaunchRegs = 168, kControlRegs = 56, kRowRegs = 224;
+static_assert(kControlWarps * kControlRegs + kRowWarps * kRowRegs <= (kControlWarps + kRowWarps) * kLaunchRegs,
+              "the shares add up to the launch's registers");
 constexpr int kRowBytes = 128;          // one K atom: a 128-byte swizzle row, 64 elements
 constexpr int kBM = 128;                // rows of a CTA's tile = TMEM lanes
 constexpr int kMaxN = 256;
-constexpr int kAccCols = 256;           // columns between the two accumulators
+constexpr int kTmemCols = 512;
+constexpr int kAccs = 2, kAccCols = kTmemCols / kAccs;
+constexpr int kHalf = kMaxN / 2;        // columns a thread has room for
+constexpr int kChunk = 16;
 
 struct Params {
     CUtensorMap tmX, tmW;               // as bytes
     int tokens, cols;                   // rows of X, and of W in this launch
     int num_m, num_n, num_kb;           // tiles; pipeline stages of K
+    int parts;                          // accumulations that share a tile's K
     int tile_n, raster_m;
     uint32_t fmt;                       // operand format of the instruction descriptor: 0 fp16, 1 bf16
     const int* target;                  // [tokens]
     int first;                          // the word of W's first row
     // forward
-    float2* part;                       // [column tile][tokens]: (M, s)
+    float2* part;                       // [half column tile][tokens]: (M, s)
     float* picked;                      // [tokens]: z of the target
     // backward
     const float* lse;                   // [tokens]
@@ -74,15 +90,16 @@ struct Shape {
 
 struct alignas(16) Ctl {
     uint64_t full[4], empty[4];
-    uint64_t tmem_full[2], tmem_empty[2];
+    uint64_t tmem_full[kAccs], tmem_empty[kAccs];
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
 };
 static_assert(sizeof(Ctl) <= 512, "the barriers fit");
 
-static __device__ __noinline__ bool spin(uint64_t* bar, uint32_t parity, int* status, long long limit_ns, Ctl* ctl, int where,
-                                         bool honor_abort) {
+// (inlined: a call's registers do not fit between the two shares)
+__device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, int* status, long long limit_ns, Ctl* ctl, int where,
+                                     bool honor_abort) {
     const uint32_t a = ptx::smem_u32(bar);
     const uint64_t t0 = ptx::globaltimer_ns();
     for (uint32_t n = 1;; ++n) {
@@ -116,48 +133,31 @@ __host__ __device__ __forceinline__ void tile_of(const Params& p, int tile, int&
     n = local / size;
 }
 
-// 32 columns of a warp's 32 TMEM lanes; the values are there after landed().
-__device__ __forceinline__ void fetch32(uint32_t taddr, uint32_t (&r)[32]) {
+// 16 columns of a warp's 32 TMEM lanes; the values are there after landed().
+__device__ __forceinline__ void fetch(uint32_t taddr, float (&r)[kChunk]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void landed(uint32_t (&r)[32]) {
+__device__ __forceinline__ void landed(float (&r)[kChunk]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]),
+                   "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
                  :
                  : "memory");
 }
 
-// One row's running maximum (times log2 e) and sum.
-struct RowStats {
-    float m = -INFINITY, m2 = -INFINITY, s = 0.0f;
-
-    __device__ __forceinline__ void add(const float (&z)[32]) {
-        float c = z[0];
-#pragma unroll
-        for (int i = 1; i < 32; ++i) c = fmaxf(c, z[i]);
-        if (c > m) {
-            const float next = c * kLog2e;
-            s = m == -INFINITY ? s : s * ptx::ex2_approx(m2 - next);   // (s holds NaN, if any, from here on)
-            m = c;
-            m2 = next;
-        }
-        const float base = m == -INFINITY ? 0.0f : m2;
-        float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < 32; ++i) q[i & 3] += ptx::ex2_approx(fmaf(z[i], kLog2e, -base));
-        s += (q[0] + q[1]) + (q[2] + q[3]);
+// The two accumulators in turn, and how often both were walked.
+struct Ring {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        phase ^= static_cast<uint32_t>(at);
+        at ^= 1;
     }
 };
 
@@ -175,16 +175,15 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
     const int worker = kPair ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
     const int workers = kPair ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
     const int tiles = p.num_m * p.num_n;
-    constexpr uint32_t kTmemCols = 512;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             ptx::mbar_init(&ctl->full[s], 1);
             ptx::mbar_init(&ctl->empty[s], 1);
         }
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < kAccs; ++a) {
             ptx::mbar_init(&ctl->tmem_full[a], 1);
-            ptx::mbar_init(&ctl->tmem_empty[a], kPair ? 8 : 4);
+            ptx::mbar_init(&ctl->tmem_empty[a], kPair ? 16 : 8);
         }
         ptx::mbar_init(&ctl->drain, 1);
         ctl->abort_flag = 0;
@@ -206,7 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
     const uint32_t tmem_base = ctl->tmem_base;
     tcg::host::wait_for_kernel_ahead();
 
-    if (warp == 0) {
+    if (warp < kControlWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+        if (warp == 0) {
         // ------------------------------------------------------ TMA producer
         const bool issuer = lane == 0;
         const int b_rows = kPair ? p.tile_n / 2 : p.tile_n;
@@ -262,21 +263,23 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             if (leader) wait(&ctl->full[s], par, p, ctl, 11, false);
             else wait(&ctl->empty[s], par, p, ctl, 13, false);
         }
-    } else if (warp == 1) {
+        } else if (warp == 1 && leader) {
         // ------------------------------------------------------- MMA issuer
-        if (leader) {
             const bool issuer = lane == 0;
             const uint32_t idesc = (1u << 4) | (p.fmt << 7) | (p.fmt << 10) | (static_cast<uint32_t>(p.tile_n >> 3) << 17) |
                                    (static_cast<uint32_t>(S::kTileM >> 4) << 24);
-            int stage = 0, t = 0;
+            const int mine = (tiles - worker + workers - 1) / workers * p.parts;   // accumulations
+            int stage = 0, part = 0;
             uint32_t phase = 0;
+            Ring acc;
             bool ok = true, issued = false;
-            for (int tile = worker; ok && tile < tiles; tile += workers, ++t) {
-                const int acc = t & 1;
-                if (!wait(&ctl->tmem_empty[acc], ((t >> 1) & 1) ^ 1u, p, ctl, 2)) break;
+            for (int u = 0; ok && u < mine; ++u) {
+                const int kb0 = p.num_kb * part / p.parts, kb1 = p.num_kb * (part + 1) / p.parts;
+                if (++part == p.parts) part = 0;
+                if (!wait(&ctl->tmem_empty[acc.at], acc.phase ^ 1u, p, ctl, 2)) break;
                 ptx::tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * kAccCols);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc.at * kAccCols);
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait(&ctl->full[stage], phase, p, ctl, 3)) { ok = false; break; }
                     ptx::tc_fence_after_sync();
                     if (issuer) {
@@ -288,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                             // four MMAs of 32 bytes of K an atom; descriptors count 16-byte units
                             const uint64_t ad = a_desc + static_cast<uint64_t>(((k / 4) * kBM * kRowBytes + (k % 4) * 32) >> 4);
                             const uint64_t bd = b_desc + static_cast<uint64_t>(((k / 4) * S::kBRows * kRowBytes + (k % 4) * 32) >> 4);
-                            const uint32_t accum = (kb > 0 || k > 0) ? 1u : 0u;
+                            const uint32_t accum = (kb > kb0 || k > 0) ? 1u : 0u;
                             if constexpr (kPair) ptx::mma_f16_pair(d_tmem, ad, bd, idesc, accum);
                             else ptx::mma_f16(d_tmem, ad, bd, idesc, accum);
                         }
@@ -300,10 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                     if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
                 }
                 if (ok && issuer) {
-                    if constexpr (kPair) ptx::mma_commit_pair(&ctl->tmem_full[acc], 0x3);
-                    else ptx::mma_commit(&ctl->tmem_full[acc]);
+                    if constexpr (kPair) ptx::mma_commit_pair(&ctl->tmem_full[acc.at], 0x3);
+                    else ptx::mma_commit(&ctl->tmem_full[acc.at]);
                 }
                 __syncwarp();
+                acc.next();
             }
             // Every MMA is done before the TMEM is freed.
             if (issued) {
@@ -317,18 +321,22 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
         }
     } else {
         // ------------------------------------- statistics, or the gradient
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
         const int g = warp & 3;                 // the TMEM lanes this warp may read
-        int t = 0;
-        for (int tile = worker; tile < tiles; tile += workers, ++t) {
+        const int half = (warp - kControlWarps) >> 2, hw = p.tile_n / 2;   // the columns [half * hw, half * hw + hw) of a tile
+        Ring acc;
+        bool ok = true;
+        for (int tile = worker; ok && tile < tiles; tile += workers) {
             int m, n;
             tile_of(p, tile, m, n);
             const int row = m * S::kTileM + static_cast<int>(rank) * kBM + g * 32 + lane;
             const bool live = row < p.tokens;
-            const int n0 = n * p.tile_n, width = min(p.tile_n, p.cols - n0);
+            const int n0 = n * p.tile_n + half * hw, width = max(0, min(hw, p.cols - n0));
             const int y = live ? p.target[row] : -1;
-            // the target's place in this tile, negative or past it where it is elsewhere
+            // the target's place in these columns, -1 where it is elsewhere
             const long long at_tile = static_cast<long long>(y) - p.first - n0;
             const int at = y >= 0 && at_tile >= 0 && at_tile < width ? static_cast<int>(at_tile) : -1;
+            const bool any = __any_sync(0xffffffffu, at >= 0);
             float scale = 0.0f, lse2 = 0.0f;
             if constexpr (kGrad) {
                 if (live) {
@@ -336,78 +344,94 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                     lse2 = p.lse[row] * kLog2e;
                 }
             }
-            const int acc = t & 1;
-            if (!wait(&ctl->tmem_full[acc], (t >> 1) & 1, p, ctl, 4)) break;
-            ptx::tc_fence_after_sync();
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(g * 32) << 16) + static_cast<uint32_t>(acc * kAccCols);
-            const int chunks = (width + 31) / 32;
-            RowStats stats;
-            uint32_t r[2][32];
-            auto use = [&](uint32_t (&raw)[32], int c) {
-                float z[32];
+            float z[kHalf / kChunk][kChunk];
+            for (int part = 0; part < p.parts; ++part) {
+                ok = wait(&ctl->tmem_full[acc.at], acc.phase, p, ctl, 4);
+                if (!ok) break;
+                ptx::tc_fence_after_sync();
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(g * 32) << 16) + static_cast<uint32_t>(acc.at * kAccCols + half * hw);
+                if (part == 0) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(raw[i]);
-                const int here = at - 32 * c;
-                const bool any = __any_sync(0xffffffffu, static_cast<unsigned>(here) < 32u);
-                if constexpr (kGrad) {
+                    for (int c = 0; c < kHalf / kChunk; ++c)
+                        if (c * kChunk < hw) fetch(taddr + static_cast<uint32_t>(c * kChunk), z[c]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] = ptx::ex2_approx(fmaf(z[i], kLog2e, -lse2));
-                    if (any) {
+                    for (int c = 0; c < kHalf / kChunk; ++c) landed(z[c]);
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) z[i] -= i == here ? 1.0f : 0.0f;
-                    }
-                    // (a token that does not count has gradient 0, whatever its logits are)
+                    for (int c = 0; c < kHalf / kChunk; c += 2) {
+                        if (c * kChunk >= hw) continue;
+                        float more[2][kChunk];
+                        fetch(taddr + static_cast<uint32_t>(c * kChunk), more[0]);
+                        if ((c + 1) * kChunk < hw) fetch(taddr + static_cast<uint32_t>((c + 1) * kChunk), more[1]);
+                        landed(more[0]);
+                        landed(more[1]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] = scale == 0.0f ? 0.0f : scale * z[i];
-                    if (live) {
-                        T* dst = static_cast<T*>(p.d) + row * p.ldd + n0 + 32 * c;
-                        uint32_t w[8];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) w[i] = pack_pair<T>(z[16 * h + 2 * i], z[16 * h + 2 * i + 1]);
-                            ptx::st_global_v8(dst + 16 * h, w);
+                        for (int i = 0; i < kChunk; ++i) {
+                            z[c][i] += more[0][i];
+                            z[c + 1][i] += more[1][i];
                         }
                     }
-                } else {
-                    if (any) {
-                        float picked = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) picked = i == here ? z[i] : picked;
-                        if (static_cast<unsigned>(here) < 32u) p.picked[row] = picked;
-                    }
-                    if (32 * c + 32 > width) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) z[i] = 32 * c + i < width ? z[i] : -INFINITY;
-                    }
-                    stats.add(z);
                 }
-            };
-            // The next 32 columns are on their way while these are used; once the
-            // last have left the TMEM the accumulator goes back.
-            auto hand_back = [&] {
+                // the accumulator goes back as soon as it is in registers
                 ptx::tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    if (kPair && !leader) ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(&ctl->tmem_empty[acc]), 0));
-                    else ptx::mbar_arrive(&ctl->tmem_empty[acc]);
+                    uint64_t* bar = &ctl->tmem_empty[acc.at];
+                    if (kPair && !leader) ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(bar), 0));
+                    else ptx::mbar_arrive(bar);
                 }
-            };
-            fetch32(taddr, r[0]);
-            for (int c = 0; c < chunks; c += 2) {
-                landed(r[0]);
-                if (c + 1 < chunks) fetch32(taddr + static_cast<uint32_t>(32 * c + 32), r[1]);
-                else hand_back();
-                use(r[0], c);
-                if (c + 1 < chunks) {
-                    landed(r[1]);
-                    if (c + 2 < chunks) fetch32(taddr + static_cast<uint32_t>(32 * c + 64), r[0]);
-                    else hand_back();
-                    use(r[1], c + 1);
-                }
+                acc.next();
             }
-            if constexpr (!kGrad) {
-                if (live) p.part[static_cast<size_t>(n) * p.tokens + row] = make_float2(stats.m2, stats.s);
+            if (!ok) break;
+            if constexpr (kGrad) {
+                T* dst = static_cast<T*>(p.d) + row * p.ldd + n0;
+#pragma unroll
+                for (int c = 0; c < kHalf / kChunk; ++c) {
+                    if (c * kChunk >= width) continue;
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) z[c][i] = ptx::ex2_approx(fmaf(z[c][i], kLog2e, -lse2));
+                    if (any) {
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) z[c][i] -= c * kChunk + i == at ? 1.0f : 0.0f;
+                    }
+                    uint32_t w[8];
+                    // (a token that does not count has gradient 0, whatever its logits are)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        w[i] = scale == 0.0f ? 0u : pack_pair<T>(scale * z[c][2 * i], scale * z[c][2 * i + 1]);
+                    if (live) ptx::st_global_v8(dst + c * kChunk, w);
+                }
+            } else {
+                if (width < hw) {
+#pragma unroll
+                    for (int c = 0; c < kHalf / kChunk; ++c)
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) z[c][i] = c * kChunk + i < width ? z[c][i] : -INFINITY;
+                }
+                if (any) {
+                    float picked = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < kHalf / kChunk; ++c)
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) picked = c * kChunk + i == at ? z[c][i] : picked;
+                    if (at >= 0) p.picked[row] = picked;
+                }
+                float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < kHalf / kChunk; ++c) {
+                    if (c * kChunk >= hw) continue;
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) most[i & 3] = fmaxf(most[i & 3], z[c][i]);
+                }
+                const float m2 = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * kLog2e;
+                const float base = m2 == -INFINITY ? 0.0f : m2;   // (nothing but -inf, or no column: s = 0)
+#pragma unroll
+                for (int c = 0; c < kHalf / kChunk; ++c) {
+                    if (c * kChunk >= hw) continue;
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) sum[i & 3] += ptx::ex2_approx(fmaf(z[c][i], kLog2e, -base));
+                }
+                if (live) p.part[static_cast<size_t>(2 * n + half) * p.tokens + row] = make_float2(m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
             }
         }
     }
