@@ -58,42 +58,60 @@ struct Route {
     tcg_dtype d_dtype;
 };
 
-// kN values of a lane from an address aligned to their size, at most 16 bytes.
+// A lane's kN experts of a row: fp32 values, or words of two 16-bit ones.
 template <typename T, int kN>
-__device__ __forceinline__ void load_lane(const T* src, T (&x)[kN]) {
-    constexpr int kBytes = kN * static_cast<int>(sizeof(T));
-    if constexpr (kBytes >= 16) {
-#pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4*>(x)[i] = *(reinterpret_cast<const uint4*>(src) + i);
-    } else if constexpr (kBytes == 8) {
-        *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(src);
-    } else if constexpr (kBytes == 4) {
-        *reinterpret_cast<uint32_t*>(x) = *reinterpret_cast<const uint32_t*>(src);
-    } else {
-        x[0] = src[0];
+struct Row {
+    static constexpr int kBytes = kN * static_cast<int>(sizeof(T)), kWords = (kBytes + 3) / 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ float value(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else if constexpr (std::is_same<T, __half>::value)
+            return __half2float(__ushort_as_half(static_cast<unsigned short>(w[i / 2] >> (16 * (i & 1)))));
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
     }
-}
 
-template <typename T>
-__device__ __forceinline__ T lowest();
-template <>
-__device__ __forceinline__ float lowest<float>() { return __uint_as_float(0xFF800000u); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 lowest<__nv_bfloat16>() { return __ushort_as_bfloat16(0xFF80u); }
-template <>
-__device__ __forceinline__ __half lowest<__half>() { return __ushort_as_half(0xFC00u); }
+    // From an address aligned to kBytes, at most 16.
+    __device__ __forceinline__ void load(const T* src) {
+        if constexpr (kBytes >= 16) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 16; ++i) {
+                const uint4 q = reinterpret_cast<const uint4*>(src)[i];
+                w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+            }
+        } else if constexpr (kBytes == 8) {
+            const uint2 q = *reinterpret_cast<const uint2*>(src);
+            w[0] = q.x, w[1] = q.y;
+        } else if constexpr (kBytes == 4) {
+            w[0] = *reinterpret_cast<const uint32_t*>(src);
+        } else {
+            w[0] = *reinterpret_cast<const uint16_t*>(src);
+        }
+    }
 
-// A lane's kN experts of row t, -inf past the last expert.
+    // The first n of them, -inf for the others.
+    __device__ __forceinline__ void load_some(const T* src, int n) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) w[i] = i < n ? __float_as_uint(src[i]) : 0xFF800000u;
+        } else {
+            constexpr uint32_t kLow = std::is_same<T, __half>::value ? 0xFC00u : 0xFF80u;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const uint32_t lo = 2 * i < n ? reinterpret_cast<const uint16_t*>(src)[2 * i] : kLow;
+                const uint32_t hi = 2 * i + 1 < n ? reinterpret_cast<const uint16_t*>(src)[2 * i + 1] : kLow;
+                w[i] = lo | hi << 16;
+            }
+        }
+    }
+};
+
 template <typename T, int kN>
-__device__ __forceinline__ void load_row(const Route& p, long long t, int lane, T (&x)[kN]) {
-    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-    const int e0 = lane * kN;
-    if (p.vec && e0 + kN <= p.experts) {
-        load_lane<T, kN>(row + e0, x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] = e0 + i < p.experts ? row[e0 + i] : lowest<T>();
-    }
+__device__ __forceinline__ void load_row(const Route& p, long long t, int lane, Row<T, kN>& x) {
+    const T* src = static_cast<const T*>(p.logits) + t * p.ld + lane * kN;
+    const int left = p.experts - lane * kN;
+    if (p.vec && left >= kN) x.load(src);
+    else x.load_some(src, left);
 }
 
 // Integers that sort as the values do.  NaN is the largest, both zeros are one,
@@ -104,15 +122,16 @@ struct Keys {   // 16-bit values
     using Key = uint32_t;
     static constexpr uint32_t kFloor = std::is_same<T, __half>::value ? 0x04000000u : 0x00800000u;
 
-    // two experts, the first in the word's low half
-    static __device__ __forceinline__ void make2(T lo, T hi, uint32_t turned, Key& k0, Key& k1) {
+    // Experts i and i + 1 of a row, `turned` the first one's number turned over.
+    template <int kN>
+    static __device__ __forceinline__ void make2(const Row<T, kN>& x, int i, uint32_t turned, Key& k0, Key& k1) {
         // (adding zero makes -0 into +0, and every NaN into the positive one)
-        uint32_t w;
+        uint32_t w = x.w[i / 2];
         if constexpr (std::is_same<T, __half>::value) {
-            const __half2 v = __hadd2(__halves2half2(lo, hi), __float2half2_rn(0.0f));
+            const __half2 v = __hadd2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(0.0f));
             w = *reinterpret_cast<const uint32_t*>(&v);
         } else {
-            const __nv_bfloat162 v = __hadd2(__halves2bfloat162(lo, hi), __float2bfloat162_rn(0.0f));
+            const __nv_bfloat162 v = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(0.0f));
             w = *reinterpret_cast<const uint32_t*>(&v);
         }
         k0 = make(w << 16, turned);
@@ -123,6 +142,19 @@ struct Keys {   // 16-bit values
         return __byte_perm(o, turned, 0x3254);   // o's upper half over the number
     }
     static __device__ __forceinline__ uint32_t rank(Key k) { return k; }
+    // Where the head was taken, the run's next key takes its place (no branch:
+    // one lane of 32 does it).  Nothing below the floor is ever taken.
+    static __device__ __forceinline__ void advance(Key& head, uint32_t& next, Key taken) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.eq.u32 p, %0, %2;\n\t"
+            "setp.ge.and.u32 p, %2, %3, p;\n\t"
+            "@p ld.shared.u32 %0, [%1];\n\t"
+            "@p add.u32 %1, %1, 4;\n\t}"
+            : "+r"(head), "+r"(next)
+            : "r"(taken), "n"(kFloor)
+            : "memory");
+    }
     static __device__ __forceinline__ float value(uint32_t rank) {
         const uint32_t x = (rank & 0x80000000u ? rank ^ 0x80000000u : ~rank) & 0xFFFF0000u;
         if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<unsigned short>(x >> 16)));
@@ -139,11 +171,23 @@ struct Keys<float> {
         const uint32_t o = v != v ? 0xFFFFFFFFu : x ^ (static_cast<uint32_t>(static_cast<int>(x) >> 31) | 0x80000000u);
         return static_cast<Key>(o) << 32 | turned;
     }
-    static __device__ __forceinline__ void make2(float lo, float hi, uint32_t turned, Key& k0, Key& k1) {
-        k0 = make(lo, turned);
-        k1 = make(hi, turned - 1u);
+    template <int kN>
+    static __device__ __forceinline__ void make2(const Row<float, kN>& x, int i, uint32_t turned, Key& k0, Key& k1) {
+        k0 = make(x.value(i), turned);
+        k1 = make(x.value(i + 1 < kN ? i + 1 : i), turned - 1u);
     }
     static __device__ __forceinline__ uint32_t rank(Key k) { return static_cast<uint32_t>(k >> 32); }
+    static __device__ __forceinline__ void advance(Key& head, uint32_t& next, Key taken) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.eq.u64 p, %0, %2;\n\t"
+            "setp.ge.and.u32 p, %3, %4, p;\n\t"
+            "@p ld.shared.u64 %0, [%1];\n\t"
+            "@p add.u32 %1, %1, 8;\n\t}"
+            : "+l"(head), "+r"(next)
+            : "l"(taken), "r"(rank(taken)), "n"(kFloor)
+            : "memory");
+    }
     static __device__ __forceinline__ float value(uint32_t rank) {
         return __uint_as_float(rank & 0x80000000u ? rank ^ 0x80000000u : ~rank);
     }
@@ -201,10 +245,10 @@ __device__ __forceinline__ Run run_of(const Route& p) {
 
 // The largest logit of a row, kN a lane (0 where all are -inf).
 template <typename T, int kN>
-__device__ __forceinline__ float row_max(const T (&x)[kN]) {
-    float m = to_float(x[0]);
+__device__ __forceinline__ float row_max(const Row<T, kN>& x) {
+    float m = x.value(0);
 #pragma unroll
-    for (int i = 1; i < kN; ++i) m = fmaxf(m, to_float(x[i]));
+    for (int i = 1; i < kN; ++i) m = fmaxf(m, x.value(i));
     m = lanes_max(m);
     return m == -INFINITY ? 0.0f : m;
 }
@@ -219,6 +263,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(kN, false)) route_kernel
     __shared__ Key sorted[kWarps][32 * kRuns * (kL + 1)];
     const int lane = threadIdx.x & 31;
     Key* mine = sorted[threadIdx.x >> 5] + lane * kRuns * (kL + 1);
+    const uint32_t mine_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
 #pragma unroll
     for (int g = 0; g < kRuns; ++g) mine[g * (kL + 1) + kL] = Key(0);
     const int slot = lane / p.width, place = lane - slot * p.width, fit = 32 / p.width;
@@ -231,27 +276,27 @@ __global__ void __launch_bounds__(32 * kWarps, resident(kN, false)) route_kernel
         for (int r = 0; r < rows; ++r) {
             const long long t = tb + r;
             if (p.mask && !p.mask[t]) continue;
-            alignas(16) T x[kN];
+            Row<T, kN> x;
             load_row<T, kN>(p, t, lane, x);
             Key head[kRuns];
-            const Key* next[kRuns];
+            uint32_t next[kRuns];   // shared addresses
 #pragma unroll
             for (int g = 0; g < kRuns; ++g) {
                 Key run[kL];
                 const uint32_t turned = 0xFFFFu - static_cast<uint32_t>(lane * kN + g * kL);
                 if constexpr (kL == 1) {
                     Key other;
-                    K::make2(x[0], x[0], turned, run[0], other);
+                    K::make2(x, 0, turned, run[0], other);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < kL; i += 2) K::make2(x[g * kL + i], x[g * kL + i + 1], turned - i, run[i], run[i + 1]);
+                    for (int i = 0; i < kL; i += 2) K::make2(x, g * kL + i, turned - i, run[i], run[i + 1]);
                 }
                 sort_run<kL>(run);
                 // (only this lane reads them)
 #pragma unroll
                 for (int i = 1; i < kL; ++i) mine[g * (kL + 1) + i] = run[i];
                 head[g] = run[0];
-                next[g] = mine + g * (kL + 1) + 1;
+                next[g] = mine_at + (g * (kL + 1) + 1) * static_cast<uint32_t>(sizeof(Key));
             }
             const int last = r * p.width + p.k;
             for (int to = r * p.width; to < last; ++to) {
@@ -259,33 +304,28 @@ __global__ void __launch_bounds__(32 * kWarps, resident(kN, false)) route_kernel
 #pragma unroll
                 for (int g = 1; g < kRuns; ++g) most = max(most, head[g]);
                 const uint32_t best = __reduce_max_sync(kAll, K::rank(most));
-                if (best < K::kFloor) break;
                 if constexpr (sizeof(T) == 4) {
                     // of lanes with equal logits the lowest has the lowest expert
                     const int holder = __ffs(__ballot_sync(kAll, K::rank(most) == best)) - 1;
-                    const Key taken = __shfl_sync(kAll, most, holder);
-                    if (lane == to) my_key = taken;
-#pragma unroll
-                    for (int g = 0; g < kRuns; ++g)
-                        if (head[g] == taken) head[g] = *next[g]++;
+                    most = __shfl_sync(kAll, most, holder);
                 } else {
-                    if (lane == to) my_key = best;
-#pragma unroll
-                    for (int g = 0; g < kRuns; ++g)
-                        if (head[g] == best) head[g] = *next[g]++;
+                    most = best;
                 }
+                if (lane == to) my_key = most;
+#pragma unroll
+                for (int g = 0; g < kRuns; ++g) K::advance(head[g], next[g], most);
             }
             if (!p.chosen_only) {
                 const float m = K::value(K::rank(__shfl_sync(kAll, my_key, r * p.width)));
                 float s = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kN; ++i) s += expf(to_float(x[i]) - m);
+                for (int i = 0; i < kN; ++i) s += expf(x.value(i) - m);
                 s = lanes_sum(s);
                 if (slot == r) my_sum = s;
             }
         }
         // (a row's first choice has its largest logit; rows without one have no choice at all)
-        const int my_e = my_key == 0 ? -1 : 0xFFFF - static_cast<int>(my_key & 0xFFFFu);
+        const int my_e = K::rank(my_key) < K::kFloor ? -1 : 0xFFFF - static_cast<int>(my_key & 0xFFFFu);
         const float v = K::value(K::rank(my_key)), m = __shfl_sync(kAll, v, slot * p.width);
         const float z = my_e >= 0 ? expf(v - m) : 0.0f;
         const float s = lanes_sum(z, p.width);
@@ -305,9 +345,15 @@ __device__ __forceinline__ void store_lane(const Route& p, long long t, int lane
     const bool whole = e0 + kN <= p.experts && (reinterpret_cast<uintptr_t>(row + e0) & (kBytes < 16 ? kBytes - 1 : 15)) == 0;
     alignas(16) D v[kN];
     if (whole) {
-        if (p.accumulate) load_lane<D, kN>(row + e0, v);
+        if (p.accumulate) {
+            Row<D, kN> old;
+            old.load(row + e0);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] = from_float<D>(p.accumulate ? to_float(v[i]) + d[i] : d[i]);
+            for (int i = 0; i < kN; ++i) v[i] = from_float<D>(old.value(i) + d[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[i] = from_float<D>(d[i]);
+        }
         if constexpr (kBytes >= 16) {
 #pragma unroll
             for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4*>(row + e0)[i] = reinterpret_cast<const uint4*>(v)[i];
@@ -380,13 +426,13 @@ __global__ void __launch_bounds__(32 * kWarps, resident(kN, true)) route_grad_ke
             if (here) row[e] = 0.0f;
             __syncwarp();
             if (any && !p.chosen_only) {
-                alignas(16) T x[kN];
+                Row<T, kN> x;
                 load_row<T, kN>(p, tb + r, lane, x);
                 const float m = row_max<T, kN>(x);
                 float z[kN], s = 0.0f, inner = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
-                    z[i] = expf(to_float(x[i]) - m);
+                    z[i] = expf(x.value(i) - m);
                     s += z[i];
                     inner += z[i] * d[i];
                 }
