@@ -1,5 +1,6 @@
 // linear_xent.cu -- softmax cross entropy of a linear layer over a vocabulary:
-// checks, the pieces of the vocabulary, launches.  The tiles: xent_kernel.cuh.
+// checks, the pieces of the vocabulary, launches.  The tiles: xent_kernel.cuh,
+// xent_product_kernel.cuh.
 //
 //   z = X W^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_{t, y_t}
 //   mean = sum of loss_t / n over the n tokens whose target names a word
@@ -8,9 +9,9 @@
 //
 // Forward, the tiles leave (M, s) of every row and column tile, which one small
 // kernel joins.  Backward, the logits of a piece of the vocabulary are computed
-// again and leave dz of that piece in the workspace, in the operands' type; two
-// products of this library take it to dX (summed over the pieces in fp32) and
-// dW.  One rounding of dz to 16 bits stands between the logits and the
+// again and leave dz of that piece in the workspace, in the operands' type; one
+// launch (xent_product_kernel.cuh) takes it to dX (summed over the pieces in
+// fp32) and dW.  One rounding of dz to 16 bits stands between the logits and the
 // gradients, of the same size as that of a 16-bit gradient: the other products
 // would need fp32 operands.  What is rounded is dz over the largest |r_t|, which
 // the products multiply by: where all tokens weigh alike, dz of an unlikely
@@ -23,7 +24,7 @@
 #include <climits>
 #include <cstring>
 
-#include "xent_kernel.cuh"
+#include "xent_product_kernel.cuh"
 
 namespace {
 
@@ -140,14 +141,14 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
 // -------------------------------------------------------- r_t, and scales
 
 struct Scales {
-    int tokens, vocab, fill;
+    int tokens, vocab;
     const int* target;
     const int* valid;
     const float* grad_mean;   // may be nullptr
     const float* grad_loss;   // may be nullptr
     float top;                // what the largest |r_t| becomes
     float* r;                 // [tokens]: r_t as the tiles take it
-    float* back;              // [fill]: what the products multiply by
+    float* back;              // what the products multiply by
 };
 
 __device__ __forceinline__ float weight_of(const Scales& p, int t, float each) {
@@ -171,30 +172,8 @@ __global__ void __launch_bounds__(1024) scales_kernel(const __grid_constant__ Sc
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     if (!(m > 0.0f && m < INFINITY)) m = 1.0f;
-    for (int i = threadIdx.x; i < p.fill; i += 1024) p.back[i] = m / p.top;
+    if (threadIdx.x == 0) *p.back = m / p.top;
     for (int t = threadIdx.x; t < p.tokens; t += 1024) p.r[t] = weight_of(p, t, each) / m * p.top;
-}
-
-// ------------------------------------------------- fp32 sums to fp16 outputs
-
-struct Half {
-    const float* src;
-    long long lds;
-    __half* dst;
-    long long ldd;
-    int rows, cols;
-    float beta;
-};
-__global__ void __launch_bounds__(256) half_kernel(const __grid_constant__ Half p) {
-    tcg::host::wait_for_kernel_ahead();
-    const int c = static_cast<int>(blockIdx.y * 256 + threadIdx.x);
-    if (c >= p.cols) return;
-    for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        float v = p.src[r * p.lds + c];
-        __half* d = p.dst + r * p.ldd + c;
-        if (p.beta != 0.0f) v = fmaf(p.beta, __half2float(*d), v);
-        *d = __float2half_rn(v);
-    }
 }
 
 // ----------------------------------------------------------------- plans
@@ -236,12 +215,48 @@ int piece_words(int tokens, int vocab) {
     return static_cast<int>(std::min<long long>(vocab, blocks(blocks(vocab, pieces), 256) * 256));
 }
 
-// Where things lie in the workspace.  Forward: behind the ranges that are kept
-// zero.  Backward: behind what the products need.
+// a counter for each warp of both CTAs of a split tile
+constexpr long long kMaxSplitTiles = tcg::host::kCounterBytes / sizeof(int) / (2 * tcg::xent::kRowWarps);
+
+// How dX's and dW's tiles go to the workers (pairs of CTAs).
+struct ProductPlan {
+    int tile_n = 256, splits = 1, early = 0, workers = 1;
+};
+
+// first, second: dX's and dW's tiles (0 where it is not wanted), kb: their
+// stages of K.  A stage is 1024 cycles of the tensor cores on a tile of 256
+// columns; a tile's way to memory takes about three stages' time and hides
+// behind the next tile's longer sums.  Pieces of a split tile cost three more
+// each.  Splits by the shortest time of the fullest worker.
+ProductPlan plan_products(long long first, int first_kb, long long second, int second_kb, int workers) {
+    ProductPlan best;
+    long long least = LLONG_MAX;
+    const long long c2 = std::max(second_kb, 3);
+    for (int s = 1; s <= 16; ++s) {
+        if (s > 1 && (first * s > 2 * workers || first > kMaxSplitTiles || first_kb < 4 * s)) break;
+        const long long units = first * s, c1 = std::max(blocks(first_kb, s), 3LL) + (s > 1 ? 3 : 0);
+        const long long rest = units % workers, early = rest > 0 ? c1 / c2 : 0;
+        const long long taken = std::min(second, early * (workers - rest));
+        const long long time = blocks(units, workers) * c1 + blocks(second - taken, workers) * c2;
+        if (time < least) {
+            least = time;
+            best.splits = s;
+            best.early = static_cast<int>(std::min(early, 1LL << 20));
+        }
+    }
+    best.workers = static_cast<int>(std::max(1LL, std::min<long long>(workers, std::max(first * best.splits, second))));
+    if (best.workers < workers) {   // fewer tiles than workers: round they go as they are
+        const long long rest = first * best.splits % best.workers;
+        best.early = rest > 0 ? static_cast<int>(std::min((blocks(first_kb, best.splits) + 3) / c2, 1LL << 20)) : 0;
+    }
+    return best;
+}
+
+// Where things lie in the workspace, behind the ranges that are kept zero.
 struct Layout {
     size_t part = 0, picked = 0, sums = 0, counts = 0;                      // forward
-    size_t r = 0, back = 0, dz = 0, dx = 0, dw = 0;                         // backward
-    size_t bytes = 0;
+    size_t r = 0, back = 0, dz = 0, dx = 0, partials = 0;                   // backward
+    size_t bytes = tcg::host::kScratchAt;
     size_t take(size_t n) {
         const size_t at = bytes;
         bytes += padded(n);
@@ -251,7 +266,6 @@ struct Layout {
 
 Layout forward_layout(int tokens, int vocab) {
     Layout l;
-    l.bytes = tcg::host::kScratchAt;
     l.part = l.take(2 * static_cast<size_t>(blocks(vocab, kMinTileN)) * tokens * sizeof(float2));
     l.picked = l.take(static_cast<size_t>(tokens) * sizeof(float));
     l.sums = l.take(static_cast<size_t>(blocks(tokens, kFinishRows)) * sizeof(double));
@@ -259,48 +273,40 @@ Layout forward_layout(int tokens, int vocab) {
     return l;
 }
 
-int padded_hidden(int hidden) { return static_cast<int>(blocks(hidden, 8) * 8); }
+int pitch_of(int n) { return static_cast<int>(blocks(n, 32) * 32); }   // rows of any type start on 32 bytes
 
-Layout backward_layout(int tokens, int vocab, int hidden) {
+Layout backward_layout(int tokens, int vocab, int hidden, int sms) {
     Layout l;
-    const int words = piece_words(tokens, vocab), rest = vocab - (vocab - 1) / words * words;
-    size_t need = tcg::host::kScratchAt;
-    for (const int w : {words, rest}) {
-        need = std::max(need, tcg_workspace_size(tokens, hidden, w, TCG_BF16));
-        need = std::max(need, tcg_workspace_size(w, hidden, tokens, TCG_BF16));
-    }
-    l.bytes = padded(need);
-    const size_t ld = padded_hidden(hidden);
+    const int words = piece_words(tokens, vocab);
     l.r = l.take(static_cast<size_t>(tokens) * sizeof(float));
-    l.back = l.take(static_cast<size_t>(std::max(tokens, words)) * sizeof(float));
-    l.dz = l.take(static_cast<size_t>(tokens) * blocks(words, 32) * 32 * 2);
-    l.dx = l.take(static_cast<size_t>(tokens) * ld * sizeof(float));
-    l.dw = l.take(static_cast<size_t>(words) * ld * sizeof(float));
+    l.back = l.take(sizeof(float));
+    l.dz = l.take(static_cast<size_t>(tokens) * pitch_of(words) * 2);
+    l.dx = l.take(words < vocab ? static_cast<size_t>(tokens) * pitch_of(hidden) * sizeof(float) : 0);
+    // (tiles are split while their pieces are at most two for each pair of SMs)
+    l.partials = l.take(static_cast<size_t>(sms / 2 * 2) * tcg::xent::kPartialFloats * sizeof(float));
     return l;
 }
 
 // ---------------------------------------------------------------- launches
 
-template <typename T, bool kPair, bool kGrad>
-tcg_status launch(const Params& p, const Plan& pl, cudaStream_t stream) {
-    auto* kernel = tcg::xent::xent_kernel<T, kPair, kGrad>;
-    constexpr int kSmem = tcg::xent::Shape<kPair>::kSmemBytes;
-    static tcg::host::OncePerDevice once;
-    cudaError_t e = once([&] {
-        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        cudaFuncAttributes a;
-        if (err == cudaSuccess) err = cudaFuncGetAttributes(&a, kernel);
-        // the register hand-over draws on what the block is launched with
-        if (err == cudaSuccess && a.numRegs < tcg::xent::kLaunchRegs) err = cudaErrorInvalidConfiguration;
-        return err;
-    });
-    if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent kernel attributes", e);
+template <typename K>
+cudaError_t set_attributes(K* kernel, int smem) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaFuncAttributes a;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
+    // the register hand-over draws on what the block is launched with
+    if (e == cudaSuccess && a.numRegs < tcg::xent::kLaunchRegs) e = cudaErrorInvalidConfiguration;
+    return e;
+}
+
+template <typename P>
+tcg_status launch_ctas(void (*kernel)(P), const P& p, bool pair, int workers, int smem, cudaStream_t stream) {
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = dim3((kPair ? 2 : 1) * pl.workers);
+    cfg.gridDim = dim3((pair ? 2 : 1) * workers);
     cfg.blockDim = dim3(tcg::xent::kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -309,9 +315,19 @@ tcg_status launch(const Params& p, const Plan& pl, cudaStream_t stream) {
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = kPair ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, p);
+    cfg.numAttrs = pair ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
     return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch("tcg_linear_xent", e);
+}
+
+template <typename T, bool kPair, bool kGrad>
+tcg_status launch(const Params& p, const Plan& pl, cudaStream_t stream) {
+    auto* kernel = tcg::xent::xent_kernel<T, kPair, kGrad>;
+    constexpr int kSmem = tcg::xent::Shape<kPair>::kSmemBytes;
+    static tcg::host::OncePerDevice once;
+    const cudaError_t e = once([&] { return set_attributes(kernel, kSmem); });
+    if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent kernel attributes", e);
+    return launch_ctas(kernel, p, kPair, pl.workers, kSmem, stream);
 }
 
 template <typename T, bool kGrad>
@@ -348,6 +364,26 @@ tcg_status launch_tiles(Params& p, tcg_dtype dtype, const void* X, int ldx, cons
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int size_of(tcg_dtype t) { return t == TCG_F32 ? 4 : 2; }
 
+int out_type(tcg_dtype t) { return t == TCG_F32 ? tcg::xent::kOutF32 : t == TCG_F16 ? tcg::xent::kOutF16 : tcg::xent::kOutBf16; }
+
+void set_output(tcg::xent::Product& q, void* out, long long ld, tcg_dtype t, float beta) {
+    q.out = out;
+    q.ldo = ld;
+    q.type = out_type(t);
+    q.beta = beta;
+    q.vec = aligned(out, 32) && ld * size_of(t) % 32 == 0;
+}
+
+tcg_status launch_products(tcg::xent::Products& p, const ProductPlan& pl, cudaStream_t stream) {
+    auto* kernel = tcg::xent::xent_product_kernel;
+    static tcg::host::OncePerDevice once;
+    cudaError_t e = once([&] { return set_attributes(kernel, tcg::xent::kProductSmem); });
+    if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent_backward kernel attributes", e);
+    p.timeout_ns = tcg::host::wait_timeout_ns();
+    p.fault_inject = tcg::host::fault_inject();
+    return launch_ctas(kernel, p, true, pl.workers, tcg::xent::kProductSmem, stream);
+}
+
 tcg_status check(int tokens, int vocab, int hidden, tcg_dtype dtype, const void* X, int ldx, const void* W, int ldw,
                  const int* target) {
     if (tokens < 0 || vocab < 1 || hidden < 1) return TCG_ERR_INVALID_ARG;
@@ -370,22 +406,16 @@ tcg_status check_gradient(const void* d, int ld, int hidden, tcg_dtype t) {
     return aligned(d, size_of(t)) ? TCG_OK : TCG_ERR_MISALIGNED;
 }
 
-tcg_status to_half(const float* src, int lds, void* dst, long long ldd, int rows, int cols, float beta, cudaStream_t stream) {
-    if (rows == 0) return TCG_OK;
-    Half p = {src, lds, static_cast<__half*>(dst), ldd, rows, cols, beta};
-    const dim3 grid(std::min(rows, 4096), static_cast<unsigned>(blocks(cols, 256)));
-    const cudaError_t e = tcg::host::launch_early(half_kernel, grid, 256, stream, p);
-    return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch("tcg_linear_xent_backward", e);
-}
-
 }  // namespace
 
 extern "C" {
 
 size_t tcg_linear_xent_workspace_size(int tokens, int vocab, int hidden, int backward) {
     if (tokens < 0 || vocab < 1 || hidden < 1) return 0;
+    tcg::host::Device dev;
+    if (tcg::host::device(dev) != TCG_OK) dev.num_sms = 1024;
     const size_t forward = forward_layout(tokens, vocab).bytes;
-    return backward ? std::max(forward, backward_layout(tokens, vocab, hidden).bytes) : forward;
+    return backward ? std::max(forward, backward_layout(tokens, vocab, hidden, dev.num_sms).bytes) : forward;
 }
 
 tcg_status tcg_linear_xent(int tokens, int vocab, int hidden, tcg_dtype dtype, const void* X, int ldx, const void* W, int ldw,
@@ -440,33 +470,27 @@ tcg_status tcg_linear_xent_backward(int tokens, int vocab, int hidden, tcg_dtype
     if (!aligned(lse, 4) || !aligned(num_valid, 4) || !aligned(grad_mean, 4) || !aligned(grad_loss, 4)) return TCG_ERR_MISALIGNED;
     tcg::host::Device dev;
     if ((st = tcg::host::device(dev)) != TCG_OK) return st;
-    const Layout l = backward_layout(tokens, vocab, hidden);
+    const Layout l = backward_layout(tokens, vocab, hidden, dev.num_sms);
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < l.bytes)
         return tcg::host::fail(TCG_ERR_WORKSPACE, "workspace NULL, not 16-byte aligned or smaller than tcg_linear_xent_workspace_size");
     if (!dX && !dW) return TCG_OK;
+    // (no tokens: dW is dw_beta times itself, which a product over no tokens at all gives as well)
     char* ws = static_cast<char*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int words = piece_words(tokens, vocab), ld = padded_hidden(hidden);
-    const int pitch = static_cast<int>(blocks(words, 32) * 32);
+    const int words = piece_words(tokens, vocab), pitch = pitch_of(words), ld = pitch_of(hidden);
     float* r = reinterpret_cast<float*>(ws + l.r);
     float* back = reinterpret_cast<float*>(ws + l.back);
-    void* dz = ws + l.dz;
     float* dx32 = reinterpret_cast<float*>(ws + l.dx);
-    float* dw32 = reinterpret_cast<float*>(ws + l.dw);
-    if (tokens > 0) {
-        Scales sc = {tokens, vocab, std::max(tokens, words), target, num_valid, grad_mean, grad_loss, dtype == TCG_F16 ? kHalfTop : 1.0f, r, back};
-        const cudaError_t e = tcg::host::launch_early(scales_kernel, dim3(1), 1024, s, sc);
-        if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent_backward", e);
-    }
-    const tcg_epilogue none = {nullptr, TCG_BF16, TCG_ACT_NONE};
-    tcg_scales scales;
-    memset(&scales, 0, sizeof scales);
-    scales.scale_a = scales.scale_b = 1.0f;
-    scales.row_scale = back;
+    char* dz = ws + l.dz;
+    Scales sc = {tokens, vocab, target, num_valid, grad_mean, grad_loss, dtype == TCG_F16 ? kHalfTop : 1.0f, r, back};
+    const cudaError_t e = tcg::host::launch_early(scales_kernel, dim3(1), 1024, s, sc);
+    if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent_backward", e);
     for (int v0 = 0; v0 < vocab; v0 += words) {
         const int n = std::min(words, vocab - v0);
         const bool last = v0 + n == vocab;
         const char* w = static_cast<const char*>(W) + static_cast<size_t>(v0) * ldw * 2;
+        tcg::xent::Products q;
+        memset(&q, 0, sizeof q);
         if (tokens > 0) {
             Params p;
             memset(&p, 0, sizeof p);
@@ -477,27 +501,44 @@ tcg_status tcg_linear_xent_backward(int tokens, int vocab, int hidden, tcg_dtype
             p.ldd = pitch;
             p.status = reinterpret_cast<int*>(ws);
             if ((st = launch_tiles<true>(p, dtype, X, ldx, W, ldw, tokens, hidden, v0, n, dev, s)) != TCG_OK) return st;
-        }
-        if (dX && tokens > 0) {
-            // fp32 sums of the pieces so far, in dX itself where it is fp32
-            const bool own = dx_dtype == TCG_F32;
-            float* sum = own ? static_cast<float*>(dX) : dx32;
-            const int lds = own ? lddx : ld;
-            const bool out = !own && last && dx_dtype == TCG_BF16;
-            st = tcg_gemm(tokens, hidden, n, 1.0f, dz, pitch, TCG_ROW, w, ldw, TCG_ROW, v0 > 0 ? 1.0f : 0.0f, sum, lds, TCG_F32,
-                          out ? dX : sum, out ? lddx : lds, out ? TCG_BF16 : TCG_F32, none, dtype, scales, ws, l.r, s);
-            if (st == TCG_OK && last && dx_dtype == TCG_F16) st = to_half(sum, lds, dX, lddx, tokens, hidden, 0.0f, s);
+            // dz as the rows operand of both, its words or its tokens being K
+            CUtensorMap map_dz;
+            st = tcg::host::map_bytes(&map_dz, dz, 2ull * n, tokens, 2ull * pitch, tcg::xent::kRowBytes, tcg::xent::kStageK);
+            q.q[0].a = q.q[1].a = map_dz;
+            if (st == TCG_OK) st = tcg::host::map_bytes(&q.q[0].b, w, 2ull * hidden, n, 2ull * ldw, tcg::xent::kRowBytes, tcg::xent::kStageK);
+            if (st == TCG_OK) st = tcg::host::map_bytes(&q.q[1].b, X, 2ull * hidden, tokens, 2ull * ldx, tcg::xent::kRowBytes, tcg::xent::kStageK);
             if (st != TCG_OK) return st;
         }
-        if (dW) {
-            const bool direct = dw_dtype != TCG_F16;
-            char* d = static_cast<char*>(dW) + static_cast<size_t>(v0) * lddw * size_of(dw_dtype);
-            st = tcg_gemm(n, hidden, tokens, 1.0f, dz, pitch, TCG_COL, X, ldx, TCG_ROW, direct ? dw_beta : 0.0f, d, lddw, direct ? dw_dtype : TCG_F32,
-                          direct ? static_cast<void*>(d) : dw32, direct ? lddw : ld, direct ? dw_dtype : TCG_F32, none, dtype, scales, ws,
-                          l.r, s);
-            if (st == TCG_OK && !direct) st = to_half(dw32, ld, d, lddw, n, hidden, dw_beta, s);
-            if (st != TCG_OK) return st;
+        q.tile_n = hidden <= 128 ? 128 : 256;
+        q.fmt = dtype == TCG_F16 ? 0u : 1u;
+        q.back = back;
+        q.partials = reinterpret_cast<float*>(ws + l.partials);
+        q.counters = reinterpret_cast<int*>(ws + tcg::host::kWorkspaceHeader);
+        q.status = reinterpret_cast<int*>(ws);
+        q.q[1].a_along_m = 1;
+        for (int i = 0; i < 2; ++i) {
+            tcg::xent::Product& one = q.q[i];
+            one.M = i == 0 ? tokens : n;
+            one.N = hidden;
+            one.num_kb = static_cast<int>(blocks(i == 0 ? n : tokens, tcg::xent::kStageK));
+            one.num_n = static_cast<int>(blocks(hidden, q.tile_n));
+            one.num_m = (i == 0 ? dX : dW) ? static_cast<int>(blocks(one.M, 2 * tcg::xent::kBM)) : 0;
+            one.splits = 1;
         }
+        // dX: fp32 sums of the pieces so far, in dX itself where it is fp32
+        if (dX && dx_dtype == TCG_F32) set_output(q.q[0], dX, lddx, TCG_F32, v0 > 0 ? 1.0f : 0.0f);
+        else if (dX && !last) set_output(q.q[0], dx32, ld, TCG_F32, v0 > 0 ? 1.0f : 0.0f);
+        else if (dX) set_output(q.q[0], dX, lddx, dx_dtype, 0.0f);
+        if (dX && dx_dtype != TCG_F32 && last && v0 > 0) {
+            q.q[0].sum = dx32;
+            q.q[0].ld_sum = ld;
+        }
+        if (dW) set_output(q.q[1], static_cast<char*>(dW) + static_cast<size_t>(v0) * lddw * size_of(dw_dtype), lddw, dw_dtype, dw_beta);
+        const long long first = static_cast<long long>(q.q[0].num_m) * q.q[0].num_n, second = static_cast<long long>(q.q[1].num_m) * q.q[1].num_n;
+        const ProductPlan pl = plan_products(first, q.q[0].num_kb, second, q.q[1].num_kb, std::max(1, dev.num_sms / 2));
+        q.q[0].splits = pl.splits;
+        q.early = pl.early;
+        if (first + second > 0 && (st = launch_products(q, pl, s)) != TCG_OK) return st;
     }
     return TCG_OK;
 }

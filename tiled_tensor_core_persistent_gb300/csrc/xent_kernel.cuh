@@ -111,6 +111,7 @@ __device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, int* status
             if (atomicCAS(status, 0, static_cast<int>(TCG_ERR_TIMEOUT)) == 0) {
                 status[1] = where;
                 status[2] = static_cast<int>(blockIdx.x);
+                status[3] = 1;   // arrival counters may be left counting
             }
             return false;
         }
@@ -118,7 +119,8 @@ __device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, int* status
 }
 
 // The whole warp waits on one barrier and agrees on the outcome.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Params& p, Ctl* ctl, int where, bool honor_abort = true) {
+template <typename P>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const P& p, Ctl* ctl, int where, bool honor_abort = true) {
     bool ok = ptx::mbar_try_wait(ptx::smem_u32(bar), parity);
     if (!ok) ok = spin(bar, parity, p.status, p.timeout_ns, ctl, where, honor_abort);
     return __all_sync(0xffffffffu, ok);
@@ -149,6 +151,44 @@ __device__ __forceinline__ void landed(float (&r)[kChunk]) {
                    "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
                  :
                  : "memory");
+}
+
+// A warp's 32 rows of an accumulator, hw columns from taddr on, into z or added to it.
+__device__ __forceinline__ void take_rows(uint32_t taddr, int hw, bool first, float (&z)[kHalf / kChunk][kChunk]) {
+    ptx::tc_fence_after_sync();
+    if (first) {
+#pragma unroll
+        for (int c = 0; c < kHalf / kChunk; ++c)
+            if (c * kChunk < hw) fetch(taddr + static_cast<uint32_t>(c * kChunk), z[c]);
+#pragma unroll
+        for (int c = 0; c < kHalf / kChunk; ++c) landed(z[c]);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < kHalf / kChunk; c += 2) {
+        if (c * kChunk >= hw) continue;
+        float more[2][kChunk];
+        fetch(taddr + static_cast<uint32_t>(c * kChunk), more[0]);
+        if ((c + 1) * kChunk < hw) fetch(taddr + static_cast<uint32_t>((c + 1) * kChunk), more[1]);
+        landed(more[0]);
+        landed(more[1]);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            z[c][i] += more[0][i];
+            z[c + 1][i] += more[1][i];
+        }
+    }
+}
+
+// The accumulator goes back as soon as it is in registers.
+template <bool kPair>
+__device__ __forceinline__ void hand_back(uint64_t* bar, bool leader, int lane) {
+    ptx::tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) {
+        if (kPair && !leader) ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(bar), 0));
+        else ptx::mbar_arrive(bar);
+    }
 }
 
 // The two accumulators in turn, and how often both were walked.
@@ -348,38 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             for (int part = 0; part < p.parts; ++part) {
                 ok = wait(&ctl->tmem_full[acc.at], acc.phase, p, ctl, 4);
                 if (!ok) break;
-                ptx::tc_fence_after_sync();
-                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(g * 32) << 16) + static_cast<uint32_t>(acc.at * kAccCols + half * hw);
-                if (part == 0) {
-#pragma unroll
-                    for (int c = 0; c < kHalf / kChunk; ++c)
-                        if (c * kChunk < hw) fetch(taddr + static_cast<uint32_t>(c * kChunk), z[c]);
-#pragma unroll
-                    for (int c = 0; c < kHalf / kChunk; ++c) landed(z[c]);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < kHalf / kChunk; c += 2) {
-                        if (c * kChunk >= hw) continue;
-                        float more[2][kChunk];
-                        fetch(taddr + static_cast<uint32_t>(c * kChunk), more[0]);
-                        if ((c + 1) * kChunk < hw) fetch(taddr + static_cast<uint32_t>((c + 1) * kChunk), more[1]);
-                        landed(more[0]);
-                        landed(more[1]);
-#pragma unroll
-                        for (int i = 0; i < kChunk; ++i) {
-                            z[c][i] += more[0][i];
-                            z[c + 1][i] += more[1][i];
-                        }
-                    }
-                }
-                // the accumulator goes back as soon as it is in registers
-                ptx::tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    uint64_t* bar = &ctl->tmem_empty[acc.at];
-                    if (kPair && !leader) ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(bar), 0));
-                    else ptx::mbar_arrive(bar);
-                }
+                take_rows(tmem_base + (static_cast<uint32_t>(g * 32) << 16) + static_cast<uint32_t>(acc.at * kAccCols + half * hw), hw, part == 0, z);
+                hand_back<kPair>(&ctl->tmem_empty[acc.at], leader, lane);
                 acc.next();
             }
             if (!ok) break;
