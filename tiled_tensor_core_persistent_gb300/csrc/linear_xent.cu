@@ -138,44 +138,6 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
     }
 }
 
-// -------------------------------------------------------- r_t, and scales
-
-struct Scales {
-    int tokens, vocab;
-    const int* target;
-    const int* valid;
-    const float* grad_mean;   // may be nullptr
-    const float* grad_loss;   // may be nullptr
-    float top;                // what the largest |r_t| becomes
-    float* r;                 // [tokens]: r_t as the tiles take it
-    float* back;              // what the products multiply by
-};
-
-__device__ __forceinline__ float weight_of(const Scales& p, int t, float each) {
-    const int y = p.target[t];
-    if (y < 0 || y >= p.vocab) return 0.0f;
-    return each + (p.grad_loss ? p.grad_loss[t] : 0.0f);
-}
-
-__global__ void __launch_bounds__(1024) scales_kernel(const __grid_constant__ Scales p) {
-    tcg::host::wait_for_kernel_ahead();
-    __shared__ float most[32];
-    const int n = *p.valid;
-    const float each = p.grad_mean && n > 0 ? *p.grad_mean / static_cast<float>(n) : 0.0f;
-    float m = 0.0f;   // (fmaxf passes over NaN: such a token leaves the others' scale alone)
-    for (int t = threadIdx.x; t < p.tokens; t += 1024) m = fmaxf(m, fabsf(weight_of(p, t, each)));
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
-    __syncthreads();
-    m = most[threadIdx.x & 31];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (!(m > 0.0f && m < INFINITY)) m = 1.0f;
-    if (threadIdx.x == 0) *p.back = m / p.top;
-    for (int t = threadIdx.x; t < p.tokens; t += 1024) p.r[t] = weight_of(p, t, each) / m * p.top;
-}
-
 // ----------------------------------------------------------------- plans
 
 long long blocks(long long n, long long b) { return (n + b - 1) / b; }
@@ -226,15 +188,16 @@ struct ProductPlan {
 // first, second: dX's and dW's tiles (0 where it is not wanted), kb: their
 // stages of K.  A stage is 1024 cycles of the tensor cores on a tile of 256
 // columns; a tile's way to memory takes about three stages' time and hides
-// behind the next tile's longer sums.  Pieces of a split tile cost three more
-// each.  Splits by the shortest time of the fullest worker.
+// behind the next tile's longer sums.  A piece of a split tile costs three more,
+// and the last one two for each piece that it adds.  Splits by the shortest time
+// of the fullest worker.
 ProductPlan plan_products(long long first, int first_kb, long long second, int second_kb, int workers) {
     ProductPlan best;
     long long least = LLONG_MAX;
     const long long c2 = std::max(second_kb, 3);
     for (int s = 1; s <= 16; ++s) {
         if (s > 1 && (first * s > 2 * workers || first > kMaxSplitTiles || first_kb < 4 * s)) break;
-        const long long units = first * s, c1 = std::max(blocks(first_kb, s), 3LL) + (s > 1 ? 3 : 0);
+        const long long units = first * s, c1 = std::max(blocks(first_kb, s), 3LL) + (s > 1 ? 3 + 2 * s : 0);
         const long long rest = units % workers, early = rest > 0 ? c1 / c2 : 0;
         const long long taken = std::min(second, early * (workers - rest));
         const long long time = blocks(units, workers) * c1 + blocks(second - taken, workers) * c2;
@@ -255,7 +218,7 @@ ProductPlan plan_products(long long first, int first_kb, long long second, int s
 // Where things lie in the workspace, behind the ranges that are kept zero.
 struct Layout {
     size_t part = 0, picked = 0, sums = 0, counts = 0;                      // forward
-    size_t r = 0, back = 0, dz = 0, dx = 0, partials = 0;                   // backward
+    size_t back = 0, dz = 0, dx = 0, partials = 0;                          // backward
     size_t bytes = tcg::host::kScratchAt;
     size_t take(size_t n) {
         const size_t at = bytes;
@@ -278,7 +241,6 @@ int pitch_of(int n) { return static_cast<int>(blocks(n, 32) * 32); }   // rows o
 Layout backward_layout(int tokens, int vocab, int hidden, int sms) {
     Layout l;
     const int words = piece_words(tokens, vocab);
-    l.r = l.take(static_cast<size_t>(tokens) * sizeof(float));
     l.back = l.take(sizeof(float));
     l.dz = l.take(static_cast<size_t>(tokens) * pitch_of(words) * 2);
     l.dx = l.take(words < vocab ? static_cast<size_t>(tokens) * pitch_of(hidden) * sizeof(float) : 0);
@@ -371,7 +333,8 @@ void set_output(tcg::xent::Product& q, void* out, long long ld, tcg_dtype t, flo
     q.ldo = ld;
     q.type = out_type(t);
     q.beta = beta;
-    q.vec = aligned(out, 32) && ld * size_of(t) % 32 == 0;
+    const long long pitch = ld * size_of(t);
+    q.vec = aligned(out, 32) && pitch % 32 == 0 ? 32 : aligned(out, 16) && pitch % 16 == 0 ? 16 : 0;
 }
 
 tcg_status launch_products(tcg::xent::Products& p, const ProductPlan& pl, cudaStream_t stream) {
@@ -478,13 +441,9 @@ tcg_status tcg_linear_xent_backward(int tokens, int vocab, int hidden, tcg_dtype
     char* ws = static_cast<char*>(workspace);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int words = piece_words(tokens, vocab), pitch = pitch_of(words), ld = pitch_of(hidden);
-    float* r = reinterpret_cast<float*>(ws + l.r);
     float* back = reinterpret_cast<float*>(ws + l.back);
     float* dx32 = reinterpret_cast<float*>(ws + l.dx);
     char* dz = ws + l.dz;
-    Scales sc = {tokens, vocab, target, num_valid, grad_mean, grad_loss, dtype == TCG_F16 ? kHalfTop : 1.0f, r, back};
-    const cudaError_t e = tcg::host::launch_early(scales_kernel, dim3(1), 1024, s, sc);
-    if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent_backward", e);
     for (int v0 = 0; v0 < vocab; v0 += words) {
         const int n = std::min(words, vocab - v0);
         const bool last = v0 + n == vocab;
@@ -496,7 +455,12 @@ tcg_status tcg_linear_xent_backward(int tokens, int vocab, int hidden, tcg_dtype
             memset(&p, 0, sizeof p);
             p.target = target;
             p.lse = lse;
-            p.scale = r;
+            p.valid = num_valid;
+            p.grad_mean = grad_mean;
+            p.grad_loss = grad_loss;
+            p.vocab = vocab;
+            p.top = dtype == TCG_F16 ? kHalfTop : 1.0f;
+            p.back = back;
             p.d = dz;
             p.ldd = pitch;
             p.status = reinterpret_cast<int*>(ws);
@@ -511,7 +475,7 @@ tcg_status tcg_linear_xent_backward(int tokens, int vocab, int hidden, tcg_dtype
         }
         q.tile_n = hidden <= 128 ? 128 : 256;
         q.fmt = dtype == TCG_F16 ? 0u : 1u;
-        q.back = back;
+        q.back = tokens > 0 ? back : nullptr;
         q.partials = reinterpret_cast<float*>(ws + l.partials);
         q.counters = reinterpret_cast<int*>(ws + tcg::host::kWorkspaceHeader);
         q.status = reinterpret_cast<int*>(ws);
@@ -526,14 +490,17 @@ tcg_status tcg_linear_xent_backward(int tokens, int vocab, int hidden, tcg_dtype
             one.splits = 1;
         }
         // dX: fp32 sums of the pieces so far, in dX itself where it is fp32
-        if (dX && dx_dtype == TCG_F32) set_output(q.q[0], dX, lddx, TCG_F32, v0 > 0 ? 1.0f : 0.0f);
-        else if (dX && !last) set_output(q.q[0], dx32, ld, TCG_F32, v0 > 0 ? 1.0f : 0.0f);
-        else if (dX) set_output(q.q[0], dX, lddx, dx_dtype, 0.0f);
-        if (dX && dx_dtype != TCG_F32 && last && v0 > 0) {
-            q.q[0].sum = dx32;
-            q.q[0].ld_sum = ld;
+        if (dX && tokens > 0) {
+            if (dx_dtype == TCG_F32) set_output(q.q[0], dX, lddx, TCG_F32, v0 > 0 ? 1.0f : 0.0f);
+            else if (!last) set_output(q.q[0], dx32, ld, TCG_F32, v0 > 0 ? 1.0f : 0.0f);
+            else set_output(q.q[0], dX, lddx, dx_dtype, 0.0f);
+            if (dx_dtype != TCG_F32 && last && v0 > 0) {
+                q.q[0].sum = dx32;
+                q.q[0].ld_sum = ld;
+            }
         }
-        if (dW) set_output(q.q[1], static_cast<char*>(dW) + static_cast<size_t>(v0) * lddw * size_of(dw_dtype), lddw, dw_dtype, dw_beta);
+        if (dW)
+            set_output(q.q[1], static_cast<char*>(dW) + static_cast<size_t>(v0) * lddw * size_of(dw_dtype), lddw, dw_dtype, dw_beta);
         const long long first = static_cast<long long>(q.q[0].num_m) * q.q[0].num_n, second = static_cast<long long>(q.q[1].num_m) * q.q[1].num_n;
         const ProductPlan pl = plan_products(first, q.q[0].num_kb, second, q.q[1].num_kb, std::max(1, dev.num_sms / 2));
         q.q[0].splits = pl.splits;

@@ -467,6 +467,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
     asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// Results and arguments below 2^-126 count as 0.
+__device__ __forceinline__ float ex2_approx_ftz(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
 // ------------------------------------------------------------ descriptors
 

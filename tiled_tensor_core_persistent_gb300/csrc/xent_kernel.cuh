@@ -6,8 +6,9 @@
 //   z_tv = sum_h X_th W_vh                                   (fp32, in TMEM)
 //   forward:  for each tile and row  M = max_v z_tv log2(e),  s = sum_v 2^(z_tv log2(e) - M),
 //             and z_ty where the row's target y lies in the tile
-//   backward: d_tv = r_t (2^((z_tv - lse_t) log2(e)) - [v = y_t]), rounded to the
-//             operands' type
+//   backward: r_t = grad_mean / n + grad_loss_t (0 where y is no word), and
+//             d_tv = top r_t / max |r| (2^((z_tv - lse_t) log2(e)) - [v = y_t]), rounded to
+//             the operands' type
 //
 // Tiles of 256 rows (a pair of CTAs; 128, one CTA, where there are no more rows
 // than that) and up to 256 columns; the width is the one whose waves fit
@@ -68,13 +69,20 @@ struct Params {
     float* picked;                      // [tokens]: z of the target
     // backward
     const float* lse;                   // [tokens]
-    const float* scale;                 // [tokens]: r_t
+    const int* valid;                   // n
+    const float* grad_mean;             // may be nullptr
+    const float* grad_loss;             // [tokens], may be nullptr
+    int vocab;                          // targets in [0, vocab) count
+    float top;                          // what the largest |r_t| becomes in d
+    float* back;                        // what undoes that
     void* d;
     long long ldd;                      // a multiple of 32
     int* status;
     long long timeout_ns;
     int fault_inject;
 };
+
+constexpr int kCtlBytes = 512;
 
 template <bool kPair>
 struct Shape {
@@ -85,7 +93,7 @@ struct Shape {
     static constexpr int kBBytes = kAtoms * kBRows * kRowBytes;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kStages = kPair ? 3 : 4;
-    static constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 512;   // alignment, barriers
+    static constexpr int kSmemBytes = kStages * kStageBytes + 1024 + kCtlBytes;   // 1024: alignment
 };
 
 struct alignas(16) Ctl {
@@ -94,8 +102,9 @@ struct alignas(16) Ctl {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    float most[kRowWarps];
 };
-static_assert(sizeof(Ctl) <= 512, "the barriers fit");
+static_assert(sizeof(Ctl) <= kCtlBytes, "the barriers fit");
 
 // (inlined: a call's registers do not fit between the two shares)
 __device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, int* status, long long limit_ns, Ctl* ctl, int where,
@@ -180,13 +189,17 @@ __device__ __forceinline__ void take_rows(uint32_t taddr, int hw, bool first, fl
     }
 }
 
-// The accumulator goes back as soon as it is in registers.
+// The accumulator goes back as soon as it is in registers.  It hands over columns
+// that this warp has read, no memory, so the arrival on the pair leader's barrier
+// needs no release at cluster scope: with one, the fence in front of it waited
+// for the warp's stores (2000 cycles a tile in the peer CTA).
 template <bool kPair>
 __device__ __forceinline__ void hand_back(uint64_t* bar, bool leader, int lane) {
     ptx::tc_fence_before_sync();
     __syncwarp();
     if (lane == 0) {
-        if (kPair && !leader) ptx::mbar_arrive_cluster(ptx::map_to_cta(ptx::smem_u32(bar), 0));
+        if (kPair && !leader)
+            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(ptx::map_to_cta(ptx::smem_u32(bar), 0)) : "memory");
         else ptx::mbar_arrive(bar);
     }
 }
@@ -364,6 +377,29 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
         const int g = warp & 3;                 // the TMEM lanes this warp may read
         const int half = (warp - kControlWarps) >> 2, hw = p.tile_n / 2;   // the columns [half * hw, half * hw + hw) of a tile
+        float each = 0.0f, to_top = 1.0f;
+        if constexpr (kGrad) {
+            // the largest |r_t|, by every CTA for itself while its first products run
+            const int count = *p.valid;
+            each = p.grad_mean && count > 0 ? *p.grad_mean / static_cast<float>(count) : 0.0f;
+            float most = fabsf(each);
+            if (p.grad_loss) {
+                most = 0.0f;   // (fmaxf passes over NaN: such a token leaves the others' scale alone)
+                for (int t = static_cast<int>(threadIdx.x) - 32 * kControlWarps; t < p.tokens; t += 32 * kRowWarps) {
+                    const int y = p.target[t];
+                    if (y >= 0 && y < p.vocab) most = fmaxf(most, fabsf(each + p.grad_loss[t]));
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                if (lane == 0) ctl->most[warp - kControlWarps] = most;
+                ptx::named_barrier_sync(1, 32 * kRowWarps);
+#pragma unroll
+                for (int i = 0; i < kRowWarps; ++i) most = fmaxf(most, ctl->most[i]);
+            }
+            if (!(most > 0.0f && most < INFINITY)) most = 1.0f;
+            to_top = most;
+            if (blockIdx.x == 0 && warp == kControlWarps && lane == 0) *p.back = most / p.top;
+        }
         Ring acc;
         bool ok = true;
         for (int tile = worker; ok && tile < tiles; tile += workers) {
@@ -376,11 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             // the target's place in these columns, -1 where it is elsewhere
             const long long at_tile = static_cast<long long>(y) - p.first - n0;
             const int at = y >= 0 && at_tile >= 0 && at_tile < width ? static_cast<int>(at_tile) : -1;
-            const bool any = __any_sync(0xffffffffu, at >= 0);
             float scale = 0.0f, lse2 = 0.0f;
             if constexpr (kGrad) {
                 if (live) {
-                    scale = p.scale[row];
+                    if (y >= 0 && y < p.vocab) scale = (each + (p.grad_loss ? p.grad_loss[row] : 0.0f)) / to_top * p.top;
                     lse2 = p.lse[row] * kLog2e;
                 }
             }
@@ -393,13 +428,14 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 acc.next();
             }
             if (!ok) break;
+            const bool any = __any_sync(0xffffffffu, at >= 0);
             if constexpr (kGrad) {
                 T* dst = static_cast<T*>(p.d) + row * p.ldd + n0;
 #pragma unroll
                 for (int c = 0; c < kHalf / kChunk; ++c) {
                     if (c * kChunk >= width) continue;
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) z[c][i] = ptx::ex2_approx(fmaf(z[c][i], kLog2e, -lse2));
+                    for (int i = 0; i < kChunk; ++i) z[c][i] = ptx::ex2_approx_ftz(fmaf(z[c][i], kLog2e, -lse2));
                     if (any) {
 #pragma unroll
                         for (int i = 0; i < kChunk; ++i) z[c][i] -= c * kChunk + i == at ? 1.0f : 0.0f;
@@ -431,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 for (int c = 0; c < kHalf / kChunk; ++c) {
                     if (c * kChunk >= hw) continue;
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) most[i & 3] = fmaxf(most[i & 3], z[c][i]);
+                    for (int i = 0; i < kChunk; i += 2) most[i / 2 & 3] = fmaxf(most[i / 2 & 3], fmaxf(z[c][i], z[c][i + 1]));
                 }
                 const float m2 = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * kLog2e;
                 const float base = m2 == -INFINITY ? 0.0f : m2;   // (nothing but -inf, or no column: s = 0)
@@ -439,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 for (int c = 0; c < kHalf / kChunk; ++c) {
                     if (c * kChunk >= hw) continue;
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) sum[i & 3] += ptx::ex2_approx(fmaf(z[c][i], kLog2e, -base));
+                    for (int i = 0; i < kChunk; ++i) sum[i & 3] += ptx::ex2_approx_ftz(fmaf(z[c][i], kLog2e, -base));
                 }
                 if (live) p.part[static_cast<size_t>(2 * n + half) * p.tokens + row] = make_float2(m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
             }

@@ -37,9 +37,9 @@ struct Product {
     void* out;
     long long ldo;
     int type;
-    int vec;                  // rows of out start on 32 bytes
+    int vec;                  // bytes that rows of out start on: 32, 16, or fewer (0)
     float beta;
-    const float* sum;         // fp32 sums of the pieces before, or nullptr (rows start on 32 bytes)
+    const float* sum;         // fp32 sums of the pieces before, or nullptr
     long long ld_sum;
 };
 
@@ -58,9 +58,9 @@ struct Products {
 
 constexpr int kStageK = 128;                       // k a stage: two atoms of 64
 constexpr int kPartStages = 64;                    // 8192 k
-constexpr int kStagePad = kChunk + 1;
-constexpr int kTurnBytes = kRowWarps * 32 * kStagePad * static_cast<int>(sizeof(float));
-constexpr int kProductSmem = Shape<true>::kStages * Shape<true>::kStageBytes + 1024 + 512 + kTurnBytes;
+constexpr int kTurnPad = kChunk + 1;
+constexpr int kTurnFloats = 32 * kTurnPad;         // a row warp's
+constexpr int kProductSmem = Shape<true>::kSmemBytes + kRowWarps * kTurnFloats * static_cast<int>(sizeof(float));
 constexpr int kPartialFloats = 2 * kRowWarps * kHalf * 32;   // a unit's
 
 struct Unit {
@@ -108,56 +108,102 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ int first_stage(const Product& q, int split) {
-    return static_cast<int>(static_cast<long long>(q.num_kb) * split / q.splits);
+// A field of the unit's product, both products' read at places known to the
+// compiler (an index into the parameters would make each a load with a latency).
+#define TCG_OF(p, v, field) ((v).which == 0 ? (p).q[0].field : (p).q[1].field)
+
+// Stages [kb0, kb1) of a unit, and where its tile starts in units of tiles.
+struct Span {
+    int kb0, kb1, m, n;
+};
+__device__ __forceinline__ Span span_of(const Products& p, const Unit& v) {
+    const int num_kb = TCG_OF(p, v, num_kb), splits = TCG_OF(p, v, splits), num_n = TCG_OF(p, v, num_n);
+    Span s;
+    s.kb0 = splits == 1 ? 0 : static_cast<int>(static_cast<long long>(num_kb) * v.split / splits);
+    s.kb1 = splits == 1 ? num_kb : static_cast<int>(static_cast<long long>(num_kb) * (v.split + 1) / splits);
+    s.m = v.tile / num_n;
+    s.n = v.tile - s.m * num_n;
+    return s;
 }
 
-template <typename T>
-__device__ __forceinline__ float old_value(const void* out, long long at) { return to_float(static_cast<const T*>(out)[at]); }
+// Where a warp's rows go: row0 + lane, columns [n0, n0 + width).
+struct Target {
+    int row0, rows, n0, width, N;   // rows: M - row0
+    long long ldo, ld_sum;
+    float beta, back;
+    const float* sum;
+    int vec;                        // bytes that rows of out start on: 32, 16, or fewer (0)
+};
 
-// 16 neighbouring values of a row that starts on 32 bytes.
-__device__ __forceinline__ void add_old(const Product& q, long long at, float (&v)[kChunk]) {
-    if (q.type == kOutF32) {
+// The rows as type O, times back: a lane its row, 16 columns at a time in words
+// of 32 or 16 bytes.  (Through shared memory and TMA, a box of 128 bytes a row at
+// a time, it took longer: each box waits for the one before to be read, 1400
+// cycles.  dW of 64 x 32768 x 4096: 145 us with dz, 133 this way.)
+template <typename O>
+__device__ __forceinline__ void store_rows(const Target& o, O* out, int lane, float (&z)[kHalf / kChunk][kChunk]) {
+    constexpr int kWords = kChunk * static_cast<int>(sizeof(O)) / 4;
+    if (lane >= o.rows) return;
+    O* row = out + (o.row0 + lane) * o.ldo + o.n0;
 #pragma unroll
-        for (int i = 0; i < kChunk; i += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(static_cast<const float*>(q.out) + at + i);
-            v[i] = fmaf(q.beta, o.x, v[i]), v[i + 1] = fmaf(q.beta, o.y, v[i + 1]);
-            v[i + 2] = fmaf(q.beta, o.z, v[i + 2]), v[i + 3] = fmaf(q.beta, o.w, v[i + 3]);
+    for (int c = 0; c < kHalf / kChunk; ++c) {
+        if (c * kChunk >= o.width) continue;
+        uint32_t w[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(O) == 4) w[i] = __float_as_uint(z[c][i] * o.back);
+            else w[i] = pack_pair<O>(z[c][2 * i] * o.back, z[c][2 * i + 1] * o.back);
         }
-    } else {
+        uint8_t* dst = reinterpret_cast<uint8_t*>(row + c * kChunk);
+        if (o.vec == 32) {
 #pragma unroll
-        for (int i = 0; i < kChunk; i += 8) {
-            float o[8];
-            if (q.type == kOutF16) values_of<__half>(load_raw8(static_cast<const __half*>(q.out) + at + i), o);
-            else values_of<__nv_bfloat16>(load_raw8(static_cast<const __nv_bfloat16*>(q.out) + at + i), o);
+            for (int h = 0; h < kWords; h += 8) {
+                const uint32_t q[8] = {w[h], w[h + 1], w[h + 2], w[h + 3], w[h + 4], w[h + 5], w[h + 6], w[h + 7]};
+                ptx::st_global_v8(dst + 4 * h, q);
+            }
+        } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[i + k] = fmaf(q.beta, o[k], v[i + k]);
+            for (int h = 0; h < kWords; h += 4) *reinterpret_cast<uint4*>(dst + 4 * h) = make_uint4(w[h], w[h + 1], w[h + 2], w[h + 3]);
         }
     }
 }
-__device__ __forceinline__ void store16(const Product& q, long long at, const float (&v)[kChunk]) {
-    uint32_t w[8];
-    if (q.type == kOutF32) {
+
+// The same with what was there and the sums of the pieces before, or to rows
+// that start anywhere or end within 16 columns: 16 columns at a time are turned in
+// shared memory, so that 16 lanes have a row's.  (One copy of the code: z moves
+// up instead.)
+template <typename O>
+__device__ __forceinline__ void add_rows(const Target& o, O* out, float* turn, int lane, float (&z)[kHalf / kChunk][kChunk]) {
+#pragma unroll 1
+    for (int c = 0; c * kChunk < o.width; ++c) {
+        __syncwarp();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int i = 0; i < kChunk; ++i) turn[lane * kTurnPad + i] = z[0][i] * o.back;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
-            ptx::st_global_v8(static_cast<float*>(q.out) + at + 8 * h, w);
+        for (int k = 0; k + 1 < kHalf / kChunk; ++k)
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) z[k][i] = z[k + 1][i];
+        __syncwarp();
+        const int col = o.n0 + c * kChunk + (lane & 15);
+        if (col >= o.N) continue;
+        const int r0 = lane >> 4;
+        O* dst = out + (o.row0 + r0) * o.ldo + col;
+        const float* sum = o.sum ? o.sum + (o.row0 + r0) * o.ld_sum + col : nullptr;
+#pragma unroll 4
+        for (int r = r0; r < 32; r += 2) {
+            if (r >= o.rows) break;
+            float y = turn[r * kTurnPad + (lane & 15)];
+            const long long step = r - r0;
+            if (sum) y += sum[step * o.ld_sum];
+            if (o.beta != 0.0f) y = fmaf(o.beta, to_float(dst[step * o.ldo]), y);
+            dst[step * o.ldo] = from_float<O>(y);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i] = q.type == kOutF16 ? pack_pair<__half>(v[2 * i], v[2 * i + 1]) : pack_pair<__nv_bfloat16>(v[2 * i], v[2 * i + 1]);
-        ptx::st_global_v8(static_cast<uint16_t*>(q.out) + at, w);
     }
 }
-__device__ __forceinline__ void store1(const Product& q, long long at, float v) {
-    if (q.type == kOutF32) static_cast<float*>(q.out)[at] = v;
-    else if (q.type == kOutF16) static_cast<__half*>(q.out)[at] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16*>(q.out)[at] = __float2bfloat16_rn(v);
-}
-__device__ __forceinline__ float load1(const Product& q, long long at) {
-    return q.type == kOutF32 ? old_value<float>(q.out, at) : q.type == kOutF16 ? old_value<__half>(q.out, at) : old_value<__nv_bfloat16>(q.out, at);
+
+template <typename O>
+__device__ __forceinline__ void write_rows(const Target& o, void* out, float* turn, int lane, float (&z)[kHalf / kChunk][kChunk]) {
+    if (!o.sum && o.beta == 0.0f && o.vec >= 16 && o.width % kChunk == 0) store_rows<O>(o, static_cast<O*>(out), lane, z);
+    else add_rows<O>(o, static_cast<O*>(out), turn, lane, z);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_constant__ Products p) {
@@ -165,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Ctl* ctl = reinterpret_cast<Ctl*>(smem + S::kStages * S::kStageBytes);
-    float* turn = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes + 512);
+    float* turn = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes + kCtlBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_ctarank();
     const bool leader = rank == 0;
@@ -207,11 +253,11 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         bool ok = true, first = true;
         while (ok && walk.next(p, v)) {
-            const Product& q = p.q[v.which];
-            const int m0 = v.tile / q.num_n * S::kTileM + static_cast<int>(rank) * kBM;
-            const int n0 = v.tile % q.num_n * p.tile_n + static_cast<int>(rank) * b_cols;
-            const int kb1 = first_stage(q, v.split + 1);
-            for (int kb = first_stage(q, v.split); kb < kb1; ++kb) {
+            const Span at = span_of(p, v);
+            const bool along_m = TCG_OF(p, v, a_along_m) != 0;
+            const CUtensorMap *ma = v.which == 0 ? &p.q[0].a : &p.q[1].a, *mb = v.which == 0 ? &p.q[0].b : &p.q[1].b;
+            const int m0 = at.m * S::kTileM + static_cast<int>(rank) * kBM, n0 = at.n * p.tile_n + static_cast<int>(rank) * b_cols;
+            for (int kb = at.kb0; kb < at.kb1; ++kb) {
                 if (!wait(&ctl->empty[stage], phase ^ 1u, p, ctl, 21)) { ok = false; break; }
                 const bool skip = first && p.fault_inject == 1 && blockIdx.x == 0;
                 first = false;
@@ -225,9 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                     // boxes of 64 elements (128 bytes; x counts bytes) by 128 rows
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int along = q.a_along_m ? m0 + 64 * i : k0 + 64 * i;
-                        ptx::tma_load_2d_pair(sA + i * kStageK * kRowBytes, &q.a, fbc, 2 * along, q.a_along_m ? k0 : m0);
-                        if (64 * i < b_cols) ptx::tma_load_2d_pair(sB + i * kStageK * kRowBytes, &q.b, fbc, 2 * (n0 + 64 * i), k0);
+                        const int along = along_m ? m0 + 64 * i : k0 + 64 * i;
+                        ptx::tma_load_2d_pair(sA + i * kStageK * kRowBytes, ma, fbc, 2 * along, along_m ? k0 : m0);
+                        if (64 * i < b_cols) ptx::tma_load_2d_pair(sB + i * kStageK * kRowBytes, mb, fbc, 2 * (n0 + 64 * i), k0);
                     }
                 }
                 if (!skip) {
@@ -252,16 +298,16 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
             Ring acc;
             bool ok = true, issued = false;
             while (ok && walk.next(p, v)) {
-                const Product& q = p.q[v.which];
+                const Span of = span_of(p, v);
+                const uint32_t along_m = static_cast<uint32_t>(TCG_OF(p, v, a_along_m));
                 // bits 15 and 16: M and N contiguous in shared memory
-                const uint32_t idesc = (1u << 4) | (p.fmt << 7) | (p.fmt << 10) | (static_cast<uint32_t>(q.a_along_m) << 15) | (1u << 16) |
+                const uint32_t idesc = (1u << 4) | (p.fmt << 7) | (p.fmt << 10) | (along_m << 15) | (1u << 16) |
                                        (static_cast<uint32_t>(p.tile_n >> 3) << 17) | (static_cast<uint32_t>(S::kTileM >> 4) << 24);
-                const int kb1 = first_stage(q, v.split + 1);
-                for (int kb0 = first_stage(q, v.split); ok && kb0 < kb1; kb0 += kPartStages) {
+                for (int kb0 = of.kb0; ok && kb0 < of.kb1; kb0 += kPartStages) {
                     if (!wait(&ctl->tmem_empty[acc.at], acc.phase ^ 1u, p, ctl, 22)) { ok = false; break; }
                     ptx::tc_fence_after_sync();
                     const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc.at * kAccCols);
-                    const int end = min(kb1, kb0 + kPartStages);
+                    const int end = min(of.kb1, kb0 + kPartStages);
                     for (int kb = kb0; kb < end; ++kb) {
                         if (!wait(&ctl->full[stage], phase, p, ctl, 23)) { ok = false; break; }
                         ptx::tc_fence_after_sync();
@@ -269,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                             const uint32_t sA = ptx::smem_u32(smem + stage * S::kStageBytes);
                             // K contiguous: 8-row groups 1024 bytes apart, 16 k are 32 bytes on; else runs of 64
                             // elements 16 KiB apart, 8-row groups of K 1024 bytes apart, 16 k are 2 KiB on
-                            const uint64_t a_desc = ptx::smem_desc_sw128(sA, q.a_along_m ? kStageK * kRowBytes : 16, 1024);
+                            const uint64_t a_desc = ptx::smem_desc_sw128(sA, along_m ? kStageK * kRowBytes : 16, 1024);
                             const uint64_t b_desc = ptx::smem_desc_sw128(sA + S::kABytes, kStageK * kRowBytes, 1024);
 #pragma unroll
                             for (int k = 0; k < kStageK / 16; ++k) {
-                                const uint32_t a_off = q.a_along_m ? k * 16 * kRowBytes : (k / 4) * kBM * kRowBytes + (k % 4) * 32;
+                                const uint32_t a_off = along_m ? k * 16 * kRowBytes : (k / 4) * kBM * kRowBytes + (k % 4) * 32;
                                 ptx::mma_f16_pair(d_tmem, a_desc + (a_off >> 4), b_desc + static_cast<uint32_t>((k * 16 * kRowBytes) >> 4), idesc,
                                                   (kb > kb0 || k > 0) ? 1u : 0u);
                             }
@@ -298,15 +344,15 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         // ------------------------------------------------------ rows to memory
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
         const int g = warp & 3, rw = warp - kControlWarps, half = rw >> 2, hw = p.tile_n / 2;
-        turn += rw * 32 * kStagePad;
-        const float back = *p.back;
+        turn += rw * kTurnFloats;
+        const float back = p.back ? *p.back : 1.0f;
         Ring acc;
         bool ok = true;
         while (ok && walk.next(p, v)) {
-            const Product& q = p.q[v.which];
-            const int row0 = v.tile / q.num_n * S::kTileM + static_cast<int>(rank) * kBM + g * 32, row = row0 + lane;
-            const int n0 = v.tile % q.num_n * p.tile_n + half * hw, width = max(0, min(hw, q.N - n0));
-            const int kb0 = first_stage(q, v.split), kb1 = first_stage(q, v.split + 1);
+            const Span of = span_of(p, v);
+            const int kb0 = of.kb0, kb1 = of.kb1, row0 = of.m * S::kTileM + static_cast<int>(rank) * kBM + g * 32;
+            const int n0 = of.n * p.tile_n + half * hw, N = TCG_OF(p, v, N), width = max(0, min(hw, N - n0));
+            const int splits = TCG_OF(p, v, splits);
             float z[kHalf / kChunk][kChunk];
             if (kb0 == kb1) {   // a sum over no tokens
 #pragma unroll
@@ -322,11 +368,13 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                 acc.next();
             }
             if (!ok) break;
-            if (q.splits > 1) {
+            const int M = TCG_OF(p, v, M), type = TCG_OF(p, v, type);
+            if (row0 >= M) continue;
+            if (splits > 1) {
                 // this warp's place among the unit's partial sums
                 const int mine = static_cast<int>(rank) * kRowWarps + rw;
                 auto place = [&](int split) {
-                    const size_t unit = static_cast<size_t>(split) * (q.num_m * q.num_n) + v.tile;
+                    const size_t unit = static_cast<size_t>(split) * (p.q[0].num_m * p.q[0].num_n) + v.tile;   // (only dX's are split)
                     return p.partials + unit * kPartialFloats + static_cast<size_t>(mine) * (kHalf * 32) + lane;
                 };
                 float* dst = place(v.split);
@@ -342,10 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                 int before = 0;
                 if (lane == 0) before = ptx::atomic_add_acq_rel_gpu(counter, 1);
                 before = __shfl_sync(0xffffffffu, before, 0);
-                if (before != q.splits - 1) continue;
+                if (before != splits - 1) continue;
                 __threadfence();
                 if (lane == 0) *counter = 0;
-                for (int s = 0; s < q.splits; ++s) {
+                for (int s = 0; s < splits; ++s) {
                     const float* src = place(s);
 #pragma unroll
                     for (int c = 0; c < kHalf / kChunk; ++c) {
@@ -358,44 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
                     }
                 }
             }
-            if (row0 >= q.M) continue;
-#pragma unroll
-            for (int c = 0; c < kHalf / kChunk; ++c) {
-                if (c * kChunk >= width) continue;
-                float (&x)[kChunk] = z[c];
-#pragma unroll
-                for (int i = 0; i < kChunk; ++i) x[i] *= back;
-                const int col = n0 + c * kChunk;
-                if (q.vec && col + kChunk <= q.N) {
-                    if (row < q.M) {
-                        if (q.sum) {
-#pragma unroll
-                            for (int i = 0; i < kChunk; i += 4) {
-                                const float4 o = *reinterpret_cast<const float4*>(q.sum + row * q.ld_sum + col + i);
-                                x[i] += o.x, x[i + 1] += o.y, x[i + 2] += o.z, x[i + 3] += o.w;
-                            }
-                        }
-                        const long long at = row * q.ldo + col;
-                        if (q.beta != 0.0f) add_old(q, at, x);
-                        store16(q, at, x);
-                    }
-                } else {
-                    // turned in shared memory: 16 lanes have a row's 16 columns
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < kChunk; ++i) turn[lane * kStagePad + i] = x[i];
-                    __syncwarp();
-                    const int own = col + (lane & 15);
-                    for (int r = lane >> 4; r < 32; r += 2) {
-                        if (row0 + r >= q.M || own >= q.N) continue;
-                        float y = turn[r * kStagePad + (lane & 15)];
-                        const long long at = (row0 + r) * q.ldo + own;
-                        if (q.sum) y += q.sum[(row0 + r) * q.ld_sum + own];
-                        if (q.beta != 0.0f) y = fmaf(q.beta, load1(q, at), y);
-                        store1(q, at, y);
-                    }
-                }
-            }
+            const Target o = {row0, M - row0, n0, width, N, TCG_OF(p, v, ldo), TCG_OF(p, v, ld_sum), TCG_OF(p, v, beta), back,
+                              TCG_OF(p, v, sum), TCG_OF(p, v, vec)};
+            void* out = TCG_OF(p, v, out);
+            if (type == kOutF32) write_rows<float>(o, out, turn, lane, z);
+            else if (type == kOutF16) write_rows<__half>(o, out, turn, lane, z);
+            else write_rows<__nv_bfloat16>(o, out, turn, lane, z);
         }
     }
 
@@ -407,6 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_
         ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
     }
 }
+
+#undef TCG_OF
 
 }  // namespace xent
 }  // namespace tcg
