@@ -135,23 +135,46 @@ struct Target {
     int vec;                        // bytes that rows of out start on: 32, 16, or fewer (0)
 };
 
-// The rows as type O, times back: a lane its row, 16 columns at a time in words
-// of 32 or 16 bytes.  (Through shared memory and TMA, a box of 128 bytes a row at
-// a time, it took longer: each box waits for the one before to be read, 1400
-// cycles.  dW of 64 x 32768 x 4096: 145 us with dz, 133 this way.)
-template <typename O>
+// The whole chunks of 16 columns as type O, times back: a lane its row, in words
+// of 32 or 16 bytes.  kMore: plus what was there and the sums of the pieces
+// before.  (Through shared memory and TMA, a box of 128 bytes a row at a time, it
+// took longer: each box waits for the one before to be read, 1400 cycles.  dW of
+// 64 x 32768 x 4096: 145 us with dz, 133 this way.)
+template <typename O, bool kMore>
 __device__ __forceinline__ void store_rows(const Target& o, O* out, int lane, float (&z)[kHalf / kChunk][kChunk]) {
     constexpr int kWords = kChunk * static_cast<int>(sizeof(O)) / 4;
     if (lane >= o.rows) return;
     O* row = out + (o.row0 + lane) * o.ldo + o.n0;
+    const float* sum = kMore && o.sum ? o.sum + (o.row0 + lane) * o.ld_sum + o.n0 : nullptr;
 #pragma unroll
     for (int c = 0; c < kHalf / kChunk; ++c) {
-        if (c * kChunk >= o.width) continue;
+        if ((c + 1) * kChunk > o.width) continue;
+        float x[kChunk];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) x[i] = z[c][i] * o.back;
+        if constexpr (kMore) {
+            if (sum) {
+#pragma unroll
+                for (int i = 0; i < kChunk; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(sum + c * kChunk + i);
+                    x[i] += f.x, x[i + 1] += f.y, x[i + 2] += f.z, x[i + 3] += f.w;
+                }
+            }
+            if (o.beta != 0.0f) {
+#pragma unroll
+                for (int i = 0; i < kChunk; i += 8) {
+                    float f[8];
+                    values_of<O>(load_raw8(row + c * kChunk + i), f);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[i + k] = fmaf(o.beta, f[k], x[i + k]);
+                }
+            }
+        }
         uint32_t w[kWords];
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
-            if constexpr (sizeof(O) == 4) w[i] = __float_as_uint(z[c][i] * o.back);
-            else w[i] = pack_pair<O>(z[c][2 * i] * o.back, z[c][2 * i + 1] * o.back);
+            if constexpr (sizeof(O) == 4) w[i] = __float_as_uint(x[i]);
+            else w[i] = pack_pair<O>(x[2 * i], x[2 * i + 1]);
         }
         uint8_t* dst = reinterpret_cast<uint8_t*>(row + c * kChunk);
         if (o.vec == 32) {
@@ -167,43 +190,50 @@ __device__ __forceinline__ void store_rows(const Target& o, O* out, int lane, fl
     }
 }
 
-// The same with what was there and the sums of the pieces before, or to rows
-// that start anywhere or end within 16 columns: 16 columns at a time are turned in
-// shared memory, so that 16 lanes have a row's.  (One copy of the code: z moves
-// up instead.)
+// Chunks from `first` on to rows that start anywhere, or that end inside one:
+// turned in shared memory, so that 16 lanes have a row's 16 columns.  (One copy of
+// the code: z moves up instead.)
 template <typename O>
-__device__ __forceinline__ void add_rows(const Target& o, O* out, float* turn, int lane, float (&z)[kHalf / kChunk][kChunk]) {
+__device__ __forceinline__ void turn_rows(const Target& o, O* out, float* turn, int lane, int first, float (&z)[kHalf / kChunk][kChunk]) {
 #pragma unroll 1
     for (int c = 0; c * kChunk < o.width; ++c) {
-        __syncwarp();
+        if (c >= first) {
+            __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) turn[lane * kTurnPad + i] = z[0][i] * o.back;
+            for (int i = 0; i < kChunk; ++i) turn[lane * kTurnPad + i] = z[0][i] * o.back;
+            __syncwarp();
+            const int col = o.n0 + c * kChunk + (lane & 15), r0 = lane >> 4;
+            if (col < o.N) {
+                O* dst = out + (o.row0 + r0) * o.ldo + col;
+                const float* sum = o.sum ? o.sum + (o.row0 + r0) * o.ld_sum + col : nullptr;
+#pragma unroll 4
+                for (int r = r0; r < 32; r += 2) {
+                    if (r >= o.rows) break;
+                    float y = turn[r * kTurnPad + (lane & 15)];
+                    const long long step = r - r0;
+                    if (sum) y += sum[step * o.ld_sum];
+                    if (o.beta != 0.0f) y = fmaf(o.beta, to_float(dst[step * o.ldo]), y);
+                    dst[step * o.ldo] = from_float<O>(y);
+                }
+            }
+        }
 #pragma unroll
         for (int k = 0; k + 1 < kHalf / kChunk; ++k)
 #pragma unroll
             for (int i = 0; i < kChunk; ++i) z[k][i] = z[k + 1][i];
-        __syncwarp();
-        const int col = o.n0 + c * kChunk + (lane & 15);
-        if (col >= o.N) continue;
-        const int r0 = lane >> 4;
-        O* dst = out + (o.row0 + r0) * o.ldo + col;
-        const float* sum = o.sum ? o.sum + (o.row0 + r0) * o.ld_sum + col : nullptr;
-#pragma unroll 4
-        for (int r = r0; r < 32; r += 2) {
-            if (r >= o.rows) break;
-            float y = turn[r * kTurnPad + (lane & 15)];
-            const long long step = r - r0;
-            if (sum) y += sum[step * o.ld_sum];
-            if (o.beta != 0.0f) y = fmaf(o.beta, to_float(dst[step * o.ldo]), y);
-            dst[step * o.ldo] = from_float<O>(y);
-        }
     }
 }
 
 template <typename O>
 __device__ __forceinline__ void write_rows(const Target& o, void* out, float* turn, int lane, float (&z)[kHalf / kChunk][kChunk]) {
-    if (!o.sum && o.beta == 0.0f && o.vec >= 16 && o.width % kChunk == 0) store_rows<O>(o, static_cast<O*>(out), lane, z);
-    else add_rows<O>(o, static_cast<O*>(out), turn, lane, z);
+    int first = 0;
+    if (o.vec >= 16) {
+        if (o.sum || o.beta != 0.0f) store_rows<O, true>(o, static_cast<O*>(out), lane, z);
+        else store_rows<O, false>(o, static_cast<O*>(out), lane, z);
+        first = o.width / kChunk;
+        if (first * kChunk == o.width) return;
+    }
+    turn_rows<O>(o, static_cast<O*>(out), turn, lane, first, z);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) xent_product_kernel(const __grid_constant__ Products p) {
