@@ -660,7 +660,7 @@ tcg_status tcg_moe_sort(int tokens, int experts, int k, const int* topk, int ld_
  * every assignment.  Entries of row_of outside [0, rows) are skipped; rows of
  * out that none names are left as they were, and one that several name holds
  * one of them.  Its gradient is tcg_moe_combine without weights.  cols <=
- * 65535 * 4096 here and below.  Outputs must not overlap inputs.
+ * 65535 * 4096 - 8 here and below.  Outputs must not overlap inputs.
  */
 tcg_status tcg_moe_dispatch(int tokens, int k, int cols, int rows, const void* x, int ldx, tcg_dtype x_dtype,
                             const int* row_of, int ld_row_of, void* out, int ldo, tcg_dtype out_dtype, void* stream);

@@ -204,7 +204,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
 
 constexpr int kMoveThreads = 256;
 constexpr int kSteps = 2;          // eight columns each that a thread has on its way
-constexpr int kMaxCols = 65535 * kMoveThreads * 8 * kSteps;   // a grid's second extent
+// CTAs of the gradient that an SM is to hold, which bounds their registers: five
+// where whole words of 16-bit values and at most two assignments are on their way
+// (16384 x 2 rows of 4096: 106 us with four), as it comes elsewhere.  (Combine
+// itself, held to as many, spills: 82 us in place of 70.)
+template <bool kWhole, typename TX, typename TY, int kJ>
+constexpr int resident() { return kWhole && sizeof(TX) == 2 && sizeof(TY) == 2 && kJ <= 2 ? 5 : 2; }
+constexpr int kMaxCols = 65535 * kMoveThreads * 8 * kSteps - 8;   // a grid's second extent
 
 struct Rows {
     const void* y;      // tokens' side: read by dispatch and the gradient, written by combine
@@ -220,32 +226,34 @@ struct Rows {
     long long ld_weights;
     float* dweights;
     long long ld_dweights;
-    int vec_in, vec_out, vec_y;   // eight values of x, out and y may be moved as whole words
     int lanes;          // threads a token
 };
 
-// Where this thread works: its token and its first eight columns.
+// Eight neighbouring columns are a thread's at a time.  kWhole: all rows start on
+// 16 bytes.  Otherwise a thread's eight lie between the 16-byte boundaries of the
+// row that is written, and what is read is shifted into place.  Those at a row's
+// ends go one by one.
+
+// Where this thread works: its token and its first group of eight columns.
 struct Place {
     long long t;
-    int c0, step;
+    int g0;
 };
 __device__ __forceinline__ Place place_of(const Rows& p) {
-    Place w;
     const int slot = threadIdx.x / p.lanes;
-    w.t = static_cast<long long>(blockIdx.x) * (kMoveThreads / p.lanes) + slot;
-    w.c0 = (static_cast<int>(blockIdx.y) * p.lanes * kSteps + static_cast<int>(threadIdx.x) - slot * p.lanes) * 8;
-    w.step = p.lanes * 8;
-    return w;
+    return {static_cast<long long>(blockIdx.x) * (kMoveThreads / p.lanes) + slot,
+            static_cast<int>(blockIdx.y) * p.lanes * kSteps + static_cast<int>(threadIdx.x) - slot * p.lanes};
 }
 
-template <typename T>
-__device__ __forceinline__ Raw8<T> fetch(const T* row, int c, int cols, int vec) {
-    return vec && c + 8 <= cols ? load_raw8<T, true>(row + c) : load_some8<T>(row + c, cols - c);
-}
-template <typename T>
-__device__ __forceinline__ void put(T* row, int c, int cols, int vec, const Raw8<T>& v) {
-    if (vec && c + 8 <= cols) store_raw8<T>(row + c, v);
-    else store_some8<T>(row + c, v, cols - c);
+// The first column of group g of a row that is written: at or before it.
+template <bool kWhole, typename T>
+__device__ __forceinline__ int column_of(const T* row, int g) { return kWhole ? 8 * g : 8 * g - past16(row); }
+
+template <bool kWhole, typename T>
+__device__ __forceinline__ Raw8<T> fetch(const T* row, int c, int cols) {
+    if constexpr (kWhole)
+        if (c + 8 <= cols) return load_raw8<T, true>(row + c);
+    return load_any8<T>(row, c, cols);
 }
 
 // The row of an assignment, -1 where it has none.
@@ -254,24 +262,29 @@ __device__ __forceinline__ int row_at(const Rows& p, long long t, int j) {
     return r >= 0 && r < p.rows ? r : -1;
 }
 
-template <typename TY, typename TX>
+template <typename TX, typename TY>
+__device__ __forceinline__ Raw8<TX> as_type(const Raw8<TY>& r) {
+    if constexpr (std::is_same<TX, TY>::value) {
+        return r;
+    } else {
+        float f[8];
+        values_of<TY>(r, f);
+        return raw_of<TX>(f);
+    }
+}
+
+template <bool kWhole, typename TY, typename TX>
 __global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const __grid_constant__ Rows p) {
     tcg::host::wait_for_kernel_ahead();
     const Place w = place_of(p);
     if (w.t >= p.tokens) return;
     const TY* src = static_cast<const TY*>(p.y) + w.t * p.ldy;
     Raw8<TX> v[kSteps];
+    if constexpr (kWhole) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int c = w.c0 + s * w.step;
-        if (c >= p.cols) break;
-        const Raw8<TY> r = fetch<TY>(src, c, p.cols, p.vec_y);
-        if constexpr (std::is_same<TX, TY>::value) {
-            v[s] = r;
-        } else {
-            float f[8];
-            values_of<TY>(r, f);
-            v[s] = raw_of<TX>(f);
+        for (int s = 0; s < kSteps; ++s) {
+            const int c = 8 * (w.g0 + s * p.lanes);
+            if (c < p.cols) v[s] = as_type<TX, TY>(fetch<true, TY>(src, c, p.cols));
         }
     }
     for (int j = 0; j < p.k; ++j) {
@@ -280,18 +293,24 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const __grid_con
         TX* dst = static_cast<TX*>(p.out) + r * p.ldo;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int c = w.c0 + s * w.step;
-            if (c < p.cols) put<TX>(dst, c, p.cols, p.vec_out, v[s]);
+            const int c = column_of<kWhole>(dst, w.g0 + s * p.lanes);
+            if (c >= p.cols) continue;
+            if constexpr (!kWhole) v[s] = as_type<TX, TY>(fetch<false, TY>(src, c, p.cols));   // (from the L1 after the first)
+            store_any8<TX>(dst, c, p.cols, v[s]);
         }
     }
 }
 
 // kJ assignments' rows are on their way at once; sums in the order of j.
-template <typename TX, typename TY, int kJ>
+template <bool kWhole, typename TX, typename TY, int kJ>
 __global__ void __launch_bounds__(kMoveThreads) combine_kernel(const __grid_constant__ Rows p) {
     tcg::host::wait_for_kernel_ahead();
     const Place w = place_of(p);
     if (w.t >= p.tokens) return;
+    TY* dst = static_cast<TY*>(p.out) + w.t * p.ldo;
+    int col[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) col[s] = column_of<kWhole>(dst, w.g0 + s * p.lanes);
     float acc[kSteps][8];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
@@ -310,39 +329,35 @@ __global__ void __launch_bounds__(kMoveThreads) combine_kernel(const __grid_cons
         for (int q = 0; q < kJ; ++q)
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                const int c = w.c0 + s * w.step;
-                if (row[q] >= 0 && c < p.cols) v[q][s] = fetch<TX>(static_cast<const TX*>(p.x) + row[q] * p.ldx, c, p.cols, p.vec_in);
+                if (row[q] >= 0 && col[s] < p.cols) v[q][s] = fetch<kWhole, TX>(static_cast<const TX*>(p.x) + row[q] * p.ldx, col[s], p.cols);
             }
 #pragma unroll
         for (int q = 0; q < kJ; ++q)
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                if (row[q] < 0 || w.c0 + s * w.step >= p.cols) continue;
+                if (row[q] < 0 || col[s] >= p.cols) continue;
                 float f[8];
                 values_of<TX>(v[q][s], f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[s][i] = fmaf(wt[q], f[i], acc[s][i]);
             }
     }
-    TY* dst = static_cast<TY*>(p.out) + w.t * p.ldo;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int c = w.c0 + s * w.step;
-        if (c < p.cols) put<TY>(dst, c, p.cols, p.vec_out, raw_of<TY>(acc[s]));
-    }
+    for (int s = 0; s < kSteps; ++s)
+        if (col[s] < p.cols) store_any8<TY>(dst, col[s], p.cols, raw_of<TY>(acc[s]));
 }
 
 // p.lanes threads a token (a power of two from 32 on), over all its columns;
 // kJ assignments at a time, whose weights' gradients are summed in a fixed order.
-template <typename TX, typename TY, int kJ>
-__global__ void __launch_bounds__(kMoveThreads) combine_grad_kernel(const __grid_constant__ Rows p) {
+template <bool kWhole, typename TX, typename TY, int kJ>
+__global__ void __launch_bounds__(kMoveThreads, resident<kWhole, TX, TY, kJ>()) combine_grad_kernel(const __grid_constant__ Rows p) {
     tcg::host::wait_for_kernel_ahead();
     __shared__ float part[kJ][kMoveThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slot = threadIdx.x / p.lanes, per_cta = kMoveThreads / p.lanes, warps = p.lanes / 32;
     const long long t = static_cast<long long>(blockIdx.x) * per_cta + slot;
     const bool in = t < p.tokens;
-    const int first = (static_cast<int>(threadIdx.x) - slot * p.lanes) * 8, step = p.lanes * 8;
+    const int thread = static_cast<int>(threadIdx.x) - slot * p.lanes;
     const TY* dy = static_cast<const TY*>(p.y) + (in ? t : 0) * p.ldy;
     for (int j0 = 0; j0 < p.k; j0 += kJ) {
         int row[kJ];
@@ -354,18 +369,26 @@ __global__ void __launch_bounds__(kMoveThreads) combine_grad_kernel(const __grid
             dot[q] = 0.0f;
         }
         if (in) {
-            for (int c = first; c < p.cols; c += step) {
+            // (rows that start anywhere: a group more, each row's columns its own, dy from the L1 after the first)
+            const int groups = (p.cols + (kWhole ? 7 : 14)) / 8;
+            for (int g = thread; g < groups; g += p.lanes) {
                 Raw8<TX> v[kJ];
-                const Raw8<TY> g = fetch<TY>(dy, c, p.cols, p.vec_y);
+                Raw8<TY> r[kWhole ? 1 : kJ];
+                int col[kJ];
 #pragma unroll
-                for (int q = 0; q < kJ; ++q)
-                    if (row[q] >= 0 && p.dweights) v[q] = fetch<TX>(static_cast<const TX*>(p.x) + row[q] * p.ldx, c, p.cols, p.vec_in);
-                float d[8];
-                values_of<TY>(g, d);
+                for (int q = 0; q < kJ; ++q) col[q] = column_of<kWhole>(static_cast<TX*>(p.out) + row[q] * p.ldo, g);
+                if constexpr (kWhole) r[0] = fetch<true, TY>(dy, 8 * g, p.cols);
 #pragma unroll
                 for (int q = 0; q < kJ; ++q) {
-                    if (row[q] < 0) continue;
-                    float f[8];
+                    if (row[q] < 0 || col[q] >= p.cols) continue;
+                    if constexpr (!kWhole) r[q] = fetch<false, TY>(dy, col[q], p.cols);
+                    if (p.dweights) v[q] = fetch<kWhole, TX>(static_cast<const TX*>(p.x) + row[q] * p.ldx, col[q], p.cols);
+                }
+#pragma unroll
+                for (int q = 0; q < kJ; ++q) {
+                    if (row[q] < 0 || col[q] >= p.cols) continue;
+                    float d[8], f[8];
+                    values_of<TY>(r[kWhole ? 0 : q], d);
                     if (p.dweights) {
                         values_of<TX>(v[q], f);
 #pragma unroll
@@ -373,7 +396,7 @@ __global__ void __launch_bounds__(kMoveThreads) combine_grad_kernel(const __grid
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] = wt[q] * d[i];
-                    put<TX>(static_cast<TX*>(p.out) + row[q] * p.ldo, c, p.cols, p.vec_out, raw_of<TX>(f));
+                    store_any8<TX>(static_cast<TX*>(p.out) + row[q] * p.ldo, col[q], p.cols, raw_of<TX>(f));
                 }
             }
         }
@@ -385,7 +408,7 @@ __global__ void __launch_bounds__(kMoveThreads) combine_grad_kernel(const __grid
             if (lane == 0) part[q][warp] = dot[q];
         }
         __syncthreads();
-        if (in && first == 0) {
+        if (in && thread == 0) {
 #pragma unroll
             for (int q = 0; q < kJ; ++q) {
                 if (j0 + q >= p.k) continue;
@@ -439,10 +462,11 @@ int lanes_for(int cols, int steps) {
     while (lanes < want && lanes < kMoveThreads) lanes *= 2;
     return lanes;
 }
-dim3 move_grid(const Rows& p) {
+dim3 move_grid(const Rows& p, bool whole) {
+    // (a row that starts anywhere may take a group more)
     const int per_cta = kMoveThreads / p.lanes, span = p.lanes * 8 * kSteps;
     return dim3(static_cast<unsigned>((static_cast<long long>(p.tokens) + per_cta - 1) / per_cta),
-                static_cast<unsigned>((static_cast<long long>(p.cols) + span - 1) / span));
+                static_cast<unsigned>((static_cast<long long>(p.cols) + (whole ? 0 : 7) + span - 1) / span));
 }
 
 tcg_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch(what, e); }
@@ -518,14 +542,13 @@ tcg_status tcg_moe_dispatch(int tokens, int k, int cols, int rows, const void* x
     p.ldy = ldx;
     p.out = out;
     p.ldo = ldo;
-    p.vec_y = whole_words(x, ldx, x_dtype);
-    p.vec_out = whole_words(out, ldo, out_dtype);
+    const bool whole = whole_words(x, ldx, x_dtype) && whole_words(out, ldo, out_dtype);
     p.lanes = lanes_for(cols, kSteps);
     cudaError_t err = cudaSuccess;
     with_type(x_dtype, [&](auto y) {
         with_type(out_dtype, [&](auto o) {
-            err = tcg::host::launch_early(dispatch_kernel<decltype(y), decltype(o)>, move_grid(p), kMoveThreads,
-                                          static_cast<cudaStream_t>(stream), p);
+            const auto kernel = whole ? dispatch_kernel<true, decltype(y), decltype(o)> : dispatch_kernel<false, decltype(y), decltype(o)>;
+            err = tcg::host::launch_early(kernel, move_grid(p, whole), kMoveThreads, static_cast<cudaStream_t>(stream), p);
         });
     });
     return launched(err, "tcg_moe_dispatch");
@@ -549,18 +572,18 @@ tcg_status tcg_moe_combine(int tokens, int k, int cols, int rows, const void* x,
     p.ld_weights = ld_weights;
     p.out = y;
     p.ldo = ldy;
-    p.vec_in = whole_words(x, ldx, x_dtype);
-    p.vec_out = whole_words(y, ldy, y_dtype);
+    const bool whole = whole_words(x, ldx, x_dtype) && whole_words(y, ldy, y_dtype);
     p.lanes = lanes_for(cols, kSteps);
     cudaError_t err = cudaSuccess;
     with_type(x_dtype, [&](auto a) {
         with_type(y_dtype, [&](auto b) {
             const auto run = [&](auto* kernel) {
-                err = tcg::host::launch_early(kernel, move_grid(p), kMoveThreads, static_cast<cudaStream_t>(stream), p);
+                err = tcg::host::launch_early(kernel, move_grid(p, whole), kMoveThreads, static_cast<cudaStream_t>(stream), p);
             };
-            if (k == 1) run(combine_kernel<decltype(a), decltype(b), 1>);
-            else if (k == 2) run(combine_kernel<decltype(a), decltype(b), 2>);
-            else run(combine_kernel<decltype(a), decltype(b), 4>);
+            if (!whole) run(combine_kernel<false, decltype(a), decltype(b), 2>);
+            else if (k == 1) run(combine_kernel<true, decltype(a), decltype(b), 1>);
+            else if (k == 2) run(combine_kernel<true, decltype(a), decltype(b), 2>);
+            else run(combine_kernel<true, decltype(a), decltype(b), 4>);
         });
     });
     return launched(err, "tcg_moe_combine");
@@ -593,9 +616,7 @@ tcg_status tcg_moe_combine_backward(int tokens, int k, int cols, int rows, const
     p.ldo = lddx;
     p.dweights = dweights;
     p.ld_dweights = ld_dweights;
-    p.vec_in = whole_words(x, ldx, x_dtype);
-    p.vec_y = whole_words(dy, lddy, dy_dtype);
-    p.vec_out = whole_words(dx, lddx, x_dtype);
+    const bool whole = (!dweights || whole_words(x, ldx, x_dtype)) && whole_words(dy, lddy, dy_dtype) && whole_words(dx, lddx, x_dtype);
     p.lanes = lanes_for(cols, 4);
     const int per_cta = kMoveThreads / p.lanes;
     const dim3 grid(static_cast<unsigned>((static_cast<long long>(tokens) + per_cta - 1) / per_cta));
@@ -605,9 +626,10 @@ tcg_status tcg_moe_combine_backward(int tokens, int k, int cols, int rows, const
             const auto run = [&](auto* kernel) {
                 err = tcg::host::launch_early(kernel, grid, kMoveThreads, static_cast<cudaStream_t>(stream), p);
             };
-            if (k == 1) run(combine_grad_kernel<decltype(a), decltype(b), 1>);
-            else if (k == 2) run(combine_grad_kernel<decltype(a), decltype(b), 2>);
-            else run(combine_grad_kernel<decltype(a), decltype(b), 4>);
+            if (!whole) run(combine_grad_kernel<false, decltype(a), decltype(b), 2>);
+            else if (k == 1) run(combine_grad_kernel<true, decltype(a), decltype(b), 1>);
+            else if (k == 2) run(combine_grad_kernel<true, decltype(a), decltype(b), 2>);
+            else run(combine_grad_kernel<true, decltype(a), decltype(b), 4>);
         });
     });
     return launched(err, "tcg_moe_combine_backward");

@@ -70,27 +70,56 @@ __device__ __forceinline__ Raw8<T> load_raw8(const T* src) {
     return r;
 }
 
-// The first n of eight values, one by one (zeros after them).
+// Eight values of a row that starts anywhere, from element e0 on (which may lie
+// before the row, or so that some lie past its end: zeros there).  Whole 16-byte
+// words are loaded, each of them holding a value that is asked for, and shifted
+// into place.
 template <typename T>
-__device__ __forceinline__ Raw8<T> load_some8(const T* src, int n) {
-    Raw8<T> r;
-    T v[8];
+__device__ __forceinline__ Raw8<T> load_any8(const T* row, int e0, int cols) {
+    constexpr int kWords = 2 * static_cast<int>(sizeof(T));          // of four bytes
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row) + static_cast<long long>(e0) * static_cast<int>(sizeof(T));
+    const uintptr_t first = reinterpret_cast<uintptr_t>(row + max(e0, 0)), last = reinterpret_cast<uintptr_t>(row + min(e0 + 8, cols));
+    const uintptr_t base = at & ~static_cast<uintptr_t>(15);
+    const uint32_t off = static_cast<uint32_t>(at & 15);
+    uint32_t w[kWords + 4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? src[i] : from_float<T>(0.0f);
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            r.w[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                                __float_as_uint(v[4 * i + 3]));
-    } else {
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            u[i] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&v[2 * i])) |
-                   (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&v[2 * i + 1])) << 16);
-        r.w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    for (int i = 0; i <= kWords / 4; ++i) {
+        const uintptr_t b = base + 16 * i;
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if ((i < kWords / 4 || off) && b + 16 > first && b < last) q = *reinterpret_cast<const uint4*>(b);
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
     }
+    uint32_t o[kWords];
+    if (off) {
+        uint32_t u[kWords + 2], t[kWords + 1];
+#pragma unroll
+        for (int i = 0; i < kWords + 2; ++i) u[i] = off & 8u ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < kWords + 1; ++i) t[i] = off & 4u ? u[i + 1] : u[i];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) o[i] = sizeof(T) == 4 ? t[i] : __funnelshift_r(t[i], t[i + 1], (off & 2u) * 8u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) o[i] = w[i];
+    }
+    if (e0 < 0 || e0 + 8 > cols) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (e0 + i >= 0 && e0 + i < cols) continue;
+            if constexpr (sizeof(T) == 4) o[i] = 0u;
+            else o[i / 2] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+        }
+    }
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) r.w[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
     return r;
+}
+
+// Elements that a row's first value lies past a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ int past16(const T* row) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 }
 
 template <typename T>
@@ -131,19 +160,21 @@ __device__ __forceinline__ void store_raw8(T* dst, const Raw8<T>& r) {
     for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) __stcs(reinterpret_cast<uint4*>(dst) + i, r.w[i]);
 }
 
+// To elements e0 on of a row, those that lie in it; row + e0 starts on 16 bytes.
 template <typename T>
-__device__ __forceinline__ void store_some8(T* dst, const Raw8<T>& r, int n) {
-    if constexpr (sizeof(T) == 4) {
-        float x[8];
-        values_of<T>(r, x);
+__device__ __forceinline__ void store_any8(T* row, int e0, int cols, const Raw8<T>& r) {
+    if (e0 >= 0 && e0 + 8 <= cols) {
+        store_raw8<T>(row + e0, r);
+        return;
+    }
+    uint32_t u[2 * sizeof(T)];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) dst[i] = x[i];
-    } else {
-        const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[4 * i] = r.w[i].x, u[4 * i + 1] = r.w[i].y, u[4 * i + 2] = r.w[i].z, u[4 * i + 3] = r.w[i].w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) reinterpret_cast<uint16_t*>(dst)[i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
+    for (int i = 0; i < 8; ++i) {
+        if (e0 + i < 0 || e0 + i >= cols) continue;
+        if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(row)[e0 + i] = u[i];
+        else reinterpret_cast<uint16_t*>(row)[e0 + i] = static_cast<uint16_t>(u[i / 2] >> (16 * (i & 1)));
     }
 }
 
