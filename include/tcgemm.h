@@ -611,7 +611,8 @@ tcg_status tcg_moe_balance_backward(int tokens, int experts, int k, tcg_dtype dt
  * An expert whose logit is -inf is switched off: it is never chosen, and where
  * fewer than k are left, the last places hold -1 with weight 0.  So do all of a
  * token's with mask 0 (mask: one byte per token, NULL: all count), whatever its
- * logits hold.  A NaN counts as the largest and makes the token's weights NaN.
+ * logits hold.  A NaN counts as the largest; it, or +inf, makes the token's
+ * weights NaN.
  * k <= experts (else TCG_ERR_INVALID_ARG), k <= 32 and experts <= 1024 (else
  * TCG_ERR_UNSUPPORTED).
  */

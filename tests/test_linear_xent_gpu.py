@@ -190,6 +190,61 @@ def test_loss_scales(scale, dtype):
     c.check_backward(gx, gw, gm, gl)
 
 
+@pytest.mark.parametrize("T,V,H", [(70000, 300, 72), (33, 30000, 1032), (5000, 40, 2056)])
+def test_many_tokens_many_words_long_rows(T, V, H):
+    """More row tiles than CTAs, a long sum in few tiles of dX (split among CTAs), few words."""
+    c = Case(T, V, H, "bf16", ignored=0.1)
+    c.forward()
+    c.check_forward()
+    gm, gl = torch.ones(1, device="cuda"), torch.randn(T, device="cuda") / T
+    gx, gw = c.backward("bf16", "bf16", gm, gl)
+    c.check_backward(gx, gw, gm, gl)
+    again = c.backward("bf16", "bf16", gm, gl)
+    assert torch.equal(gx, again[0]) and torch.equal(gw, again[1])
+
+
+def test_weights_past_31_bits():
+    """W and dW whose elements reach past 2^31; the last words are looked at."""
+    T, V, H = 24, 270000, 8192
+    if torch.cuda.get_device_properties(0).total_memory < 64 << 30:
+        pytest.skip("needs 20 GB")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w = torch.empty(V, H, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, V, 30000):
+        w[a:a + 30000] = (torch.randn(min(30000, V - a), H, generator=g, device="cuda") * (2.0 / H ** 0.5)).to(torch.bfloat16)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    target = torch.randint(V - 100, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    lse, loss, mean = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty(1, device="cuda")
+    n = torch.empty(1, dtype=torch.int32, device="cuda")
+    size = tcg.linear_xent_workspace_size(T, V, H, True)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    tcg.linear_xent(T, V, H, "bf16", x, H, w, H, target, lse, loss, mean, n, workspace=ws, workspace_bytes=size)
+    z = torch.cat([x.double() @ w[a:a + 10000].double().t() for a in range(0, V, 10000)], 1)
+    ref = torch.logsumexp(z, 1)
+    S = float((x.double().abs() @ w[:4000].double().abs().t()).max()) * 1.1
+    err = (H / 16 + 3) * 2.0 ** -22 * S + 200 * U + U * ref.abs()
+    assert bool(((lse.double() - ref).abs() <= err).all())
+    dw = torch.full((V + 1, H), 5.0, dtype=torch.bfloat16, device="cuda")
+    dx = torch.empty_like(x)
+    gm = torch.ones(1, device="cuda")
+    tcg.linear_xent_backward(T, V, H, "bf16", x, H, w, H, target, lse, n, gm, None, dx, H, "bf16", 0.0, dw, H, "bf16", workspace=ws,
+                             workspace_bytes=size)
+    p = torch.exp(z - ref[:, None]) / T
+    p[torch.arange(T, device="cuda"), target.long()] -= 1.0 / T
+    for rows in (slice(0, 200), slice(V // 2, V // 2 + 200), slice(V - 200, V)):
+        want = p[:, rows].t() @ x.double()
+        # half a step of dz and half a step of the output, and p's own error
+        bound = (p[:, rows].abs().t() @ x.double().abs()) * (half_step("bf16") * 1.01 + 2 * float(err.max())) + half_step("bf16") * 1.02 * want.abs() + 1e-30
+        assert bool(((dw[rows].double() - want).abs() <= bound).all())
+    assert bool((dw[V] == 5).all())
+    want, bound = torch.zeros(T, H, dtype=torch.float64, device="cuda"), torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    for a in range(0, V, 10000):
+        want += p[:, a:a + 10000] @ w[a:a + 10000].double()
+        bound += p[:, a:a + 10000].abs() @ w[a:a + 10000].double().abs()
+    bound = bound * (half_step("bf16") * 1.01 + 2 * float(err.max()) + (8192 / 16 + 40) * 2.0 ** -22) + half_step("bf16") * 1.02 * want.abs()
+    assert bool(((dx.double() - want).abs() <= bound).all())
+
+
 def test_which_gradients_and_outputs():
     c = Case(150, 600, 96)
     c.forward(loss=False)
