@@ -10,10 +10,16 @@
 // runs of those, so a row is the expert's start, plus the expert's assignments
 // in the CTAs and warps before, plus its place among equal ones of the warp.
 // Two launches (counts per CTA; places), one where a single CTA holds all; the
-// second starts while the first runs and counts its own run meanwhile.
+// second starts while the first runs and counts its own run meanwhile.  Bound by
+// latencies: two launches, a load of the assignments in each, the sums over the
+// CTAs' counts.  262144 assignments to 256 experts 10.2 us in a graph, 128 to 16
+// 3.7; a thread's loads four at a time in place of one by one took 2.7 us off.
 //
 // The other three go by tokens, so that a token's row is read or written once
-// however many experts it has, and each expert's row once.  Bound by memory.
+// however many experts it has, and each expert's row once.  Bound by memory:
+// 16384 tokens x 2 rows of 4096 bf16 values, dispatch and its gradient 124 us
+// (800 MB, 6.4 TB/s, 0.95 of the copy rate), combine and both gradients 166 us
+// (1070 MB in the two calls, 6.5 TB/s).
 #include <algorithm>
 #include <climits>
 #include <cstdint>

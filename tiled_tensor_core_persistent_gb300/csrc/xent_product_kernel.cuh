@@ -19,6 +19,14 @@
 // Roles, registers, accumulators and bounded waits as in xent_kernel.cuh: pairs
 // of CTAs on tiles of 256 rows, 256 or 128 columns.  Sums longer than 8192 k are
 // added up in registers in pieces of that length.
+//
+// Bound by the tensor cores where the sums are long (1000 x 50021 x 1280: both
+// products 150 us, tensor pipe 72 %; as two calls of tcg_gemm 245), by the way of
+// dW's tiles to memory where there are few tokens (64 x 32768 x 4096: a tile of 64
+// KB a CTA in 2.1 us, of which the stores 1.5: 32 rows of 32 bytes at a time).
+// What helped there: an accumulator's hand-back without a release at cluster scope
+// (265 -> 195 us for all of the backward pass), one output type's code at a time
+// (fewer instructions fetched), stores straight from registers (186).
 #pragma once
 
 #include "xent_kernel.cuh"
