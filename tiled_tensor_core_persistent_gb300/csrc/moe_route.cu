@@ -378,6 +378,13 @@ __device__ __forceinline__ void store_lane(const Route& p, long long t, int lane
     }
 }
 
+template <int kN>
+__device__ __forceinline__ void store_typed(const Route& p, long long t, int lane, const float (&d)[kN]) {
+    if (p.d_dtype == TCG_F32) store_lane<float, kN>(p, t, lane, d);
+    else if (p.d_dtype == TCG_F16) store_lane<__half, kN>(p, t, lane, d);
+    else store_lane<__nv_bfloat16, kN>(p, t, lane, d);
+}
+
 template <typename T, int kN>
 __global__ void __launch_bounds__(32 * kWarps, resident(kN, true)) route_grad_kernel(const __grid_constant__ Route p) {
     tcg::host::wait_for_kernel_ahead();
@@ -420,6 +427,19 @@ __global__ void __launch_bounds__(32 * kWarps, resident(kN, true)) route_grad_ke
             }
             g = sum;
         }
+        if (p.chosen_only && !p.accumulate) {
+            // zeros, then the few that are not
+            const float zero[kN] = {};
+            for (int r = 0; r < rows; ++r) store_typed<kN>(p, tb + r, lane, zero);
+            __syncwarp();
+            if (first) {
+                const long long at = my_t * p.ldd + e;
+                if (p.d_dtype == TCG_F32) static_cast<float*>(p.dlogits)[at] = g;
+                else if (p.d_dtype == TCG_F16) static_cast<__half*>(p.dlogits)[at] = __float2half_rn(g);
+                else static_cast<__nv_bfloat16*>(p.dlogits)[at] = __float2bfloat16_rn(g);
+            }
+            continue;
+        }
         for (int r = 0; r < rows; ++r) {
             const bool any = (__shfl_sync(kAll, live & of_slot, r * p.width)) != 0u;
             if (!any && p.accumulate) continue;   // a token of nobody adds nothing, whatever its logits hold
@@ -449,9 +469,7 @@ __global__ void __launch_bounds__(32 * kWarps, resident(kN, true)) route_grad_ke
 #pragma unroll
                 for (int i = 0; i < kN; ++i) d[i] = z[i] * inv * (d[i] - inner);
             }
-            if (p.d_dtype == TCG_F32) store_lane<float, kN>(p, tb + r, lane, d);
-            else if (p.d_dtype == TCG_F16) store_lane<__half, kN>(p, tb + r, lane, d);
-            else store_lane<__nv_bfloat16, kN>(p, tb + r, lane, d);
+            store_typed<kN>(p, tb + r, lane, d);
         }
     }
 }
