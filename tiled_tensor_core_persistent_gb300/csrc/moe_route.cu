@@ -11,8 +11,9 @@
 // that sort alike; a lane sorts its own in runs of eight and leaves them in
 // shared memory, and each round takes the warp's largest head in one reduction,
 // after which the lane that had it reads its next.  16-bit logits share a
-// 32-bit key with the expert's number, so keys differ; an fp32 key is 64 bits,
-// and of equal logits the lowest lane has the lower expert.  Weights, their
+// 32-bit key with the expert's number, so keys differ; an fp32 logit takes all 32
+// bits, of equal ones the lowest lane has the lower expert, and the expert's
+// number is found at the end, for all of a row's choices at once.  Weights, their
 // gradients and the chosen logits are worked on k lanes a row, for as many rows
 // as fit a warp.  Statistics are fp32.
 //
@@ -122,16 +123,16 @@ __device__ __forceinline__ void load_row(const Route& p, long long t, int lane, 
 }
 
 // Integers that sort as the values do.  NaN is the largest, both zeros are one,
-// and what stands for -inf is below kFloor.  A key ends in the expert's number
-// turned over, so that of equal values the lower expert has the larger key.
+// and what stands for -inf is below kFloor.  A 16-bit value's key ends in the
+// expert's number turned over, so that of equal values the lower expert has the
+// larger key; an fp32 value has all 32 bits.
 template <typename T>
 struct Keys {   // 16-bit values
-    using Key = uint32_t;
     static constexpr uint32_t kFloor = std::is_same<T, __half>::value ? 0x04000000u : 0x00800000u;
 
     // Experts i and i + 1 of a row, `turned` the first one's number turned over.
     template <int kN>
-    static __device__ __forceinline__ void make2(const Row<T, kN>& x, int i, uint32_t turned, Key& k0, Key& k1) {
+    static __device__ __forceinline__ void make2(const Row<T, kN>& x, int i, uint32_t turned, uint32_t& k0, uint32_t& k1) {
         // (adding zero makes -0 into +0, and every NaN into the positive one)
         uint32_t w = x.w[i / 2];
         if constexpr (std::is_same<T, __half>::value) {
@@ -144,67 +145,52 @@ struct Keys {   // 16-bit values
         k0 = make(w << 16, turned);
         k1 = make(w, turned - 1u);
     }
-    static __device__ __forceinline__ Key make(uint32_t x, uint32_t turned) {
+    static __device__ __forceinline__ uint32_t make(uint32_t x, uint32_t turned) {
         const uint32_t o = x ^ (static_cast<uint32_t>(static_cast<int>(x) >> 31) | 0x80000000u);
         return __byte_perm(o, turned, 0x3254);   // o's upper half over the number
     }
-    static __device__ __forceinline__ uint32_t rank(Key k) { return k; }
-    // Where the head was taken, the run's next key takes its place (no branch:
-    // one lane of 32 does it).  Nothing below the floor is ever taken.
-    static __device__ __forceinline__ void advance(Key& head, uint32_t& next, Key taken) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.eq.u32 p, %0, %2;\n\t"
-            "setp.ge.and.u32 p, %2, %3, p;\n\t"
-            "@p ld.shared.u32 %0, [%1];\n\t"
-            "@p add.u32 %1, %1, 4;\n\t}"
-            : "+r"(head), "+r"(next)
-            : "r"(taken), "n"(kFloor)
-            : "memory");
-    }
-    static __device__ __forceinline__ float value(uint32_t rank) {
-        const uint32_t x = (rank & 0x80000000u ? rank ^ 0x80000000u : ~rank) & 0xFFFF0000u;
+    static __device__ __forceinline__ float value(uint32_t key) {
+        const uint32_t x = (key & 0x80000000u ? key ^ 0x80000000u : ~key) & 0xFFFF0000u;
         if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<unsigned short>(x >> 16)));
         else return __uint_as_float(x);
     }
 };
 template <>
 struct Keys<float> {
-    using Key = unsigned long long;
     static constexpr uint32_t kFloor = 0x00800000u;
 
-    static __device__ __forceinline__ Key make(float v, uint32_t turned) {
+    static __device__ __forceinline__ uint32_t make(float v) {
         const uint32_t x = __float_as_uint(v + 0.0f);
-        const uint32_t o = v != v ? 0xFFFFFFFFu : x ^ (static_cast<uint32_t>(static_cast<int>(x) >> 31) | 0x80000000u);
-        return static_cast<Key>(o) << 32 | turned;
+        return v != v ? 0xFFFFFFFFu : x ^ (static_cast<uint32_t>(static_cast<int>(x) >> 31) | 0x80000000u);
     }
     template <int kN>
-    static __device__ __forceinline__ void make2(const Row<float, kN>& x, int i, uint32_t turned, Key& k0, Key& k1) {
-        k0 = make(x.value(i), turned);
-        k1 = make(x.value(i + 1 < kN ? i + 1 : i), turned - 1u);
+    static __device__ __forceinline__ void make2(const Row<float, kN>& x, int i, uint32_t, uint32_t& k0, uint32_t& k1) {
+        k0 = make(x.value(i));
+        k1 = make(x.value(i + 1 < kN ? i + 1 : i));
     }
-    static __device__ __forceinline__ uint32_t rank(Key k) { return static_cast<uint32_t>(k >> 32); }
-    static __device__ __forceinline__ void advance(Key& head, uint32_t& next, Key taken) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.eq.u64 p, %0, %2;\n\t"
-            "setp.ge.and.u32 p, %3, %4, p;\n\t"
-            "@p ld.shared.u64 %0, [%1];\n\t"
-            "@p add.u32 %1, %1, 8;\n\t}"
-            : "+l"(head), "+r"(next)
-            : "l"(taken), "r"(rank(taken)), "n"(kFloor)
-            : "memory");
-    }
-    static __device__ __forceinline__ float value(uint32_t rank) {
-        return __uint_as_float(rank & 0x80000000u ? rank ^ 0x80000000u : ~rank);
+    static __device__ __forceinline__ float value(uint32_t key) {
+        return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
     }
 };
 
+// Where the head was taken, the run's next key takes its place (no branch: one
+// lane of 32 does it).
+__device__ __forceinline__ void advance(uint32_t& head, uint32_t& next, bool taken) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "@p ld.shared.u32 %0, [%1];\n\t"
+        "@p add.u32 %1, %1, 4;\n\t}"
+        : "+r"(head), "+r"(next)
+        : "r"(static_cast<uint32_t>(taken))
+        : "memory");
+}
+
 // Falling order, for one, two, four or eight keys (odd-even merges).
-template <int kL, typename K>
-__device__ __forceinline__ void sort_run(K (&k)[kL]) {
+template <int kL>
+__device__ __forceinline__ void sort_run(uint32_t (&k)[kL]) {
     auto order = [&](int i, int j) {
-        const K a = k[i], b = k[j];
+        const uint32_t a = k[i], b = k[j];
         k[i] = max(a, b);
         k[j] = min(a, b);
     };
@@ -264,66 +250,95 @@ template <typename T, int kN>
 __global__ void __launch_bounds__(32 * kWarps, resident(kN, false)) route_kernel(const __grid_constant__ Route p) {
     tcg::host::wait_for_kernel_ahead();
     using K = Keys<T>;
-    using Key = typename K::Key;
+    constexpr bool kWide = sizeof(T) == 4;   // equal keys are possible
     constexpr int kL = kN < 8 ? kN : 8, kRuns = kN / kL;
     // each run ends in a key that is below any
-    __shared__ Key sorted[kWarps][32 * kRuns * (kL + 1)];
+    __shared__ uint32_t sorted[kWarps][32 * kRuns * (kL + 1)];
     const int lane = threadIdx.x & 31;
-    Key* mine = sorted[threadIdx.x >> 5] + lane * kRuns * (kL + 1);
+    uint32_t* mine = sorted[threadIdx.x >> 5] + lane * kRuns * (kL + 1);
     const uint32_t mine_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
 #pragma unroll
-    for (int g = 0; g < kRuns; ++g) mine[g * (kL + 1) + kL] = Key(0);
+    for (int g = 0; g < kRuns; ++g) mine[g * (kL + 1) + kL] = 0u;
     const int slot = lane / p.width, place = lane - slot * p.width, fit = 32 / p.width;
     const Run tokens = run_of(p);
     for (long long tb = tokens.t0; tb < tokens.t1; tb += fit) {
         const int rows = static_cast<int>(min(static_cast<long long>(fit), tokens.t1 - tb));
         // lane (slot, place): the place's choice of row tb + slot
-        Key my_key = 0;
+        uint32_t my_key = 0u;
+        int my_e = -1;
         float my_sum = 0.0f;
         for (int r = 0; r < rows; ++r) {
             const long long t = tb + r;
             if (p.mask && !p.mask[t]) continue;
             Row<T, kN> x;
             load_row<T, kN>(p, t, lane, x);
-            Key head[kRuns];
-            uint32_t next[kRuns];   // shared addresses
+            uint32_t head[kRuns], next[kRuns];   // next: shared addresses
+            uint32_t keys[kWide ? kN : 1];
 #pragma unroll
             for (int g = 0; g < kRuns; ++g) {
-                Key run[kL];
+                uint32_t run[kL];
                 const uint32_t turned = 0xFFFFu - static_cast<uint32_t>(lane * kN + g * kL);
                 if constexpr (kL == 1) {
-                    Key other;
+                    uint32_t other;
                     K::make2(x, 0, turned, run[0], other);
                 } else {
 #pragma unroll
                     for (int i = 0; i < kL; i += 2) K::make2(x, g * kL + i, turned - i, run[i], run[i + 1]);
+                }
+                if constexpr (kWide) {
+#pragma unroll
+                    for (int i = 0; i < kL; ++i) keys[g * kL + i] = run[i];
                 }
                 sort_run<kL>(run);
                 // (only this lane reads them)
 #pragma unroll
                 for (int i = 1; i < kL; ++i) mine[g * (kL + 1) + i] = run[i];
                 head[g] = run[0];
-                next[g] = mine_at + (g * (kL + 1) + 1) * static_cast<uint32_t>(sizeof(Key));
+                next[g] = mine_at + (g * (kL + 1) + 1) * 4u;
             }
-            const int last = r * p.width + p.k;
-            for (int to = r * p.width; to < last; ++to) {
-                Key most = head[0];
+            const int from = r * p.width, last = from + p.k;
+            if constexpr (kWide) {
+                // A choice is its key, the lowest lane that holds it, and how many equal ones that lane gave before.
+                uint32_t before = 0u;
+                int holder = -1, nth = 0, my_holder = 0, my_nth = 0;
+                for (int to = from; to < last; ++to) {
+                    uint32_t most = head[0];
 #pragma unroll
-                for (int g = 1; g < kRuns; ++g) most = max(most, head[g]);
-                const uint32_t best = __reduce_max_sync(kAll, K::rank(most));
-                if constexpr (sizeof(T) == 4) {
-                    // of lanes with equal logits the lowest has the lowest expert
-                    const int holder = __ffs(__ballot_sync(kAll, K::rank(most) == best)) - 1;
-                    most = __shfl_sync(kAll, most, holder);
-                } else {
-                    most = best;
+                    for (int g = 1; g < kRuns; ++g) most = max(most, head[g]);
+                    const uint32_t best = __reduce_max_sync(kAll, most);
+                    const int owner = __ffs(__ballot_sync(kAll, most == best)) - 1;
+                    nth = best == before && owner == holder ? nth + 1 : 0;
+                    before = best;
+                    holder = owner;
+                    if (lane == to) my_key = best, my_holder = owner, my_nth = nth;
+                    bool open = lane == owner && best >= K::kFloor;   // nothing below the floor is ever taken
+#pragma unroll
+                    for (int g = 0; g < kRuns; ++g) {
+                        const bool here = open && head[g] == best;
+                        advance(head[g], next[g], here);
+                        open = open && !here;
+                    }
                 }
-                if (lane == to) my_key = most;
+                // ... and so its expert is the nth of the lane's that have that key.
+                const bool of_row = lane >= from && lane < last && my_key >= K::kFloor;
 #pragma unroll
-                for (int g = 0; g < kRuns; ++g) K::advance(head[g], next[g], most);
+                for (int i = 0; i < kN; ++i) {
+                    const uint32_t key = __shfl_sync(kAll, keys[i], my_holder);
+                    if (of_row && key == my_key && my_nth-- == 0) my_e = my_holder * kN + i;
+                }
+            } else {
+                for (int to = from; to < last; ++to) {
+                    uint32_t most = head[0];
+#pragma unroll
+                    for (int g = 1; g < kRuns; ++g) most = max(most, head[g]);
+                    const uint32_t best = __reduce_max_sync(kAll, most);
+                    if (lane == to) my_key = best;
+#pragma unroll
+                    for (int g = 0; g < kRuns; ++g) advance(head[g], next[g], head[g] == best && best >= K::kFloor);
+                }
             }
             if (!p.chosen_only) {
-                const float m = K::value(K::rank(__shfl_sync(kAll, my_key, r * p.width)));
+                const float m = K::value(__shfl_sync(kAll, my_key, from));
                 float s = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kN; ++i) s += expf(x.value(i) - m);
@@ -332,8 +347,8 @@ __global__ void __launch_bounds__(32 * kWarps, resident(kN, false)) route_kernel
             }
         }
         // (a row's first choice has its largest logit; rows without one have no choice at all)
-        const int my_e = K::rank(my_key) < K::kFloor ? -1 : 0xFFFF - static_cast<int>(my_key & 0xFFFFu);
-        const float v = K::value(K::rank(my_key)), m = __shfl_sync(kAll, v, slot * p.width);
+        if (!kWide && my_key >= K::kFloor) my_e = 0xFFFF - static_cast<int>(my_key & 0xFFFFu);
+        const float v = K::value(my_key), m = __shfl_sync(kAll, v, slot * p.width);
         const float z = my_e >= 0 ? expf(v - m) : 0.0f;
         const float s = lanes_sum(z, p.width);
         if (slot < rows && place < p.k) {
