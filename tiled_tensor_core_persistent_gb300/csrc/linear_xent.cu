@@ -55,18 +55,19 @@ struct Finish {
 };
 
 // 32 threads a row, each some of the column tiles, eight of them on their way at
-// once; sums in a fixed order.
+// once: first a warp's lanes are 32 rows (whose tiles lie side by side), then, the
+// 32 x 32 results turned in shared memory, the threads of one row.  What is in
+// 64 bits is one warp's (64-bit operations are slow, and as slow for one lane as
+// for 32).  Sums in a fixed order.
 __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ Finish p) {
     tcg::host::wait_for_kernel_ahead();
-    __shared__ float2 slot[kFinishSlices][kFinishRows];
+    __shared__ float2 slot[kFinishSlices][kFinishRows + 1];
+    __shared__ float2 joined[kFinishRows];
     __shared__ int last;
+    static_assert(kFinishRows == 32 && kFinishSlices == 32, "a warp a row, a lane a slice");
     const int r = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const long long row = static_cast<long long>(blockIdx.x) * kFinishRows + r;
     const bool in = row < p.tokens;
-    auto join = [](float2 a, float2 b) {
-        const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.0f : m;
-        return make_float2(m, a.y * exp2f(a.x - base) + b.y * exp2f(b.x - base));
-    };
     float2 v = make_float2(-INFINITY, 0.0f);
     for (int n0 = slice; in && n0 < p.num_n; n0 += kFinishSlices * kFinishBatch) {
         float2 w[kFinishBatch];
@@ -86,14 +87,23 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
     }
     slot[slice][r] = v;
     __syncthreads();
+    // row `slice` of the CTA's
+    v = slot[r][slice];
+    float m = v.x;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float s = v.y * exp2f(v.x - (m == -INFINITY ? 0.0f : m));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (r == 0) joined[slice] = make_float2(m, s);
+    __syncthreads();
     double sum = 0.0;
     int count = 0;
     if (slice == 0) {
         if (in) {
-#pragma unroll
-            for (int i = 1; i < kFinishSlices; ++i) v = join(v, slot[i][r]);
             // (logits were multiplied by kLog2e as it is held, so that is what divides here)
-            const double lse = (static_cast<double>(v.x) + static_cast<double>(log2f(v.y))) / static_cast<double>(tcg::xent::kLog2e);
+            const double lse = (static_cast<double>(joined[r].x) + static_cast<double>(log2f(joined[r].y))) *
+                               (1.0 / static_cast<double>(tcg::xent::kLog2e));
             p.lse[row] = static_cast<float>(lse);
             const int y = p.target[row];
             const bool counts = y >= 0 && y < p.vocab;
@@ -133,7 +143,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
         if (threadIdx.x == 0) *p.arrivals = 0;
     }
     if (threadIdx.x == 0) {
-        *p.mean = count > 0 ? static_cast<float>(sum / count) : 0.0f;
+        *p.mean = count > 0 ? static_cast<float>(sum) / static_cast<float>(count) : 0.0f;
         *p.valid = count;
     }
 }
