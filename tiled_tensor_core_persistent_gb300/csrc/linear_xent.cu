@@ -261,14 +261,17 @@ Layout backward_layout(int tokens, int vocab, int hidden, int sms) {
 
 // ---------------------------------------------------------------- launches
 
-template <typename K>
-cudaError_t set_attributes(K* kernel, int smem) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    cudaFuncAttributes a;
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
-    // the register hand-over draws on what the block is launched with
-    if (e == cudaSuccess && a.numRegs < tcg::xent::kLaunchRegs) e = cudaErrorInvalidConfiguration;
-    return e;
+template <auto* kKernel, int kSmem>
+cudaError_t set_attributes() {
+    static tcg::host::OncePerDevice once;
+    return once([] {
+        cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaFuncAttributes a;
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kKernel);
+        // the register hand-over draws on what the block is launched with
+        if (e == cudaSuccess && a.numRegs < tcg::xent::kLaunchRegs) e = cudaErrorInvalidConfiguration;
+        return e;
+    });
 }
 
 template <typename P>
@@ -294,12 +297,11 @@ tcg_status launch_ctas(void (*kernel)(P), const P& p, bool pair, int workers, in
 
 template <typename T, bool kPair, bool kGrad>
 tcg_status launch(const Params& p, const Plan& pl, cudaStream_t stream) {
-    auto* kernel = tcg::xent::xent_kernel<T, kPair, kGrad>;
+    constexpr auto* kKernel = &tcg::xent::xent_kernel<T, kPair, kGrad>;
     constexpr int kSmem = tcg::xent::Shape<kPair>::kSmemBytes;
-    static tcg::host::OncePerDevice once;
-    const cudaError_t e = once([&] { return set_attributes(kernel, kSmem); });
+    const cudaError_t e = set_attributes<kKernel, kSmem>();
     if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent kernel attributes", e);
-    return launch_ctas(kernel, p, kPair, pl.workers, kSmem, stream);
+    return launch_ctas(kKernel, p, kPair, pl.workers, kSmem, stream);
 }
 
 template <typename T, bool kGrad>
@@ -348,13 +350,12 @@ void set_output(tcg::xent::Product& q, void* out, long long ld, tcg_dtype t, flo
 }
 
 tcg_status launch_products(tcg::xent::Products& p, const ProductPlan& pl, cudaStream_t stream) {
-    auto* kernel = tcg::xent::xent_product_kernel;
-    static tcg::host::OncePerDevice once;
-    cudaError_t e = once([&] { return set_attributes(kernel, tcg::xent::kProductSmem); });
+    constexpr auto* kKernel = &tcg::xent::xent_product_kernel;
+    const cudaError_t e = set_attributes<kKernel, tcg::xent::kProductSmem>();
     if (e != cudaSuccess) return tcg::host::fail_launch("tcg_linear_xent_backward kernel attributes", e);
     p.timeout_ns = tcg::host::wait_timeout_ns();
     p.fault_inject = tcg::host::fault_inject();
-    return launch_ctas(kernel, p, true, pl.workers, tcg::xent::kProductSmem, stream);
+    return launch_ctas(kKernel, p, true, pl.workers, tcg::xent::kProductSmem, stream);
 }
 
 tcg_status check(int tokens, int vocab, int hidden, tcg_dtype dtype, const void* X, int ldx, const void* W, int ldw,
