@@ -393,6 +393,21 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_exact(T):
     c.check_forward()
 
 
+@pytest.mark.parametrize("V", [600, 100003])
+def test_a_workspace_that_starts_on_any_16_bytes(V):
+    c = Case(70 if V < 1000 else 2000, V, 72)
+    want = []
+    for shift in (0, 16):
+        c.ws = torch.zeros(c.bytes + shift + 16, dtype=torch.uint8, device="cuda")[shift:shift + c.bytes]
+        assert c.ws.data_ptr() % 32 == shift
+        c.forward()
+        one = torch.ones(1, device="cuda")
+        gx, gw = c.backward("bf16", "f32", one)
+        want.append([c.lse.clone(), c.loss.clone(), gx, gw])
+    for a, b in zip(*want):
+        assert torch.equal(a, b)
+
+
 def test_a_workspace_that_does_not_do():
     c = Case(10, 50, 64)
     gm = torch.ones(1, device="cuda")

@@ -246,13 +246,16 @@ Layout forward_layout(int tokens, int vocab) {
     return l;
 }
 
-int pitch_of(int n) { return static_cast<int>(blocks(n, 32) * 32); }   // rows of any type start on 32 bytes
+// Rows of any type start on 32 bytes, as dz is stored in such words: its first
+// one past a workspace that starts on 16.
+constexpr size_t kWord = 32;
+int pitch_of(int n) { return static_cast<int>(blocks(n, kWord) * kWord); }
 
 Layout backward_layout(int tokens, int vocab, int hidden, int sms) {
     Layout l;
     const int words = piece_words(tokens, vocab);
     l.back = l.take(sizeof(float));
-    l.dz = l.take(static_cast<size_t>(tokens) * pitch_of(words) * 2);
+    l.dz = l.take(static_cast<size_t>(tokens) * pitch_of(words) * 2 + kWord);
     l.dx = l.take(words < vocab ? static_cast<size_t>(tokens) * pitch_of(hidden) * sizeof(float) : 0);
     // (tiles are split while their pieces are at most two for each pair of SMs)
     l.partials = l.take(static_cast<size_t>(sms / 2 * 2) * tcg::xent::kPartialFloats * sizeof(float));
@@ -454,7 +457,7 @@ tcg_status tcg_linear_xent_backward(int tokens, int vocab, int hidden, tcg_dtype
     const int words = piece_words(tokens, vocab), pitch = pitch_of(words), ld = pitch_of(hidden);
     float* back = reinterpret_cast<float*>(ws + l.back);
     float* dx32 = reinterpret_cast<float*>(ws + l.dx);
-    char* dz = ws + l.dz;
+    char* dz = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws + l.dz) + kWord - 1) & ~uintptr_t(kWord - 1));
     for (int v0 = 0; v0 < vocab; v0 += words) {
         const int n = std::min(words, vocab - v0);
         const bool last = v0 + n == vocab;
