@@ -659,9 +659,11 @@ tcg_status tcg_moe_sort(int tokens, int experts, int k, const int* topk, int ld_
 /*
  * tcg_moe_dispatch -- row row_of[t, j] of out is row t of x (tokens x cols), for
  * every assignment.  Entries of row_of outside [0, rows) are skipped; rows of
- * out that none names are left as they were, and one that several name holds
- * one of them.  Its gradient is tcg_moe_combine without weights.  cols <=
- * 65535 * 4096 - 8 here and below.  Outputs must not overlap inputs.
+ * out that none names are left as they were.  tcg_moe_sort names no row twice;
+ * where row_of does, each value of that row is one of those it was given, not
+ * the same one every time.  The gradient (of rows named once) is tcg_moe_combine
+ * without weights.  cols <= 65535 * 4096 - 8 here and below.  Outputs must not
+ * overlap inputs.
  */
 tcg_status tcg_moe_dispatch(int tokens, int k, int cols, int rows, const void* x, int ldx, tcg_dtype x_dtype,
                             const int* row_of, int ld_row_of, void* out, int ldo, tcg_dtype out_dtype, void* stream);
@@ -679,9 +681,10 @@ tcg_status tcg_moe_combine(int tokens, int k, int cols, int rows, const void* x,
 /*
  * tcg_moe_combine_backward -- both gradients of tcg_moe_combine, in one pass
  * over dy and x: dx[row_of[t, j]] = weights[t, j] * dy_t (rows that no
- * assignment names are left as they were) and dweights[t, j] = sum over the
- * columns of dy_t * x[row_of[t, j]], 0 for skipped entries.  dx has x's type.
- * dweights may be NULL, and x with it.
+ * assignment names are left as they were; one that several name is given to
+ * each in turn as in tcg_moe_dispatch, not their sum) and dweights[t, j] = sum
+ * over the columns of dy_t * x[row_of[t, j]], 0 for skipped entries.  dx has x's
+ * type.  dweights may be NULL, and x with it.
  */
 tcg_status tcg_moe_combine_backward(int tokens, int k, int cols, int rows, const void* x, int ldx, tcg_dtype x_dtype,
                                     const int* row_of, int ld_row_of, const float* weights, int ld_weights,
@@ -709,8 +712,9 @@ size_t tcg_linear_xent_workspace_size(int tokens, int vocab, int hidden, int bac
  * tcg_linear_xent -- lse_t = log sum_v exp(x_t . W_v) (every token's), loss_t =
  * lse_t - x_t . W_target (0 where the token does not count; loss may be NULL),
  * num_valid = n, the tokens that count, and mean = their losses' sum / n (0 when
- * n = 0); fp32, device memory.  A logit that is NaN or +inf makes its token's
- * lse and loss NaN.  The results are the same every time.
+ * n = 0); fp32, device memory.  A logit that is NaN, +inf or above 2^127 (which
+ * times log2(e) may be +inf) makes its token's lse and loss NaN.  The results are
+ * the same every time.
  */
 tcg_status tcg_linear_xent(int tokens, int vocab, int hidden, tcg_dtype dtype, const void* X, int ldx,
                            const void* W, int ldw, const int* target, float* lse, float* loss, float* mean, int* num_valid,

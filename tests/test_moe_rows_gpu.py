@@ -273,6 +273,41 @@ def test_nothing_to_move():
     assert torch.equal(y, x[[0, 3, 1, 2]])
 
 
+def test_no_columns_at_addresses_that_are_not_whole_words():
+    row_of = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    m = torch.full((4, 7), 2.0, dtype=torch.bfloat16, device="cuda")
+    for shift in range(1, 7):
+        at = m.view(-1)[shift:]
+        dw = torch.full((4, 2), 7.0, device="cuda")
+        tcg.moe_dispatch(4, 2, 0, 4, at, 7, "bf16", row_of, 2, at, 7, "bf16")
+        tcg.moe_combine(4, 2, 0, 4, at, 7, "bf16", row_of, 2, None, 2, at, 7, "bf16")
+        tcg.moe_combine_backward(4, 2, 0, 4, at, 7, "bf16", row_of, 2, None, 2, at, 7, "bf16", at, 7, dw, 2)
+        assert not bool(dw.any())
+    assert bool((m == 2).all())
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_the_same_row_twice(shift):
+    """By two places of a token, and by two tokens: each value is one of theirs, sums and weights' gradients are exact."""
+    cols, rows = 40, 3
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    row_of = torch.tensor([[1, 1], [2, 0], [2, 1]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[1.0, 2.0], [4.0, 8.0], [16.0, 32.0]], device="cuda")
+    small = lambda n: torch.randint(-9, 10, (n, cols), generator=gen, device="cuda").float()
+    room = lambda m: torch.cat([torch.zeros(shift, device="cuda"), m.flatten()])[shift:].view_as(m)
+    x, y, dx, out = room(small(rows)), room(small(3)), room(torch.full((rows, cols), 500.0, device="cuda")), room(torch.zeros(rows, cols, device="cuda"))
+    dw, got = torch.zeros(3, 2, device="cuda"), room(torch.zeros(3, cols, device="cuda"))
+    tcg.moe_dispatch(3, 2, cols, rows, y, cols, "f32", row_of, 2, out, cols, "f32")
+    tcg.moe_combine(3, 2, cols, rows, x, cols, "f32", row_of, 2, w, 2, got, cols, "f32")
+    tcg.moe_combine_backward(3, 2, cols, rows, x, cols, "f32", row_of, 2, w, 2, y, cols, "f32", dx, cols, dw, 2)
+    assert torch.equal(got, (w[:, :, None] * x[row_of.long()]).sum(1))
+    assert torch.equal(dw, (y[:, None] * x[row_of.long()]).sum(2))
+    for r in range(rows):
+        named = (row_of == r).nonzero().tolist()
+        assert bool(torch.stack([out[r] == y[t] for t, _ in named]).any(0).all())
+        assert bool(torch.stack([dx[r] == w[t, j] * y[t] for t, j in named]).any(0).all())
+
+
 def test_offsets_past_31_bits():
     """Rows whose elements start past 2^31."""
     T, k, cols = 600000, 1, 4096

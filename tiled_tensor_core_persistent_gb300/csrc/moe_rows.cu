@@ -622,7 +622,8 @@ tcg_status tcg_moe_combine_backward(int tokens, int k, int cols, int rows, const
     p.ldo = lddx;
     p.dweights = dweights;
     p.ld_dweights = ld_dweights;
-    const bool whole = (!dweights || whole_words(x, ldx, x_dtype)) && whole_words(dy, lddy, dy_dtype) && whole_words(dx, lddx, x_dtype);
+    // (without a column there is no word that may be read; the weights' gradients are written all the same)
+    const bool whole = cols == 0 || ((!dweights || whole_words(x, ldx, x_dtype)) && whole_words(dy, lddy, dy_dtype) && whole_words(dx, lddx, x_dtype));
     p.lanes = lanes_for(cols, 4);
     const int per_cta = kMoveThreads / p.lanes;
     const dim3 grid(static_cast<unsigned>((static_cast<long long>(tokens) + per_cta - 1) / per_cta));
