@@ -20,12 +20,13 @@
 // Bound by the instructions issued (a row of 256 bf16 logits, eight chosen: about
 // 310, most of them integer compares and selects, which issue every other cycle),
 // next by memory, whose part is 2.5 us each way.  32768 x 256, one call after the
-// other in a graph: forward 13.2 us, backward 8.8 (over all experts 16.2 and
-// 13.4; fp32 logits 23.4 and 11.6).  Steps that helped: one reduction a round on
-// keys that hold the expert's number, in place of value, then place (37 us both
-// ways); runs sorted once in place of a search after each round (29); a row's k
-// weights on k lanes, so that exponentials and divisions serve several rows (27);
-// heads replaced under a predicate, without a branch (24, calls included).
+// other in a graph: forward 13.1 us, backward 7.4 (over all experts 16.1 and
+// 12.1; fp32 logits 19.8 and 11.6).  Steps that helped, both ways and calls
+// included: one reduction a round on keys that hold the expert's number, in place
+// of value, then place (37 us); runs sorted once in place of a search after each
+// round (29); a row's k weights on k lanes, so that exponentials and divisions
+// serve several rows (27); heads replaced under a predicate, without a branch
+// (24); zeros first and then the few chosen, where the gradient has no others (22).
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>

@@ -26,7 +26,7 @@
 //
 // What it takes: 4096 x 131072 x 2048 forward 1.08 ms by itself (2.03 PFLOP/s,
 // above the library's 1.93 in bf16) and 1.19 in a loop that draws the power limit
-// (1.85, the library's 1.74); 64 x 32768 x 4096 52 us, 5.2 TB/s of weights (0.78 of
+// (1.85, the library's 1.74); 64 x 32768 x 4096 51 us, 5.3 TB/s of weights (0.79 of
 // the copy rate; the rest is a launch's start, the last tile and the joining).
 // Sums in one go instead of in parts take the same time.  Measured and slower:
 // two accumulators of a tile side by side (1.20 ms against 1.07 at 4096 x 65536 x
