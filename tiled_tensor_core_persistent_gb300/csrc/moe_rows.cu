@@ -38,10 +38,12 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-// Assignments a CTA takes at least.
-constexpr int kSortRun = 2048;
-// As many as this are one CTA's, in one launch.
-constexpr int kSortAlone = 4096;
+// Assignments a CTA takes at least (262144 to 256 experts 8.9 us, 9.3 with 2048;
+// 32768 6.2 and 6.6, 6.5 with 512).
+constexpr int kSortRun = 1024;
+// As many as this are one CTA's, in one launch: 2048 to 16 experts 3.5 us and 4.3
+// in two launches, 4096 5.4 and 4.5.
+constexpr int kSortAlone = 2048;
 // Assignments whose loads a thread has on their way at once.
 constexpr int kSortBatch = 4;
 
@@ -56,8 +58,11 @@ struct Sort {
     int* row_token;
     int* row_of;
     long long ld_row_of;
-    int* counts;                 // [CTA][expert], nullptr where one CTA holds all
+    int* counts;                 // [CTA][pitch_of(experts)], nullptr where one CTA holds all
 };
+
+// A CTA's counts start on 16 bytes (what lies past the experts is never used).
+__host__ __device__ __forceinline__ int pitch_of(int experts) { return (experts + 3) & ~3; }
 
 __device__ __forceinline__ int run_start(int total, int part, int parts) {
     return static_cast<int>(static_cast<long long>(total) * part / parts);
@@ -100,15 +105,15 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_c
             if (v[i].e >= 0) atomicAdd(&hist[v[i].e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.experts; e += kSortThreads) p.counts[static_cast<size_t>(blockIdx.x) * p.experts + e] = hist[e];
+    for (int e = threadIdx.x; e < p.experts; e += kSortThreads) p.counts[static_cast<size_t>(blockIdx.x) * pitch_of(p.experts) + e] = hist[e];
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_constant__ Sort p) {
     extern __shared__ int smem[];
-    int* total = smem;                       // [experts]: all assignments, then the expert's first row
+    int* total = smem;                       // [experts]: all assignments
     int* before = smem + p.experts;          // [experts]: those of the CTAs before
     int* place = smem + 2 * p.experts;       // [warp][experts]: counts, then the warp's next row
-    __shared__ int rows;
+    __shared__ int of_warp[kSortWarps];      // those of its threads' experts
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool alone = p.counts == nullptr;
     if (alone) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -117,89 +122,98 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
     const int c0 = run_start(p.total, blockIdx.x, gridDim.x), c1 = run_start(p.total, blockIdx.x + 1, gridDim.x);
     const int a0 = c0 + run_start(c1 - c0, warp, kSortWarps), a1 = c0 + run_start(c1 - c0, warp + 1, kSortWarps);
     int* mine = place + warp * p.experts;
-    for (int a = a0 + lane; a < a1; a += kSortBatch * 32) {
-        Assignment v[kSortBatch];
-        load_batch<32>(p, a, a1, v);
+    // (the first batch stays in registers until the rows are known)
+    Assignment v[kSortBatch], first[kSortBatch];
+    if (a0 < a1) load_batch<32>(p, a0 + lane, a1, first);
+    for (int b = a0; b < a1; b += kSortBatch * 32) {
+        if (b != a0) load_batch<32>(p, b + lane, a1, v);
 #pragma unroll
-        for (int i = 0; i < kSortBatch; ++i)
-            if (v[i].e >= 0) atomicAdd(&mine[v[i].e], 1);
+        for (int i = 0; i < kSortBatch; ++i) {
+            const int e = b == a0 ? first[i].e : v[i].e;
+            if (e >= 0) atomicAdd(&mine[e], 1);
+        }
     }
     if (!alone) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        // parts threads an expert add up the CTAs' counts
-        const int per = min(kSortThreads, (p.experts + 31) / 32 * 32), parts = kSortThreads / per;
-        const int part = threadIdx.x / per;
-        if (part < parts) {
-            for (int e = threadIdx.x - part * per; e < p.experts; e += per) {
-                int all = 0, ahead = 0;
+        // four experts a thread, each CTA's four in one load; parts threads share the CTAs
+        const int quads = pitch_of(p.experts) / 4, per = max(quads, 16), parts = kSortThreads / per;
+        const int part = threadIdx.x / per, e = 4 * (static_cast<int>(threadIdx.x) - part * per);
+        if (part < parts && e < p.experts) {
+            int4 all = make_int4(0, 0, 0, 0), ahead = all;
 #pragma unroll 16
-                for (int b = part; b < static_cast<int>(gridDim.x); b += parts) {
-                    const int n = p.counts[static_cast<size_t>(b) * p.experts + e];
-                    all += n;
-                    ahead += b < static_cast<int>(blockIdx.x) ? n : 0;
-                }
-                atomicAdd(&total[e], all);
-                atomicAdd(&before[e], ahead);
+            for (int b = part; b < static_cast<int>(gridDim.x); b += parts) {
+                const int4 n = *reinterpret_cast<const int4*>(p.counts + static_cast<size_t>(b) * pitch_of(p.experts) + e);
+                const int is = b < static_cast<int>(blockIdx.x) ? -1 : 0;
+                all.x += n.x, all.y += n.y, all.z += n.z, all.w += n.w;
+                ahead.x += n.x & is, ahead.y += n.y & is, ahead.z += n.z & is, ahead.w += n.w & is;
+            }
+            const int sums[2][4] = {{all.x, all.y, all.z, all.w}, {ahead.x, ahead.y, ahead.z, ahead.w}};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (e + i >= p.experts) continue;
+                atomicAdd(&total[e + i], sums[0][i]);
+                atomicAdd(&before[e + i], sums[1][i]);
             }
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();
-    if (alone) {
-        for (int e = threadIdx.x; e < p.experts; e += kSortThreads) {
-            int n = 0;
+    // a thread's experts: one, or two neighbours
+    const int own = p.experts > kSortThreads ? 2 : 1, e0 = own * static_cast<int>(threadIdx.x), e1 = min(e0 + own, p.experts);
+    int n = 0;
+    for (int e = e0; e < e1; ++e) {
+        if (alone) {
+            int sum = 0;
 #pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) n += place[w * p.experts + e];
-            total[e] = n;
+            for (int w = 0; w < kSortWarps; ++w) sum += place[w * p.experts + e];
+            total[e] = sum;
         }
-        __syncthreads();
+        n += total[e];
     }
-    if (warp == 0) {
-        // each lane a run of experts
-        const int per = (p.experts + 31) / 32, e0 = min(lane * per, p.experts), e1 = min(e0 + per, p.experts);
-        int n = 0;
-        for (int e = e0; e < e1; ++e) n += total[e];
-        int start = n;
+    int start = n;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(kAll, start, d);
-            if (lane >= d) start += o;
-        }
-        if (lane == 31) rows = start;
-        start -= n;
-        for (int e = e0; e < e1; ++e) {
-            const int m = total[e];
-            total[e] = start;
-            start += m;
-        }
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, start, d);
+        if (lane >= d) start += o;
     }
+    if (lane == 31) of_warp[warp] = start;
     __syncthreads();
-    for (int e = threadIdx.x; e < p.experts; e += kSortThreads) {
-        int next = total[e] + before[e];
+    start -= n;
+    int rows = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        const int m = of_warp[w];
+        start += w < warp ? m : 0;
+        rows += m;
+    }
+    for (int e = e0; e < e1; ++e) {
+        int of[kSortWarps], next = start + before[e];
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) of[w] = place[w * p.experts + e];
 #pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
-            const int n = place[w * p.experts + e];
             place[w * p.experts + e] = next;
-            next += n;
+            next += of[w];
         }
-        if (p.offsets && blockIdx.x == 0) p.offsets[e] = total[e];
+        if (p.offsets && blockIdx.x == 0) p.offsets[e] = start;
+        start += total[e];
     }
     if (p.offsets && blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.experts] = rows;
     __syncthreads();
     for (int b = a0; b < a1; b += kSortBatch * 32) {
-        Assignment v[kSortBatch];
-        load_batch<32>(p, b + lane, a1, v);
+        if (b != a0) load_batch<32>(p, b + lane, a1, v);
 #pragma unroll
         for (int i = 0; i < kSortBatch; ++i) {
-            const int e = v[i].e;
+            const Assignment at = b == a0 ? first[i] : v[i];
+            const int e = at.e;
             const uint32_t same = __match_any_sync(kAll, e);
             int row = -1;
             if (e >= 0) row = mine[e] + __popc(same & ((1u << lane) - 1u));
             __syncwarp();
             if (e >= 0 && (same >> lane) == 1u) mine[e] = row + 1;   // the last of its equals
             __syncwarp();
-            if (row >= 0) p.row_token[row] = v[i].t;
-            if (b + i * 32 + lane < a1) p.row_of[v[i].t * p.ld_row_of + v[i].j] = row;
+            if (row >= 0) p.row_token[row] = at.t;
+            if (b + i * 32 + lane < a1) p.row_of[at.t * p.ld_row_of + at.j] = row;
         }
     }
     for (int r = rows + static_cast<int>(blockIdx.x * kSortThreads + threadIdx.x); r < p.total; r += static_cast<int>(gridDim.x) * kSortThreads)
@@ -490,7 +504,7 @@ size_t tcg_moe_sort_workspace_size(int tokens, int experts, int k) {
     tcg::host::Device dev;
     if (tcg::host::device(dev) != TCG_OK) dev.num_sms = 1024;
     const int ctas = sort_ctas(static_cast<long long>(tokens) * k, dev.num_sms);
-    return tcg::host::kScratchAt + (ctas > 1 ? static_cast<size_t>(ctas) * experts * sizeof(int) : 0);
+    return tcg::host::kScratchAt + (ctas > 1 ? static_cast<size_t>(ctas) * pitch_of(experts) * sizeof(int) : 0);
 }
 
 tcg_status tcg_moe_sort(int tokens, int experts, int k, const int* topk, int ld_topk, const uint8_t* mask, int* offsets,
