@@ -662,7 +662,7 @@ tcg_status tcg_moe_sort(int tokens, int experts, int k, const int* topk, int ld_
  * out that none names are left as they were.  tcg_moe_sort names no row twice;
  * where row_of does, each value of that row is one of those it was given, not
  * the same one every time.  The gradient (of rows named once) is tcg_moe_combine
- * without weights.  cols <= 65535 * 4096 - 8 here and below.  Outputs must not
+ * without weights.  cols <= 65535 * 2048 - 8 here and below.  Outputs must not
  * overlap inputs.
  */
 tcg_status tcg_moe_dispatch(int tokens, int k, int cols, int rows, const void* x, int ldx, tcg_dtype x_dtype,

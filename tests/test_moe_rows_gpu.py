@@ -66,7 +66,7 @@ def sort(T, E, k, topk, mask, ws=None, offsets=True, pad=0, stream=None):
 
 
 SIZES = [(1, 1, 1), (1, 1, 5), (2, 3, 2), (64, 16, 2), (17, 5, 3), (4096, 8, 1), (4097, 8, 1), (1000, 1024, 7), (1366, 40, 3), (700, 2, 6),
-         (32768, 256, 8), (20001, 300, 13), (100000, 7, 4), (300000, 64, 2), (2, 9, 100000)]
+         (32768, 256, 8), (20001, 300, 13), (100000, 7, 4), (300000, 64, 2), (2, 9, 100000), (2048, 8, 1), (2049, 9, 1), (3000, 1021, 3), (1030, 513, 2)]
 
 
 @pytest.mark.parametrize("T,E,k", SIZES)
@@ -162,7 +162,7 @@ class Rows:
 
 
 SHAPES = [(1, 1, 1, 1), (1, 4, 2, 8), (3, 5, 3, 7), (64, 16, 2, 4096), (50, 8, 8, 100), (17, 9, 5, 1030), (300, 40, 4, 264), (5, 3, 2, 9000),
-          (1, 2, 33, 16), (2000, 16, 2, 65)]
+          (1, 2, 33, 16), (2000, 16, 2, 65), (900, 12, 5, 4100), (350, 12, 3, 2050)]
 TYPES = [("bf16", "bf16", 0, 0), ("f16", "f32", 3, 1), ("f32", "bf16", 0, 0), ("bf16", "f16", 8, 0), ("f32", "f32", 1, 1)]
 
 

@@ -12,14 +12,17 @@
 // Two launches (counts per CTA; places), one where a single CTA holds all; the
 // second starts while the first runs and counts its own run meanwhile.  Bound by
 // latencies: two launches, a load of the assignments in each, the sums over the
-// CTAs' counts.  262144 assignments to 256 experts 10.2 us in a graph, 128 to 16
-// 3.7; a thread's loads four at a time in place of one by one took 2.7 us off.
+// CTAs' counts.  262144 assignments to 256 experts 8.9 us in a graph, 128 to 16
+// 2.7.  What helped: a thread's loads four at a time (2.7 us off), four experts'
+// counts a load and the starts by all warps (0.7), the first batch kept (0.4).
 //
 // The other three go by tokens, so that a token's row is read or written once
 // however many experts it has, and each expert's row once.  Bound by memory:
 // 16384 tokens x 2 rows of 4096 bf16 values, dispatch and its gradient 124 us
 // (800 MB, 6.4 TB/s, 0.95 of the copy rate), combine and both gradients 166 us
-// (1070 MB in the two calls, 6.5 TB/s).
+// (1070 MB in the two calls, 6.5 TB/s).  Rows that start anywhere take a quarter
+// to three quarters longer (4095 columns: dispatch 91, combine 120 us, its gradient
+// 152; whole words 61, 67 and 102): each is read in words that are shifted into place.
 #include <algorithm>
 #include <climits>
 #include <cstdint>
@@ -223,14 +226,25 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
 // --------------------------------------------- rows to their experts and back
 
 constexpr int kMoveThreads = 256;
-constexpr int kSteps = 2;          // eight columns each that a thread has on its way
-// CTAs of the gradient that an SM is to hold, which bounds their registers: five
-// where whole words of 16-bit values and at most two assignments are on their way
-// (16384 x 2 rows of 4096: 106 us with four), as it comes elsewhere.  (Combine
-// itself, held to as many, spills: 82 us in place of 70.)
-template <bool kWhole, typename TX, typename TY, int kJ>
-constexpr int resident() { return kWhole && sizeof(TX) == 2 && sizeof(TY) == 2 && kJ <= 2 ? 5 : 2; }
-constexpr int kMaxCols = 65535 * kMoveThreads * 8 * kSteps - 8;   // a grid's second extent
+// Groups of eight columns that a thread has on its way: two, but one in combine
+// where rows start anywhere (9761 x 8 rows of 1268 87 us, 102 with two).
+constexpr int kSteps = 2;
+__host__ __device__ constexpr int combine_steps(bool whole) { return whole ? kSteps : 1; }
+// CTAs an SM is to hold, which bounds their registers.  Where rows start anywhere and
+// hold 16 bits, eight (9761 x 8 rows of 1268: combine 70 us, 79 without a bound; its
+// gradient 139, 149 with five).  Where they do not and at most two assignments are on
+// their way, four of combine (16384 x 2 rows of 4096: 67 us, 77 with the registers of
+// three, 82 with five, which spills; three of fp32 rows, which take more) and five of
+// the gradient (102; 106 with four).
+template <bool kWhole, bool kGrad, typename TX, typename TY, int kJ>
+constexpr int resident() {
+    constexpr bool kHalf = sizeof(TX) == 2 && sizeof(TY) == 2;
+    if (kJ > 2) return 2;
+    if (!kWhole) return kHalf ? 8 : 2;
+    if (kGrad) return kHalf ? 5 : 2;
+    return sizeof(TX) == 2 ? 4 : 3;
+}
+constexpr int kMaxCols = 65535 * kMoveThreads * 8 - 8;   // a grid's second extent
 
 struct Rows {
     const void* y;      // tokens' side: read by dispatch and the gradient, written by combine
@@ -259,10 +273,10 @@ struct Place {
     long long t;
     int g0;
 };
-__device__ __forceinline__ Place place_of(const Rows& p) {
+__device__ __forceinline__ Place place_of(const Rows& p, int steps) {
     const int slot = threadIdx.x / p.lanes;
     return {static_cast<long long>(blockIdx.x) * (kMoveThreads / p.lanes) + slot,
-            static_cast<int>(blockIdx.y) * p.lanes * kSteps + static_cast<int>(threadIdx.x) - slot * p.lanes};
+            static_cast<int>(blockIdx.y) * p.lanes * steps + static_cast<int>(threadIdx.x) - slot * p.lanes};
 }
 
 // The first column of group g of a row that is written: at or before it.
@@ -296,7 +310,7 @@ __device__ __forceinline__ Raw8<TX> as_type(const Raw8<TY>& r) {
 template <bool kWhole, typename TY, typename TX>
 __global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const __grid_constant__ Rows p) {
     tcg::host::wait_for_kernel_ahead();
-    const Place w = place_of(p);
+    const Place w = place_of(p, kSteps);
     if (w.t >= p.tokens) return;
     const TY* src = static_cast<const TY*>(p.y) + w.t * p.ldy;
     Raw8<TX> v[kSteps];
@@ -321,23 +335,26 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const __grid_con
     }
 }
 
-// kJ assignments' rows are on their way at once; sums in the order of j.
+// kJ assignments' rows are on their way at once; sums in the order of j.  (Rows that
+// start anywhere: one, whose shifting takes the registers; 9761 x 8 rows of 1268 83
+// us and 108 with two, the gradient 203 and 255.)
 template <bool kWhole, typename TX, typename TY, int kJ>
-__global__ void __launch_bounds__(kMoveThreads) combine_kernel(const __grid_constant__ Rows p) {
+__global__ void __launch_bounds__(kMoveThreads, resident<kWhole, false, TX, TY, kJ>()) combine_kernel(const __grid_constant__ Rows p) {
     tcg::host::wait_for_kernel_ahead();
-    const Place w = place_of(p);
+    constexpr int kS = combine_steps(kWhole);
+    const Place w = place_of(p, kS);
     if (w.t >= p.tokens) return;
     TY* dst = static_cast<TY*>(p.out) + w.t * p.ldo;
-    int col[kSteps];
+    int col[kS];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) col[s] = column_of<kWhole>(dst, w.g0 + s * p.lanes);
-    float acc[kSteps][8];
+    for (int s = 0; s < kS; ++s) col[s] = column_of<kWhole>(dst, w.g0 + s * p.lanes);
+    float acc[kS][8];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+    for (int s = 0; s < kS; ++s)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[s][i] = 0.0f;
     for (int j0 = 0; j0 < p.k; j0 += kJ) {
-        Raw8<TX> v[kJ][kSteps];
+        Raw8<TX> v[kJ][kS];
         int row[kJ];
         float wt[kJ];
 #pragma unroll
@@ -348,13 +365,13 @@ __global__ void __launch_bounds__(kMoveThreads) combine_kernel(const __grid_cons
 #pragma unroll
         for (int q = 0; q < kJ; ++q)
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
+            for (int s = 0; s < kS; ++s) {
                 if (row[q] >= 0 && col[s] < p.cols) v[q][s] = fetch<kWhole, TX>(static_cast<const TX*>(p.x) + row[q] * p.ldx, col[s], p.cols);
             }
 #pragma unroll
         for (int q = 0; q < kJ; ++q)
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
+            for (int s = 0; s < kS; ++s) {
                 if (row[q] < 0 || col[s] >= p.cols) continue;
                 float f[8];
                 values_of<TX>(v[q][s], f);
@@ -363,14 +380,14 @@ __global__ void __launch_bounds__(kMoveThreads) combine_kernel(const __grid_cons
             }
     }
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+    for (int s = 0; s < kS; ++s)
         if (col[s] < p.cols) store_any8<TY>(dst, col[s], p.cols, raw_of<TY>(acc[s]));
 }
 
 // p.lanes threads a token (a power of two from 32 on), over all its columns;
 // kJ assignments at a time, whose weights' gradients are summed in a fixed order.
 template <bool kWhole, typename TX, typename TY, int kJ>
-__global__ void __launch_bounds__(kMoveThreads, resident<kWhole, TX, TY, kJ>()) combine_grad_kernel(const __grid_constant__ Rows p) {
+__global__ void __launch_bounds__(kMoveThreads, resident<kWhole, true, TX, TY, kJ>()) combine_grad_kernel(const __grid_constant__ Rows p) {
     tcg::host::wait_for_kernel_ahead();
     __shared__ float part[kJ][kMoveThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -482,12 +499,18 @@ int lanes_for(int cols, int steps) {
     while (lanes < want && lanes < kMoveThreads) lanes *= 2;
     return lanes;
 }
-dim3 move_grid(const Rows& p, bool whole) {
+dim3 move_grid(const Rows& p, bool whole, int steps) {
     // (a row that starts anywhere may take a group more)
-    const int per_cta = kMoveThreads / p.lanes, span = p.lanes * 8 * kSteps;
+    const int per_cta = kMoveThreads / p.lanes, span = p.lanes * 8 * steps;
     return dim3(static_cast<unsigned>((static_cast<long long>(p.tokens) + per_cta - 1) / per_cta),
                 static_cast<unsigned>((static_cast<long long>(p.cols) + (whole ? 0 : 7) + span - 1) / span));
 }
+
+// Whether all CTAs run at once with four assignments' rows on their way, whose
+// registers let two be on an SM: then four, where there are as many, else two
+// (4096 columns, 8 rows a token: combine of 256 tokens 5.8 us with four and 6.6
+// with two, of 512 10.1 and 7.8; its gradient of 512 17 and 23, of 1024 32 and 30).
+bool few(dim3 grid, int sms) { return static_cast<long long>(grid.x) * grid.y <= 2LL * sms; }
 
 tcg_status launched(cudaError_t e, const char* what) { return e == cudaSuccess ? TCG_OK : tcg::host::fail_launch(what, e); }
 
@@ -568,7 +591,7 @@ tcg_status tcg_moe_dispatch(int tokens, int k, int cols, int rows, const void* x
     with_type(x_dtype, [&](auto y) {
         with_type(out_dtype, [&](auto o) {
             const auto kernel = whole ? dispatch_kernel<true, decltype(y), decltype(o)> : dispatch_kernel<false, decltype(y), decltype(o)>;
-            err = tcg::host::launch_early(kernel, move_grid(p, whole), kMoveThreads, static_cast<cudaStream_t>(stream), p);
+            err = tcg::host::launch_early(kernel, move_grid(p, whole, kSteps), kMoveThreads, static_cast<cudaStream_t>(stream), p);
         });
     });
     return launched(err, "tcg_moe_dispatch");
@@ -593,16 +616,17 @@ tcg_status tcg_moe_combine(int tokens, int k, int cols, int rows, const void* x,
     p.out = y;
     p.ldo = ldy;
     const bool whole = whole_words(x, ldx, x_dtype) && whole_words(y, ldy, y_dtype);
-    p.lanes = lanes_for(cols, kSteps);
+    p.lanes = lanes_for(cols, combine_steps(whole));
+    const dim3 grid = move_grid(p, whole, combine_steps(whole));
     cudaError_t err = cudaSuccess;
     with_type(x_dtype, [&](auto a) {
         with_type(y_dtype, [&](auto b) {
             const auto run = [&](auto* kernel) {
-                err = tcg::host::launch_early(kernel, move_grid(p, whole), kMoveThreads, static_cast<cudaStream_t>(stream), p);
+                err = tcg::host::launch_early(kernel, grid, kMoveThreads, static_cast<cudaStream_t>(stream), p);
             };
-            if (!whole) run(combine_kernel<false, decltype(a), decltype(b), 2>);
+            if (!whole) run(combine_kernel<false, decltype(a), decltype(b), 1>);
             else if (k == 1) run(combine_kernel<true, decltype(a), decltype(b), 1>);
-            else if (k == 2) run(combine_kernel<true, decltype(a), decltype(b), 2>);
+            else if (k == 2 || !few(grid, dev.num_sms)) run(combine_kernel<true, decltype(a), decltype(b), 2>);
             else run(combine_kernel<true, decltype(a), decltype(b), 4>);
         });
     });
@@ -647,9 +671,9 @@ tcg_status tcg_moe_combine_backward(int tokens, int k, int cols, int rows, const
             const auto run = [&](auto* kernel) {
                 err = tcg::host::launch_early(kernel, grid, kMoveThreads, static_cast<cudaStream_t>(stream), p);
             };
-            if (!whole) run(combine_grad_kernel<false, decltype(a), decltype(b), 2>);
+            if (!whole) run(combine_grad_kernel<false, decltype(a), decltype(b), 1>);
             else if (k == 1) run(combine_grad_kernel<true, decltype(a), decltype(b), 1>);
-            else if (k == 2) run(combine_grad_kernel<true, decltype(a), decltype(b), 2>);
+            else if (k == 2 || !few(grid, dev.num_sms)) run(combine_grad_kernel<true, decltype(a), decltype(b), 2>);
             else run(combine_grad_kernel<true, decltype(a), decltype(b), 4>);
         });
     });
