@@ -8,8 +8,9 @@ the sum of |x w|.  lse moves by no more than the largest |dz|; its exponentials
 are good to 2^-22 and their arguments to 2 u of the distance from the maximum,
 its sums are 40 additions in line in a thread and 8 + V / 4096 between them.
 The gradients sum dz over words or tokens in the same way, dz being off by half
-a step of its type, by the relative error of p, and by 4 u; fp16 adds half a
-step of its smallest numbers (2^-25 of 2^14 times the largest weight).
+a step of its type, by the relative error of p, by 4 u, and by u of grad_mean / n
+where grad_loss is added to that; fp16 adds half a step of its smallest numbers
+(2^-25 of 2^14 times the largest weight).
 """
 import pytest
 import torch
@@ -128,6 +129,10 @@ class Case:
         dz = r[:, None] * (p - hit)
         rel = float(self.lse_error(z, lse, S).max()) + self.z_error(S) + 8 * U + 2.0 ** -22   # of p
         off = half_step(self.dtype) * dz.abs() * 1.01 + r.abs()[:, None] * (p * rel * 1.01 + 4 * U * (p + hit))
+        if grad_mean is not None:
+            # r = fl(fl(g / n) + l): the quotient's rounding is u |g / n| whatever the sum is, which may be far smaller
+            # than both where l is about -g / n; the sum's own and what follows are the 4 u of r above
+            off += torch.where(self.live, U * abs(float(grad_mean)) / max(n, 1), 0.0)[:, None] * (p + hit)
         if self.dtype == "f16":
             off += float(r.abs().max()) * 2.0 ** -39
         size = dz.abs() + off
@@ -149,7 +154,7 @@ class Case:
 
 
 SIZES = [(1, 1, 8), (1, 100, 64), (3, 7, 5), (2, 300, 72), (64, 1000, 200), (128, 257, 96), (129, 500, 136), (257, 1030, 72), (256, 256, 64),
-         (300, 5000, 1100), (40, 700, 1600), (130, 513, 4104), (700, 3001, 1537), (5, 40000, 256)]
+         (300, 5000, 1100), (40, 700, 1600), (130, 513, 4104), (700, 3001, 1537), (5, 40000, 256), (64, 40000, 1290)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -177,6 +182,15 @@ def test_a_vocabulary_in_several_pieces(dtype):
     c.check_backward(gx, gw, gm, None)
     a, b = c.backward("f32", "f32", gm, beta=1.0, old=torch.ones(140011, 64, device="cuda"))
     c.check_backward(a, b, gm, None, 1.0, torch.ones(140011, 64, device="cuda"))
+
+
+def test_a_vocabulary_in_many_pieces():
+    c = Case(5000, 160011, 72, ignored=0.1)
+    c.forward()
+    c.check_forward()
+    gm = torch.ones(1, device="cuda")
+    gx, gw = c.backward("bf16", "bf16", gm, pad=8)
+    c.check_backward(gx, gw, gm, None)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -393,7 +407,7 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_exact(T):
     c.check_forward()
 
 
-@pytest.mark.parametrize("V", [600, 100003])
+@pytest.mark.parametrize("V", [600, 150003])
 def test_a_workspace_that_starts_on_any_16_bytes(V):
     c = Case(70 if V < 1000 else 2000, V, 72)
     want = []
