@@ -30,8 +30,10 @@ namespace {
 
 using tcg::xent::Params;
 
-// What dz of a piece may take of the workspace.
-constexpr size_t kPieceBytes = size_t(256) << 20;
+// What dz of a piece may take of the workspace: the fewer pieces, the fewer last
+// waves and sums of dX (backward of 8192 x 100000 x 512 1.80 ms; 2.27 with 64 MB, 1.92
+// with 256, 1.70 with 1 GB; of 4096 x 65536 x 4096 3.74, 3.91, 3.74 and 3.75).
+constexpr size_t kPieceBytes = size_t(512) << 20;
 constexpr int kMinTileN = 128;
 constexpr int kPartK = 1024;           // k of the statistics' products that the tensor cores sum in one go, about
 constexpr int kFinishRows = 32, kFinishSlices = 32, kFinishThreads = kFinishRows * kFinishSlices;
@@ -159,8 +161,10 @@ struct Plan {
     int tile_n = 256, num_m = 1, num_n = 1, workers = 1;
 };
 
-// The width whose waves of tiles take the least: a tile's time goes with its
-// columns, plus what a tile costs by itself (about sixteen columns' worth).
+// A pair of CTAs a tile where one CTA's rows do not hold all tokens (128 x 32768 x
+// 4096 51.6 us, 56.7 with pairs; 129 56.0, 63.4 without).  The width whose waves of
+// tiles take the least: a tile's time goes with its columns, plus what a tile costs
+// by itself (about sixteen columns' worth).
 Plan make_plan(int tokens, long long cols, int hidden, bool grad, int sms) {
     Plan pl;
     pl.pair = tokens > tcg::xent::kBM;
@@ -189,6 +193,17 @@ int piece_words(int tokens, int vocab) {
 
 // a counter for each warp of both CTAs of a split tile
 constexpr long long kMaxSplitTiles = tcg::host::kCounterBytes / sizeof(int) / (2 * tcg::xent::kRowWarps);
+
+// Columns of the products' tiles.  128 where hidden has no more, and where dX has
+// so few tiles that their long sums and the joining of their pieces are the time,
+// of which half as wide ones take half (256 x 32768 x 1024, four tiles: backward 68
+// us, 79 with 256; 512 x 32768 x 512 63 and 72).  Elsewhere a stage or a tile's way
+// to memory takes three quarters as long at half the width (1000 x 50021 x 512,
+// eight: 147 and 125; 1000 x 50021 x 1280 311 and 235).
+int product_columns(int tokens, int hidden, bool want_dx) {
+    const long long tiles = blocks(tokens, 2 * tcg::xent::kBM) * blocks(hidden, 256);
+    return hidden <= 128 || (want_dx && tiles <= 4) ? 128 : 256;
+}
 
 // How dX's and dW's tiles go to the workers (pairs of CTAs).
 struct ProductPlan {
@@ -487,7 +502,7 @@ tcg_status tcg_linear_xent_backward(int tokens, int vocab, int hidden, tcg_dtype
             if (st == TCG_OK) st = tcg::host::map_bytes(&q.q[1].b, X, 2ull * hidden, tokens, 2ull * ldx, tcg::xent::kRowBytes, tcg::xent::kStageK);
             if (st != TCG_OK) return st;
         }
-        q.tile_n = hidden <= 128 ? 128 : 256;
+        q.tile_n = product_columns(tokens, hidden, dX != nullptr);
         q.fmt = dtype == TCG_F16 ? 0u : 1u;
         q.back = tokens > 0 ? back : nullptr;
         q.partials = reinterpret_cast<float*>(ws + l.partials);
