@@ -1,0 +1,94 @@
+"""Softmax cross entropy of a linear layer: what its gradients take from the
+forward call.
+
+Tolerances as in test_linear_xent_gpu.py (u = 2^-24).  The logits' sums are taken
+in parts of at most 1536 k, cut after every 16 (at most 2^-22 of the part's
+magnitudes a step), and the parts are added with a rounding each: a logit is off by
+no more than ((1536 + 128) / 16 2^-22 + (H / 1024 + 2) u) S.
+"""
+import pytest
+import torch
+
+import tiled_tensor_core_persistent_gb300 as tcg
+
+from block128 import TYPE
+from test_linear_xent_gpu import U, Case, half_step
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from tiled_tensor_core_persistent_gb300 import _build
+    _build.build()
+    tcg.debug_set()
+    yield
+    tcg.debug_set()
+
+
+def sure(T, V, H, dtype, unlikely=1e-4):
+    """Every token's hidden state lies along its target's weights, so that all other words together have about
+    `unlikely`; the products of the target's logit are all of one sign.  W's first column is 1 (and X's 0): the first
+    column of dX is the sum of dz over the words, which is 0."""
+    c = Case(T, V, H, dtype, ignored=0.0)
+    w = torch.randn(V, H, generator=c.gen, device="cuda") * (2.0 / H ** 0.5)
+    w[:, 0] = 1.0
+    c.w = c.held(w)
+    at = c.w[c.target.long(), :H].float()
+    at[:, 0] = 0.0
+    z = torch.log(torch.tensor(V / unlikely))
+    c.x = c.held(at * (z.cuda() / (at * at).sum(1, keepdim=True)))
+    return c
+
+
+def sum_error(H, S):
+    return ((1536 + 128) / 16 * 2.0 ** -22 + (H / 1024 + 2) * U) * S
+
+
+LONG = [(100, 300, 131080), (200, 300, 131080)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,V,H", LONG)
+def test_long_sums_of_one_sign(T, V, H, dtype):
+    """Sums of 131080 products in one go are about five times this bound too near zero."""
+    c = sure(T, V, H, dtype)
+    c.forward()
+    _, lse, loss, _, S = c.exact()
+    # (exponentials, their sums and the join: a probability that is all but 1)
+    err = sum_error(H, S) + 2.0 ** -22 + 60 * U + U * lse.abs()
+    assert bool(((c.lse[:T].double() - lse).abs() <= err).all()), float(((c.lse[:T].double() - lse).abs() - err).max())
+    # the loss is lse less the target's logit, which are off together
+    assert bool(((c.loss[:T].double() - loss).abs() <= 2 * sum_error(H, S) * loss + 2.0 ** -22 + 60 * U + 2 * U * lse.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T,V,H", LONG)
+def test_gradients_of_what_is_all_but_certain(T, V, H, dtype):
+    """exp(z - lse) of a target of probability p is off by (1 - p) times what z is off, as lse is off with it, plus
+    roundings of lse (here and times log2 e): the gradient takes the same sums as the loss."""
+    c = sure(T, V, H, dtype)
+    c.forward()
+    z, lse, _, n, S = c.exact()
+    gm = torch.full((1,), float(n), device="cuda")      # every token's weight is 1
+    gx, gw = c.backward("f32", "f32", gm)
+    p = torch.exp(z - lse[:, None])
+    rows, y = torch.arange(T, device="cuda"), c.target.long()
+    rest = p.clone()
+    rest[rows, y] = 0.0
+    rest = rest.sum(1)                                  # 1 - p of the target
+    assert 1e-5 < float(rest.min()) and float(rest.max()) < 1e-3
+    dz = p.clone()
+    dz[rows, y] = -rest
+    arg = 2 * U * lse.abs() + 2 * 2.0 ** -22 + 16 * U   # roundings of lse and of its multiple, the exponentials here and there
+    off = p * (2 * sum_error(H, S) + arg[:, None])
+    off[rows, y] = rest * 2 * sum_error(H, S) + arg + 4 * U
+    off = off * 1.01 + half_step(dtype) * (dz.abs() + off) * 1.01 + (2.0 ** -39 if dtype == "f16" else 0.0)
+    x, w = c.x[:, :H].double(), c.w[:, :H].double()
+    size = dz.abs() + off
+    for got, ref, bound in ((gx, dz @ w, off @ w.abs() + (V / 16 + 40) * 2.0 ** -22 * (size @ w.abs())),
+                            (gw, dz.t() @ x, off.t() @ x.abs() + (T / 16 + 40) * 2.0 ** -22 * (size.t() @ x.abs()))):
+        bound = bound + 5 * U * ref.abs() + 2.0 ** -120
+        assert bool(((got.double() - ref).abs() <= bound).all()), float(((got.double() - ref).abs() / bound).max())

@@ -35,7 +35,7 @@ using tcg::xent::Params;
 // with 256, 1.70 with 1 GB; of 4096 x 65536 x 4096 3.74, 3.91, 3.74 and 3.75).
 constexpr size_t kPieceBytes = size_t(512) << 20;
 constexpr int kMinTileN = 128;
-constexpr int kPartK = 1024;           // k of the statistics' products that the tensor cores sum in one go, about
+constexpr int kPartK = 1024;           // k of the logits' products that the tensor cores sum in one go, about
 constexpr int kFinishRows = 32, kFinishSlices = 32, kFinishThreads = kFinishRows * kFinishSlices;
 constexpr int kFinishBatch = 8;
 constexpr float kHalfTop = 16384.0f;   // fp16: what the largest |r_t| becomes
@@ -165,10 +165,10 @@ struct Plan {
 // 4096 51.6 us, 56.7 with pairs; 129 56.0, 63.4 without).  The width whose waves of
 // tiles take the least: a tile's time goes with its columns, plus what a tile costs
 // by itself (about sixteen columns' worth).
-Plan make_plan(int tokens, long long cols, int hidden, bool grad, int sms) {
+Plan make_plan(int tokens, long long cols, int hidden, int sms) {
     Plan pl;
     pl.pair = tokens > tcg::xent::kBM;
-    pl.parts = grad ? 1 : std::max(1, (hidden + kPartK / 2) / kPartK);
+    pl.parts = std::max(1, (hidden + kPartK / 2) / kPartK);
     pl.num_m = static_cast<int>(blocks(tokens, pl.pair ? 256 : 128));
     const int workers = std::max(1, pl.pair ? sms / 2 : sms);
     long long best = LLONG_MAX;
@@ -331,7 +331,7 @@ tcg_status launch_plan(const Params& p, const Plan& pl, cudaStream_t stream) {
 template <bool kGrad>
 tcg_status launch_tiles(Params& p, tcg_dtype dtype, const void* X, int ldx, const void* W, int ldw, int tokens, int hidden,
                         int first, int cols, const tcg::host::Device& dev, cudaStream_t stream) {
-    const Plan pl = make_plan(tokens, cols, hidden, kGrad, dev.num_sms);
+    const Plan pl = make_plan(tokens, cols, hidden, dev.num_sms);
     const int atoms = pl.pair ? tcg::xent::Shape<true>::kAtoms : tcg::xent::Shape<false>::kAtoms;
     p.tokens = tokens;
     p.cols = cols;
