@@ -1,5 +1,5 @@
 """Softmax cross entropy of a linear layer: what its gradients take from the
-forward call.
+forward call, and tokens' weights that are not finite.
 
 Tolerances as in test_linear_xent_gpu.py (u = 2^-24).  The logits' sums are taken
 in parts of at most 1536 k, cut after every 16 (at most 2^-22 of the part's
@@ -92,3 +92,27 @@ def test_gradients_of_what_is_all_but_certain(T, V, H, dtype):
                             (gw, dz.t() @ x, off.t() @ x.abs() + (T / 16 + 40) * 2.0 ** -22 * (size.t() @ x.abs()))):
         bound = bound + 5 * U * ref.abs() + 2.0 ** -120
         assert bool(((got.double() - ref).abs() <= bound).all()), float(((got.double() - ref).abs() / bound).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("weight", [float("inf"), float("-inf"), float("nan")])
+def test_a_weight_that_is_not_finite_leaves_other_tokens_alone(weight, dtype):
+    """dz is held over the largest weight that is finite: the others' gradients are as without that token."""
+    c = Case(260, 700, 72, dtype, ignored=0.1)
+    c.target[131] = 5
+    c.live[131] = True
+    c.forward()
+    for size in (1e-9, 20.0):
+        gl = torch.randn(260, generator=c.gen, device="cuda") * size
+        gl[131] = 0.0
+        want, _ = c.backward("f32", "f32", None, gl)
+        want = want.clone()
+        gl[131] = weight
+        got, gw = c.backward("f32", "f32", None, gl)
+        others = torch.arange(260, device="cuda") != 131
+        assert torch.equal(got[others], want[others]) and bool(want[others].isfinite().all())
+        assert not bool(got[131].isfinite().any())
+        gl[~c.live] = weight                            # of tokens that do not count: nothing
+        gl[131] = 0.0
+        again, _ = c.backward("f32", "f32", None, gl)
+        assert torch.equal(again, want)

@@ -13,7 +13,7 @@
 // launch (xent_product_kernel.cuh) takes it to dX (summed over the pieces in
 // fp32) and dW.  One rounding of dz to 16 bits stands between the logits and the
 // gradients, of the same size as that of a 16-bit gradient: the other products
-// would need fp32 operands.  What is rounded is dz over the largest |r_t|, which
+// would need fp32 operands.  What is rounded is dz over the largest finite |r_t|, which
 // the products multiply by: where all tokens weigh alike, dz of an unlikely
 // target is then a number just above -1, which 16 bits hold to 2^-9 of itself or
 // exactly, where r_t times it would be off by the same part of a step for every

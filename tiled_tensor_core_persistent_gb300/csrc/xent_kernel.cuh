@@ -87,7 +87,7 @@ struct Params {
     const float* grad_mean;             // may be nullptr
     const float* grad_loss;             // [tokens], may be nullptr
     int vocab;                          // targets in [0, vocab) count
-    float top;                          // what the largest |r_t| becomes in d
+    float top;                          // what the largest finite |r_t| becomes in d
     float* back;                        // what undoes that
     void* d;
     long long ldd;                      // a multiple of 32
@@ -393,15 +393,16 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
         const int half = (warp - kControlWarps) >> 2, hw = p.tile_n / 2;   // the columns [half * hw, half * hw + hw) of a tile
         float each = 0.0f, to_top = 1.0f;
         if constexpr (kGrad) {
-            // the largest |r_t|, by every CTA for itself while its first products run
+            // the largest |r_t| that is finite, by every CTA for itself while its first products run
             const int count = *p.valid;
             each = p.grad_mean && count > 0 ? *p.grad_mean / static_cast<float>(count) : 0.0f;
             float most = fabsf(each);
             if (p.grad_loss) {
-                most = 0.0f;   // (fmaxf passes over NaN: such a token leaves the others' scale alone)
+                most = 0.0f;   // (a token whose weight is not finite leaves the others' scale alone)
                 for (int t = static_cast<int>(threadIdx.x) - 32 * kControlWarps; t < p.tokens; t += 32 * kRowWarps) {
                     const int y = p.target[t];
-                    if (y >= 0 && y < p.vocab) most = fmaxf(most, fabsf(each + p.grad_loss[t]));
+                    const float r = fabsf(each + p.grad_loss[t]);
+                    if (y >= 0 && y < p.vocab && r < INFINITY) most = fmaxf(most, r);
                 }
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
