@@ -1,5 +1,5 @@
 """Softmax cross entropy of a linear layer: what its gradients take from the
-forward call, and tokens' weights that are not finite.
+forward call, tokens' weights that are not finite, and very long sums.
 
 Tolerances as in test_linear_xent_gpu.py (u = 2^-24).  The logits' sums are taken
 in parts of at most 1536 k, cut after every 16 (at most 2^-22 of the part's
@@ -116,3 +116,45 @@ def test_a_weight_that_is_not_finite_leaves_other_tokens_alone(weight, dtype):
         gl[131] = 0.0
         again, _ = c.backward("f32", "f32", None, gl)
         assert torch.equal(again, want)
+
+
+class Spread(Case):
+    """A case of 64 hidden values that stand in `hidden` columns, all others 0 (the first and the last are among them)."""
+
+    def __init__(self, T, V, hidden):
+        super().__init__(T, V, 64, ignored=0.2)
+        self.hidden = hidden
+        at = torch.randint(1, hidden - 1, (64,), generator=self.gen, device="cuda").unique()
+        assert at.numel() == 64
+        at[0], at[-1] = 0, hidden - 1
+        self.at = at
+        self.wide = [torch.zeros(m.shape[0], -(-hidden // 8) * 8, dtype=m.dtype, device="cuda") for m in (self.x, self.w)]
+        for big, m in zip(self.wide, (self.x, self.w)):
+            big[:, at] = m[:, :64]
+        self.bytes = tcg.linear_xent_workspace_size(T, V, hidden, True)
+        self.ws = torch.zeros(self.bytes, dtype=torch.uint8, device="cuda")
+
+    def z_error(self, S):
+        return (64 + 3) * 2.0 ** -22 * S + 64 * U * S     # zeros cut nothing
+
+
+@pytest.mark.parametrize("T,V,H", [(3, 5, 12_000_008), (130, 6, 16_800_001)])
+def test_hidden_sizes_of_many_millions(T, V, H):
+    """Stages of K times parts of K pass 2^31; one CTA a tile, and a pair."""
+    if torch.cuda.get_device_properties(0).total_memory < 100 << 30:
+        pytest.skip("needs 20 GB")
+    c = Spread(T, V, H)
+    x, w = c.wide
+    ld = x.shape[1]
+    tcg.linear_xent(T, V, H, "bf16", x, ld, w, ld, c.target, c.lse, c.loss, c.mean, c.valid, workspace=c.ws, workspace_bytes=c.bytes)
+    c.check_forward()
+    gm = torch.ones(1, device="cuda")
+    gx, gw = torch.full_like(x, 5.0), torch.full_like(w, 5.0)
+    tcg.linear_xent_backward(T, V, H, "bf16", x, ld, w, ld, c.target, c.lse, c.valid, gm, None, gx, ld, "bf16", 0.0, gw, ld, "bf16",
+                             workspace=c.ws, workspace_bytes=c.bytes)
+    assert tcg.device_status(c.ws) == 0
+    c.check_backward(gx[:, c.at], gw[:, c.at], gm, None)
+    for g in (gx, gw):
+        assert bool((g[:, H:] == 5).all())
+        g[:, c.at] = 0
+        assert not bool(g[:, :H].any())

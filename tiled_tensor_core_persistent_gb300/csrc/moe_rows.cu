@@ -28,6 +28,7 @@
 #include <cstdint>
 
 #include "host.h"
+#include "split.cuh"
 #include "values.cuh"
 
 namespace {
@@ -66,10 +67,6 @@ struct Sort {
 
 // A CTA's counts start on 16 bytes (what lies past the experts is never used).
 __host__ __device__ __forceinline__ int pitch_of(int experts) { return (experts + 3) & ~3; }
-
-__device__ __forceinline__ int run_start(int total, int part, int parts) {
-    return static_cast<int>(static_cast<long long>(total) * part / parts);
-}
 
 struct Assignment {
     int t, j, e;   // e: -1 where it has no expert

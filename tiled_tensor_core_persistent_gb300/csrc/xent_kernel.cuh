@@ -49,6 +49,7 @@
 
 #include "host.h"
 #include "ptx.cuh"
+#include "split.cuh"
 #include "values.cuh"
 
 namespace tcg {
@@ -335,18 +336,18 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
             const bool issuer = lane == 0;
             const uint32_t idesc = (1u << 4) | (p.fmt << 7) | (p.fmt << 10) | (static_cast<uint32_t>(p.tile_n >> 3) << 17) |
                                    (static_cast<uint32_t>(S::kTileM >> 4) << 24);
-            const int mine = (tiles - worker + workers - 1) / workers * p.parts;   // accumulations
-            int stage = 0, part = 0;
+            const long long mine = static_cast<long long>((tiles - worker + workers - 1) / workers) * p.parts;   // accumulations
+            int stage = 0;
             uint32_t phase = 0;
             Ring acc;
+            Pieces of(p.num_kb, p.parts);
             bool ok = true, issued = false;
-            for (int u = 0; ok && u < mine; ++u) {
-                const int kb0 = p.num_kb * part / p.parts, kb1 = p.num_kb * (part + 1) / p.parts;
-                if (++part == p.parts) part = 0;
+            for (long long u = 0; ok && u < mine; ++u) {
+                of.next();
                 if (!wait(&ctl->tmem_empty[acc.at], acc.phase ^ 1u, p, ctl, 2)) break;
                 ptx::tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc.at * kAccCols);
-                for (int kb = kb0; kb < kb1; ++kb) {
+                for (int kb = of.begin; kb < of.end; ++kb) {
                     if (!wait(&ctl->full[stage], phase, p, ctl, 3)) { ok = false; break; }
                     ptx::tc_fence_after_sync();
                     if (issuer) {
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                             // four MMAs of 32 bytes of K an atom; descriptors count 16-byte units
                             const uint64_t ad = a_desc + static_cast<uint64_t>(((k / 4) * kBM * kRowBytes + (k % 4) * 32) >> 4);
                             const uint64_t bd = b_desc + static_cast<uint64_t>(((k / 4) * S::kBRows * kRowBytes + (k % 4) * 32) >> 4);
-                            const uint32_t accum = (kb > kb0 || k > 0) ? 1u : 0u;
+                            const uint32_t accum = (kb > of.begin || k > 0) ? 1u : 0u;
                             if constexpr (kPair) ptx::mma_f16_pair(d_tmem, ad, bd, idesc, accum);
                             else ptx::mma_f16(d_tmem, ad, bd, idesc, accum);
                         }

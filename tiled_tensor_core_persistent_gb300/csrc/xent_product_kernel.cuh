@@ -127,8 +127,8 @@ struct Span {
 __device__ __forceinline__ Span span_of(const Products& p, const Unit& v) {
     const int num_kb = TCG_OF(p, v, num_kb), splits = TCG_OF(p, v, splits), num_n = TCG_OF(p, v, num_n);
     Span s;
-    s.kb0 = splits == 1 ? 0 : static_cast<int>(static_cast<long long>(num_kb) * v.split / splits);
-    s.kb1 = splits == 1 ? num_kb : static_cast<int>(static_cast<long long>(num_kb) * (v.split + 1) / splits);
+    s.kb0 = splits == 1 ? 0 : run_start(num_kb, v.split, splits);
+    s.kb1 = splits == 1 ? num_kb : run_start(num_kb, v.split + 1, splits);
     s.m = v.tile / num_n;
     s.n = v.tile - s.m * num_n;
     return s;
