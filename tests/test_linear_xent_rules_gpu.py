@@ -158,3 +158,29 @@ def test_hidden_sizes_of_many_millions(T, V, H):
         assert bool((g[:, H:] == 5).all())
         g[:, c.at] = 0
         assert not bool(g[:, :H].any())
+
+
+@pytest.mark.parametrize("T,V,H,split", [(40, 3000, 128, True), (600, 3000, 128, True), (33, 30000, 1032, True), (2048, 140011, 64, False)])
+def test_a_wait_of_the_gradient_that_runs_out_is_reported_and_the_next_call_is_exact(T, V, H, split):
+    """In the kernel of dz and in that of the products, whose split tiles are left with counters that count; one piece of
+    the vocabulary and two."""
+    c = Case(T, V, H)
+    c.forward()
+    gm = torch.ones(1, device="cuda")
+    want = [g.clone() for g in c.backward("bf16", "bf16", gm)]
+    gx, gw = torch.empty(T, H, dtype=torch.bfloat16, device="cuda"), torch.empty(V, H, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    tcg.debug_set(fault_inject=1, wait_timeout_ns=20_000_000)
+    tcg.linear_xent_backward(T, V, H, "bf16", c.x, c.ld, c.w, c.ld, c.target, c.lse, c.valid, gm, None, gx, H, "bf16", 0.0, gw, H, "bf16",
+                             workspace=c.ws, workspace_bytes=c.bytes)
+    torch.cuda.synchronize()
+    counters = c.ws[256:256 + 8192]
+    assert bool(counters.any()) or not split
+    assert tcg.device_status(c.ws) == 7
+    tcg.debug_set()
+    assert not bool(counters.any())
+    got = c.backward("bf16", "bf16", gm)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    c.forward()
+    c.check_forward()
+    c.check_backward(*got, gm, None)
