@@ -30,8 +30,9 @@ namespace {
 
 using tcg::xent::Params;
 
-// What dz of a piece may take of the workspace: the fewer pieces, the fewer last
-// waves and sums of dX (backward of 8192 x 100000 x 512 1.80 ms; 2.27 with 64 MB, 1.92
+// What dz of a piece may take of the workspace (more only where 256 words, a piece's
+// least, do: from 2^20 tokens on): the fewer pieces, the fewer last waves and sums of
+// dX, and a dz of the whole vocabulary that fits is one piece (backward of 8192 x 100000 x 512 1.80 ms; 2.27 with 64 MB, 1.92
 // with 256, 1.70 with 1 GB; of 4096 x 65536 x 4096 3.74, 3.91, 3.74 and 3.75).
 constexpr size_t kPieceBytes = size_t(512) << 20;
 constexpr int kMinTileN = 128;
