@@ -37,6 +37,11 @@ using tcg::xent::Params;
 constexpr size_t kPieceBytes = size_t(512) << 20;
 constexpr int kMinTileN = 128;
 constexpr int kPartK = 1024;           // k of the logits' products that the tensor cores sum in one go, about
+// Row tiles that are walked before the next column tile (by themselves: 4096 x 65536 x
+// 4096 forward 1036 us and backward 3270; 1123 and 3561 with 4, 1059 and 3295 with 8,
+// 1037 and 3260 with 32; 8192 x 100000 x 512 534 and 1915, 530 and 1883 with 8, 537 and
+// 1911 with 32; no difference at 1000 and fewer tokens).
+constexpr int kRasterM = 16;
 constexpr int kFinishRows = 32, kFinishSlices = 32, kFinishThreads = kFinishRows * kFinishSlices;
 constexpr int kFinishBatch = 8;
 constexpr float kHalfTop = 16384.0f;   // fp16: what the largest |r_t| becomes
@@ -342,7 +347,7 @@ tcg_status launch_tiles(Params& p, tcg_dtype dtype, const void* X, int ldx, cons
     p.num_kb = static_cast<int>(blocks(2LL * hidden, tcg::xent::kRowBytes * atoms));
     p.parts = std::min(pl.parts, p.num_kb);
     p.tile_n = pl.tile_n;
-    p.raster_m = 16;
+    p.raster_m = kRasterM;
     p.fmt = dtype == TCG_F16 ? 0u : 1u;
     p.timeout_ns = tcg::host::wait_timeout_ns();
     p.fault_inject = tcg::host::fault_inject();

@@ -17,9 +17,11 @@
 // gradients and the chosen logits are worked on k lanes a row, for as many rows
 // as fit a warp.  Statistics are fp32.
 //
-// Bound by the instructions issued (a row of 256 bf16 logits, eight chosen: about
-// 310, most of them integer compares and selects, which issue every other cycle),
-// next by memory, whose part is 2.5 us each way.  32768 x 256, one call after the
+// Most of the time goes to instructions (a row of 256 bf16 logits, eight chosen:
+// about 310, most of them integer compares and selects, which issue every other
+// cycle: 59 % of the issue slots, 62 % of the ALU pipe), the rest to waiting for
+// the row, of which a warp has one under way (all keys are made and sorted before
+// the next is asked for); memory's part is 2.5 us each way.  32768 x 256, one call after the
 // other in a graph: forward 13.1 us, backward 7.4 (over all experts 16.1 and
 // 12.1; fp32 logits 19.8 and 11.6).  Steps that helped, both ways and calls
 // included: one reduction a round on keys that hold the expert's number, in place

@@ -20,7 +20,7 @@
 // however many experts it has, and each expert's row once.  Bound by memory:
 // 16384 tokens x 2 rows of 4096 bf16 values, dispatch and its gradient 124 us
 // (800 MB, 6.4 TB/s, 0.95 of the copy rate), combine and both gradients 166 us
-// (1070 MB in the two calls, 6.5 TB/s).  Rows that start anywhere take half to
+// (1070 MB in the two calls, 6.4 TB/s, 0.96).  Rows that start anywhere take half to
 // four fifths longer (4095 columns: dispatch 91, combine 120 us, its gradient
 // 152; whole words 61, 67 and 102): each is read in words that are shifted into place.
 #include <algorithm>

@@ -18,15 +18,18 @@
 //
 // Roles, registers, accumulators and bounded waits as in xent_kernel.cuh: pairs
 // of CTAs on tiles of 256 rows, 256 or 128 columns.  Sums longer than 8192 k are
-// added up in registers in pieces of that length.
+// added up in registers in pieces of that length.  (Of 1024 k, as the logits' are,
+// dX of 64 x 32768 x 4096 is 7e-6 of itself less near zero, where dz's rounding is
+// 6.7e-4 in the 2-norm, and backward takes 1 % longer at 4096 x 65536 x 4096 and
+// 2 % at 8192 x 100000 x 512.)
 //
 // Bound by the tensor cores where the sums are long (1000 x 50021 x 1280: both
-// products 150 us, tensor pipe 72 %; as two calls of tcg_gemm 245), by the way of
+// products 151 us, tensor pipe 79 %; as two calls of tcg_gemm 245), by the way of
 // dW's tiles to memory where there are few tokens (64 x 32768 x 4096: a tile of 64
 // KB a CTA in 2.1 us, of which the stores 1.5: 32 rows of 32 bytes at a time).
 // What helped there: an accumulator's hand-back without a release at cluster scope
 // (265 -> 195 us for all of the backward pass), one output type's code at a time
-// (fewer instructions fetched), stores straight from registers (186).
+// (fewer instructions fetched), stores straight from registers (186; 177 as it stands).
 #pragma once
 
 #include "xent_kernel.cuh"
