@@ -596,9 +596,10 @@ tcg_status tcg_moe_balance_backward(int tokens, int experts, int k, tcg_dtype dt
  * the assignments are put in expert order (tcg_moe_sort), the tokens' rows go to
  * the experts' (tcg_moe_dispatch; tcg_quantize_rows128 with row_token where the
  * products run in 8 bits), the grouped products take the offsets, and the
- * results go back with their weights (tcg_moe_combine).  Types: TCG_BF16,
- * TCG_F16 or TCG_F32; any alignments of the element and leading dimensions,
- * whole words where rows start on 16 bytes.
+ * results go back with their weights (tcg_moe_combine).  Up to 2^31 - 4096 tokens
+ * and rows (else TCG_ERR_UNSUPPORTED).  Types: TCG_BF16, TCG_F16 or TCG_F32; any
+ * alignments of the element and leading dimensions, whole words where rows start
+ * on 16 bytes.
  * ---------------------------------------------------------------------------
  */
 
@@ -700,6 +701,8 @@ tcg_status tcg_moe_combine_backward(int tokens, int k, int cols, int rows, const
  *   X: tokens x hidden, W: vocab x hidden, row-major, both dtype (TCG_BF16 or
  *     TCG_F16), 16-byte aligned with leading dimensions that are multiples of 8
  *     (else TCG_ERR_UNSUPPORTED).  vocab, hidden >= 1.
+ *   tokens and vocab up to 2^30 - 2048, hidden up to 2^29 - 1024, at most 2^30 -
+ *     2048 blocks of 128 x 128 logits (else TCG_ERR_UNSUPPORTED).
  *   target: the word of each token; one outside [0, vocab) does not count.
  *   workspace: tcg_linear_xent_workspace_size bytes (backward != 0: of the
  *     gradient, which suffices for the loss as well), zero-filled once and
