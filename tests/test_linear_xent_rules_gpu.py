@@ -6,12 +6,13 @@ in parts of at most 1536 k, cut after every 16 (at most 2^-22 of the part's
 magnitudes a step), and the parts are added with a rounding each: a logit is off by
 no more than ((1536 + 128) / 16 2^-22 + (H / 1024 + 2) u) S.
 """
+import copy
+
 import pytest
 import torch
 
 import tiled_tensor_core_persistent_gb300 as tcg
 
-from block128 import TYPE
 from test_linear_xent_gpu import U, Case, half_step
 
 pytestmark = pytest.mark.gpu
@@ -184,3 +185,38 @@ def test_a_wait_of_the_gradient_that_runs_out_is_reported_and_the_next_call_is_e
     c.forward()
     c.check_forward()
     c.check_backward(*got, gm, None)
+
+
+@pytest.mark.parametrize("dx_type", ["bf16", "f32"])
+def test_nine_pieces_of_a_vocabulary(dx_type):
+    """262144 tokens leave a piece 1024 words; looked at in 64 bits, 16384 tokens at a time."""
+    T, V, H, step = 262144, 9000, 64, 16384
+    if torch.cuda.get_device_properties(0).total_memory < 100 << 30:
+        pytest.skip("needs 20 GB")
+    c = Case(T, V, H, ignored=0.1)
+    assert c.bytes < (512 << 20) + T * H * 4 + (300 << 20)      # not of the whole vocabulary (4.7 GB)
+    c.forward()
+    n = int(c.live.sum())
+    assert int(c.valid) == n
+    gm = torch.full((1,), 3.0 * n, device="cuda")
+    gx, gw = c.backward(dx_type, "f32", gm)
+    each = torch.full((T,), float(gm / c.valid.float()), device="cuda")     # every token's weight
+    want, bound = (torch.zeros(V, H, dtype=torch.double, device="cuda") for _ in range(2))
+    for a in range(0, T, step):
+        s = copy.copy(c)
+        s.T = step
+        s.x, s.target, s.live, s.lse = c.x[a:a + step], c.target[a:a + step], c.live[a:a + step], c.lse[a:a + step]
+        s.check_backward(gx[a:a + step], None, None, each[a:a + step])
+        z, lse, _, _, S = s.exact()
+        err = s.lse_error(z, lse, S)
+        assert bool(((s.lse.double() - lse).abs() <= err).all())
+        p = torch.exp(z - lse[:, None])
+        hit = torch.zeros_like(p)
+        hit[torch.arange(step, device="cuda"), s.target.long().clamp(0, V - 1)] = s.live.double()
+        r = torch.where(s.live, each[a:a + step].double(), 0.0)[:, None]
+        dz = r * (p - hit)
+        off = half_step("bf16") * dz.abs() * 1.01 + r * (p * (float(err.max()) + s.z_error(S) + 8 * U + 2.0 ** -22) * 1.01 + 4 * U * (p + hit))
+        x = s.x[:, :H].double()
+        want += dz.t() @ x
+        bound += off.t() @ x.abs() + (8192 / 16 + T / 8192 + 40) * 2.0 ** -22 * ((dz.abs() + off).t() @ x.abs())
+    assert bool(((gw.double() - want).abs() <= bound + 4 * U * want.abs()).all())
