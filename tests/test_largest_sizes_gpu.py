@@ -136,5 +136,5 @@ def test_the_most_words():
         assert bool(((got - one).abs() <= (2 * 2.0 ** -8 * 1.01 + 2 * off) * one.abs() + 1e-38).all())
         want += dz @ rows
         size += dz.abs() @ rows.abs()
-    # sums of 8192 words in one go and those in fp32, a round of pieces
+    # sums of 8192 words in one go, and those added in fp32
     assert bool(((dx[0].double() - want).abs() <= (2.0 ** -8 * 1.01 + 2 * off + (8192 / 16 + 40) * 2.0 ** -22) * size).all())
